@@ -257,6 +257,106 @@ int moe_prefill_group(const moe_layer *L, const float *x, int t, uint32_t *topk_
                       int32_t *group_offs, int32_t *group_rows, float *group_w, void *work,
                       size_t work_bytes, int *dev_status, moe_stream_t stream);
 
+/* ---- 8-bit experts: routing from given logits, e4m3 values with a
+ * power-of-two scale per block of 128, and the products over them.
+ *
+ * Value format: e4m3 bytes (1-4-3, bias 7, no infinity, 0x7f / 0xff NaN,
+ * largest 448).  Scale format: E8M0 bytes, e stands for 2^(e - 127), 255 is
+ * NaN.  Activations carry one scale per 128 consecutive k of a row, weights
+ * one per 128 x 128 block (the last block of a row or a matrix may be
+ * smaller).  A power of two keeps the scaling exact, so a value is rounded
+ * once, and is what the tensor cores apply by themselves. */
+enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 };
+
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GATE_RENORM = 1 /* weights divided by their sum over the chosen experts */ };
+
+/* How moe_gate turns a row's logits l into expert ids and weights.
+ *   p_e   = softmax of l over all experts, or 1 / (1 + exp(-l_e))
+ *   sel_e = p_e + bias_e, the selection score (without a bias experts are
+ *           compared by their logits, which p orders the same, and so are
+ *           groups when group_top is 1)
+ * Experts form n_groups runs of n_experts / n_groups ids.  A group's score is
+ * the sum of its group_top (1 or 2) highest sel; the top_groups best groups
+ * stay, and of their experts the top_k highest sel are chosen, in descending
+ * order.  Ties go to the lowest id everywhere.  Weights are the p of the
+ * chosen experts (never the bias), with MOE_GATE_RENORM divided by their sum,
+ * times `scale`.  An expert whose logit or bias is -inf or NaN is masked: it
+ * is never chosen and counts in no sum; slots left without an expert get the
+ * id 0xffffffff and weight 0 (a fully masked row: all of them).  Comparisons
+ * hold as in 64-bit arithmetic: rows whose order 32 bits cannot tell are
+ * decided again in 64. */
+typedef struct {
+  uint32_t n_experts, top_k; /* n_experts <= 1024, top_k <= min(32, experts of top_groups groups) */
+  uint32_t score;            /* MOE_SCORE_* */
+  uint32_t n_groups, top_groups, group_top; /* n_groups 1..32, a divisor of n_experts; 1, 1, 1: no groups */
+  uint32_t flags;            /* MOE_GATE_* */
+  float scale;               /* finite */
+} moe_gate_cfg;
+
+/* Route t rows from their logits (a router that moe_route does not compute).
+ *   logits   [t] rows of n_experts values of logit_dtype, ld elements apart
+ *   bias     [n_experts] float32, or NULL
+ *   topk_idx [t][top_k] uint32, topk_w [t][top_k] float32
+ * t may be 0.  Needs no workspace; has no device-side failures. */
+int moe_gate(const moe_gate_cfg *cfg, const void *logits, int logit_dtype, int64_t ld, const float *bias, int t,
+             uint32_t *topk_idx, float *topk_w, moe_stream_t stream);
+
+/* Quantise x [rows] x cols (x_dtype, rows ldx elements apart) to e4m3 q
+ * (rows ldq bytes apart) with scales s.  block_rows 1: a scale per row and
+ * 128 columns (activations), s [rows] rows of ceil(cols / 128) bytes, lds
+ * apart; block_rows 128: a scale per 128 x 128 block (weights), s
+ * [ceil(rows / 128)] rows, lds apart.  A block's exponent is the least with
+ * max |x| <= 448 * 2^e over its finite values (0 for a block of zeros, never
+ * below -127); values are rounded to nearest, ties to even.  Infinities and
+ * NaN become NaN (0x7f) and do not move the scale. */
+int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int block_rows, uint8_t *q, int64_t ldq,
+               uint8_t *s, int64_t lds, moe_stream_t stream);
+
+/* out[r][j] = sum over k of a[r][k] b[j][k], scaled: the block-scaled 8-bit
+ * matrix product, accumulated in fp32 and rounded once to out_dtype.
+ *   a    e4m3 [t] rows of k, lda bytes apart; 16-byte aligned, lda % 16 == 0
+ *   sa   E8M0 [t] rows of ceil(k / 128), lds bytes apart; 4-byte aligned, lds % 4 == 0
+ *   b    e4m3 [max(n_groups, 1)][n][k], 16-byte aligned; sb E8M0 [..][ceil(n / 128)][ceil(k / 128)]
+ *   out  [t] rows of n, ldo elements apart; must not overlap the inputs
+ *   offs NULL (one weight matrix for every row, n_groups 0), or device int32
+ *        [n_groups + 1], ascending, 0 <= offs[g] <= t: rows offs[g] ..
+ *        offs[g+1] - 1 are multiplied with b[g]; rows outside
+ *        [offs[0], offs[n_groups]) are left as they are.  Offsets that do
+ *        not ascend or leave 0..t are reported (MOE_EDEVICE) and nothing is
+ *        written.
+ *   flags 0 (MOE_TEST_WITHHOLD: failure-detection test, grouped form only)
+ * k % 16 == 0; n_groups <= 1024; t may be 0. */
+int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t, const uint8_t *b, const uint8_t *sb,
+            int n, int k, void *out, int out_dtype, int64_t ldo, const int32_t *offs, int n_groups, uint32_t flags,
+            int *dev_status, moe_stream_t stream);
+
+/* Routed experts held in 8 bits: gate_up e4m3 [n_experts][2 * inter][hidden]
+ * (rows 0..inter-1 the gate), down e4m3 [n_experts][hidden][inter], with
+ * their block scales.  16-byte aligned. */
+typedef struct {
+  uint32_t hidden, n_experts, inter; /* hidden, inter: multiples of 128 up to 16384; n_experts <= 1024 */
+  const uint8_t *gate_up, *gate_up_s;
+  const uint8_t *down, *down_s;
+} moe_layer8;
+
+/* The routed experts' step over t rows from given ids and weights (moe_gate's,
+ * moe_route's or a caller's):
+ *   x8 = quant8(x);  (g, u) = mm8 with gate_up;  h8 = quant8(silu(g) * u);
+ *   out[r] = sum over j of topk_w[r][j] * (mm8 of h8 with down of expert topk_idx[r][j])
+ * in fp32 between the roundings to 8 bits; for more than a few rows the
+ * weighted expert outputs are held in out's type before they are summed (in
+ * the order of j).  Ids >= n_experts (0xffffffff, or another rank's experts
+ * after the caller subtracted its first id) contribute nothing; a row without
+ * experts gives zeros; an expert twice in a row counts twice.
+ *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype, must not overlap x
+ *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned
+ * top_k 1..32; t 0..1048576 with t * top_k < 2^31 / 2. */
+int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const uint32_t *topk_idx,
+                 const float *topk_w, int top_k, void *out, int out_dtype, void *work, size_t work_bytes,
+                 int *dev_status, moe_stream_t stream);
+size_t moe_experts8_workspace(const moe_layer8 *L, int t, int top_k);
+
 /* Workspace bytes moe_forward needs for these layers and nb rows (0 if the
  * arguments are invalid). */
 size_t moe_forward_workspace(const moe_layer *layers, int n_layers, int nb);

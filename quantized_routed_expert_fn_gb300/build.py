@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
-SOURCES = ["decode.cu", "prefill.cu", "api.cu", "tier.cu"]
+SOURCES = ["decode.cu", "prefill.cu", "mm8.cu", "experts8.cu", "gate.cu", "quant8.cu", "api.cu", "api8.cu", "tier.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

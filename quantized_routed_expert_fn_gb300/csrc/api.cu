@@ -14,6 +14,7 @@
 #include <mutex>
 #include <string>
 
+#include "api.cuh"
 #include "decode.cuh"
 #include "moe_api.h"
 #include "prefill.cuh"
@@ -21,8 +22,10 @@
 static_assert(MOE_PREFILL_KERNELS == moe::kPfStages, "prefill kernel count");
 
 namespace {
-
 thread_local std::string g_err;
+}
+
+namespace moe {
 
 int fail(int code, const char *fmt, ...) {
   char buf[512];
@@ -33,6 +36,26 @@ int fail(int code, const char *fmt, ...) {
   g_err = buf;
   return code;
 }
+
+unsigned long long timeout_ns() {
+  const char *s = getenv("MOE_TIMEOUT_MS");
+  double ms = s ? atof(s) : 1000.0;
+  if (!(ms > 0)) ms = 1000.0;
+  return (unsigned long long)(ms * 1e6);
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const char *pa = (const char *)a, *pb = (const char *)b;
+  return pa < pb + nb && pb < pa + na;
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::fail;
+using moe::overlap;
+using moe::timeout_ns;
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -130,18 +153,6 @@ int check_layers(const moe_layer *layers, int nl, int nb) {
     }
   }
   return MOE_OK;
-}
-
-unsigned long long timeout_ns() {
-  const char *s = getenv("MOE_TIMEOUT_MS");
-  double ms = s ? atof(s) : 1000.0;
-  if (!(ms > 0)) ms = 1000.0;
-  return (unsigned long long)(ms * 1e6);
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const char *pa = (const char *)a, *pb = (const char *)b;
-  return pa < pb + nb && pb < pa + na;
 }
 
 int run(const moe_layer *layers, int nl, const float *x, int nb, float *out, void *work, size_t work_bytes,

@@ -1,0 +1,143 @@
+// fp8.cuh -- parameters and helpers of the 8-bit expert kernels: routing from
+// given logits, quantisation to e4m3 with E8M0 block scales, the
+// block-scaled products and the routed experts' step.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace moe {
+
+// ---- routing (gate.cu)
+struct GateP {
+  const void *logits;
+  int bf16;
+  int64_t ld;
+  const float *bias;  // [E] or nullptr
+  int t, E, K;
+  int sigmoid, renorm;
+  int ng, gs, top_groups, group_top;  // ng 1: no groups; gs = E / ng
+  float scale;
+  uint32_t *idx;
+  float *w;
+};
+cudaError_t launch_gate(const GateP &p, cudaStream_t st);
+
+// ---- quantisation (quant8.cu)
+struct Quant8P {
+  const void *x;
+  int bf16;
+  int64_t ldx;
+  int rows, cols;
+  uint8_t *q;
+  int64_t ldq;
+  uint8_t *s;
+  int64_t lds;
+};
+cudaError_t launch_quant8_rows(const Quant8P &p, int n_sms, cudaStream_t st);
+cudaError_t launch_quant8_blocks(const Quant8P &p, cudaStream_t st);
+
+// ---- products (mm8.cu)
+struct Mm8P {
+  // tokens: boxes of 128 bytes x 128 / 32 rows; weights [G * n][k]: 128 bytes x 128 rows; 128B swizzle
+  CUtensorMap tm_a128, tm_a32, tm_b;
+  const uint8_t *a, *sa, *b, *sb;
+  int64_t lda, lds;
+  int t, n, k, nk, nb;  // nk = ceil(k / 128), nb = ceil(n / 128)
+  int G;                // 0: one weight matrix for every row
+  const int *offs;      // [G + 1] or nullptr
+  void *out;            // [t][n], or h8 [t][n / 2] (silu)
+  int64_t ldo;
+  uint8_t *hs;          // silu: scales of h8
+  int64_t ldhs;
+  int withhold;
+  int *status;
+  unsigned long long timeout_ns;
+};
+enum { kOutF32 = 0, kOutBf16 = 1, kOutSilu8 = 2 };
+// rows the few-row kernel takes (weights streamed once, mma.sync)
+constexpr int kMm8SmallRows = 32;
+int mm8_tensor_maps(Mm8P &p, const char **why);
+cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st);
+cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// e8m0 byte -> the power of two it stands for
+__device__ __forceinline__ float e8m0_f(uint32_t e) {
+  return __uint_as_float(e == 0 ? 0x00400000u : (e == 255u ? 0x7fc00000u : e << 23));
+}
+
+// Scale byte of a block whose largest finite magnitude has the bits `a`:
+// the least e with |x| <= 448 * 2^(e - 127) = 1.75 * 2^(e - 119); 127 for a
+// block of zeros, 0 at least.
+__device__ __forceinline__ uint32_t e8m0_of_amax(uint32_t a) {
+  if (a == 0) return 127u;
+  int ex = (int)(a >> 23);           // a = m * 2^(ex - 127)
+  const uint32_t m = a & 0x7fffffu;
+  if (ex == 0) return 0u;            // below 2^-126: e would be below 0
+  ex = ex - 8 + (m > 0x600000u);     // m > 1.75
+  return ex > 0 ? (uint32_t)ex : 0u;
+}
+// 2^(127 - e): what a value is multiplied with before it is rounded
+__device__ __forceinline__ float e8m0_inv(uint32_t e) {
+  return e >= 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - e) << 23);
+}
+
+// magnitude bits that count for the block's scale: finite values only
+__device__ __forceinline__ uint32_t mag_bits(float v) {
+  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+
+// two values, scaled, to two e4m3 bytes (nearest, ties to even; infinities
+// and NaN to NaN: an infinity times 0 is the NaN the conversion keeps)
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  const float l = lo + 0.f * lo, h = hi + 0.f * hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(h), "f"(l));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | e4m3x2(c, d) << 16;
+}
+
+#endif
+
+}  // namespace moe
+
+namespace moe {
+
+// ---- the routed experts' step (experts8.cu)
+struct Ex8P {
+  int H, E, I, t, K;
+  const uint8_t *gu, *gus, *dn, *dns;
+  const void *x;
+  int x_bf16, out_bf16;
+  const uint32_t *idx;  // [t][K]
+  const float *w;       // [t][K]
+  void *out;            // [t][H]
+  int *status;
+  // workspace
+  uint8_t *h8, *h8s;    // [t * K][I] e4m3 and [t * K][ldi] scales
+  int ldi, ldh;         // scale bytes of a row of h8 / x8
+  uint8_t *x8, *x8s;    // many rows: [t * K][H] grouped rows, [t * K][ldh]
+  int *counts;          // [E] entries per expert, then one ticket
+  int *offs;            // [E + 1]
+  int *place;           // [t * K] place of an entry within its expert, -1: none
+  void *y;              // [t * K][H] weighted outputs in out's type
+};
+struct Ex8Sizes {
+  size_t h8, h8s, x8, x8s, counts, offs, place, y, total;
+};
+constexpr int kEx8SmallRows = 8;  // rows of the few-row path: one column each of an m16n8 tile
+bool ex8_small(int H, int I, int t, int K);
+Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size);
+cudaError_t launch_ex8_small(const Ex8P &p, cudaStream_t st);
+cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st);
+cudaError_t launch_ex8_combine(const Ex8P &p, cudaStream_t st);
+
+}  // namespace moe

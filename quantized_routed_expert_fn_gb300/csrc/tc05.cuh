@@ -46,6 +46,38 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
          | ((uint32_t)(128 >> 4) << 24);
 }
 
+// Instruction descriptor, kind::mxf8f6f4 with block scaling: D fp32, A and B
+// e4m3 (format 0), both K-major, E8M0 scales (bit 23), scale byte 0 of each
+// scale word, M = 128, N = n (multiple of 16, 16..256).
+__host__ __device__ __forceinline__ uint32_t idesc_mx_e4m3(int n) {
+  return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Shared-memory descriptor of 32 rows x 16 bytes, rows 16 bytes apart (no
+// swizzle; 8-row groups 128 bytes apart): the source of a scale copy.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t smem_addr) {
+  return (uint64_t)((smem_addr >> 4) & 0x3fffu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// One thread: 32 rows x 16 bytes of shared memory into four TMEM columns,
+// the same in each of the four 32-lane quadrants.  MMAs issued after it by
+// the same thread read what it wrote.
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// One thread: D[tmem] (+)= (A * scale A) (B * scale B)^T over k = 32 e4m3
+// values.  The scale word of row r (of A, or of B = column r of D) is in
+// column r / 32 of its scale columns, lane r % 32.
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
 // One warp: allocate ncols TMEM columns (power of two >= 32); the address is
 // written to *dst (shared memory).
 __device__ __forceinline__ void alloc(uint32_t *dst, uint32_t ncols) {
@@ -130,6 +162,19 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+
+// Warp: 16 consecutive fp32 columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
 
 // ---- TMA (tensor maps live in kernel parameter space, passed by address)

@@ -7,6 +7,7 @@ is no fallback: if the library is missing the import of `lib()` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -20,13 +21,17 @@ PRENORM = 2
 LOOKAHEAD = 4
 TEST_WITHHOLD = 0x100
 
+F32, BF16 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
+GATE_RENORM = 1
+
 OK, EINVAL, ESHAPE, EALIGN, ECUDA, ETIMEOUT, EDEVICE, ENOSPACE = 0, -1, -2, -3, -4, -5, -6, -7
 STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EALIGN", -4: "MOE_ECUDA",
                 -5: "MOE_ETIMEOUT", -6: "MOE_EDEVICE", -7: "MOE_ENOSPACE"}
 
 EXPORTS = ["moe_route", "moe_forward", "moe_forward_traced", "moe_forward_noalloc", "moe_forward_workspace",
            "moe_prefill", "moe_prefill_timed", "moe_prefill_workspace", "moe_prefill_group", "moe_last_error",
-           "moe_tier_create", "moe_tier_update", "moe_tier_slot", "moe_tier_get_stats", "moe_tier_addresses",
+           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_tier_create", "moe_tier_update", "moe_tier_slot", "moe_tier_get_stats", "moe_tier_addresses",
            "moe_tier_destroy", "moe_tier_last_error"]
 PREFILL_KERNELS = 10
 PREFILL_KERNEL_NAMES = ["prep", "router_gemm", "topk", "group_count", "group_scan", "group_fill", "gather",
@@ -56,6 +61,18 @@ class MoeLayer(ctypes.Structure):
 class TierStats(ctypes.Structure):
     _fields_ = [("resident", ctypes.c_int), ("last_host_reads", ctypes.c_int), ("last_promoted", ctypes.c_int),
                 ("promotions", ctypes.c_longlong), ("evictions", ctypes.c_longlong)]
+
+
+class MoeGateCfg(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_uint32), ("top_k", ctypes.c_uint32), ("score", ctypes.c_uint32),
+                ("n_groups", ctypes.c_uint32), ("top_groups", ctypes.c_uint32), ("group_top", ctypes.c_uint32),
+                ("flags", ctypes.c_uint32), ("scale", ctypes.c_float)]
+
+
+class MoeLayer8(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_uint32), ("n_experts", ctypes.c_uint32), ("inter", ctypes.c_uint32),
+                ("gate_up", ctypes.c_void_p), ("gate_up_s", ctypes.c_void_p), ("down", ctypes.c_void_p),
+                ("down_s", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -95,6 +112,17 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.moe_prefill_timed.argtypes = [ctypes.POINTER(MoeLayer), vp, i32, vp, vp, sz, vp, vp, vp, vp]
         L.moe_prefill_group.restype = i32
         L.moe_prefill_group.argtypes = [ctypes.POINTER(MoeLayer), vp, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+        i64, u32 = ctypes.c_int64, ctypes.c_uint32
+        L.moe_gate.restype = i32
+        L.moe_gate.argtypes = [ctypes.POINTER(MoeGateCfg), vp, i32, i64, vp, i32, vp, vp, vp]
+        L.moe_quant8.restype = i32
+        L.moe_quant8.argtypes = [vp, i32, i64, i32, i32, i32, vp, i64, vp, i64, vp]
+        L.moe_mm8.restype = i32
+        L.moe_mm8.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, i32, vp, i32, i64, vp, i32, u32, vp, vp]
+        L.moe_experts8_workspace.restype = sz
+        L.moe_experts8_workspace.argtypes = [ctypes.POINTER(MoeLayer8), i32, i32]
+        L.moe_experts8.restype = i32
+        L.moe_experts8.argtypes = [ctypes.POINTER(MoeLayer8), vp, i32, i32, vp, vp, i32, vp, i32, vp, sz, vp, vp]
         L.moe_tier_create.restype = i32
         L.moe_tier_create.argtypes = [i32, i32, sz, vp, vp, i32, vp, vp, vp, ctypes.POINTER(vp)]
         L.moe_tier_update.restype = i32
@@ -278,6 +306,158 @@ def prefill_timed(layers: DeviceLayers, x: torch.Tensor, out: torch.Tensor, work
     wp, wb = _aligned(work)
     _check(lib().moe_prefill_timed(_layer_ptr(layers, layer), _p(x), x.shape[0], _p(out), wp, wb, _p(topk_idx),
                                    _p(status), arr, _stream(stream)))
+
+
+# ---- 8-bit experts: routing from given logits, quantisation, products
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_E8M0 = (torch.uint8, getattr(torch, "float8_e8m0fnu", torch.uint8))
+_I32 = (torch.int32, getattr(torch, "uint32", torch.int32))
+_F32 = (torch.float32,)
+
+
+def _bad(code: int, msg: str):
+    raise MoeError(code, msg)
+
+
+def _arg(t, name: str, shape: tuple, dtypes, dev=None) -> int:
+    """Address of a CUDA tensor after checking type, shape, device and that its
+    last dimension is contiguous (the strides of the others are the caller's)."""
+    if t.dtype not in dtypes:
+        _bad(EINVAL, f"{name} is {t.dtype}")
+    if t.shape != shape:
+        _bad(ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != dev:
+        _bad(EINVAL, f"{name} is on {t.device}, expected {dev}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+        _bad(EINVAL, f"{name}'s last dimension is not contiguous")
+    return t.data_ptr()
+
+
+def _whole(t, name: str, shape: tuple, dtypes, dev) -> int:
+    p = _arg(t, name, shape, dtypes, dev)
+    if not t.is_contiguous():
+        _bad(EINVAL, f"{name} is not contiguous")
+    return p
+
+
+def _device(t, name: str) -> torch.device:
+    """The call's device: the current one, where the stream and every tensor have to be."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        _bad(EINVAL, f"{name} is on {t.device}, not on the current CUDA device")
+    return t.device
+
+
+def _ld(t) -> int:
+    """Row stride; of a single row, whose stride means nothing, its length."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+@functools.lru_cache(maxsize=64)
+def _gate_cfg(n_experts, top_k, score, n_groups, top_groups, group_top, flags, scale) -> MoeGateCfg:
+    if score not in SCORES:
+        _bad(EINVAL, f"unknown score {score!r}")
+    return MoeGateCfg(n_experts, top_k, SCORES[score], n_groups, top_groups, group_top, flags, scale)
+
+
+def gate(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, bias=None, score: str = "softmax",
+         n_groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = False, scale: float = 1.0,
+         stream=None) -> None:
+    """moe_gate: logits float32 / bfloat16 [t][E] (any row stride) -> topk_idx int32 [t][k]
+    (-1: no expert left), topk_w float32 [t][k]; bias float32 [E] steers the choice only."""
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        _bad(ESHAPE, "logits and topk_idx are matrices")
+    t, e = logits.shape
+    k = topk_idx.shape[1]
+    dev = _device(logits, "logits")
+    lp = _arg(logits, "logits", (t, e), _FLOATS, dev)
+    ip = _whole(topk_idx, "topk_idx", (t, k), _I32, dev)
+    wp = _whole(topk_w, "topk_w", (t, k), _F32, dev)
+    bp = None if bias is None else _whole(bias, "bias", (e,), _F32, dev)
+    cfg = _gate_cfg(e, k, score, n_groups, top_groups, group_top, GATE_RENORM if renorm else 0, scale)
+    _check(lib().moe_gate(cfg, lp, _FLOATS[logits.dtype], _ld(logits), bp, t, ip, wp, _stream(stream)))
+
+
+def quant8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 1, stream=None) -> None:
+    """moe_quant8: x float32 / bfloat16 [rows][cols] -> q e4m3 [rows][cols] (float8_e4m3fn or uint8) and
+    s E8M0 [ceil(rows / block_rows)][ceil(cols / 128)] (float8_e8m0fnu or uint8); row strides as they are."""
+    if x.dim() != 2 or block_rows not in (1, 128):
+        _bad(ESHAPE, "x is a matrix; block_rows is 1 or 128")
+    rows, cols = x.shape
+    dev = _device(x, "x")
+    xp = _arg(x, "x", (rows, cols), _FLOATS, dev)
+    qp = _arg(q, "q", (rows, cols), _E4M3, dev)
+    sp = _arg(s, "s", (-(-rows // block_rows), -(-cols // 128)), _E8M0, dev)
+    _check(lib().moe_quant8(xp, _FLOATS[x.dtype], _ld(x), rows, cols, block_rows, qp, _ld(q), sp, _ld(s),
+                            _stream(stream)))
+
+
+def mm8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, out: torch.Tensor, status: torch.Tensor,
+        offs=None, flags: int = 0, stream=None) -> None:
+    """moe_mm8: a e4m3 [t][k] with sa E8M0 [t][ceil(k / 128)] (its rows a multiple of 4 bytes apart, the last
+    one held whole) times b e4m3 [n][k] with sb [ceil(n / 128)][ceil(k / 128)] -> out float32 / bfloat16 [t][n].
+    With offs int32 [G + 1]: b [G][n][k], sb [G][..][..], group g has the rows offs[g] .. offs[g + 1] - 1."""
+    groups = 0 if offs is None else offs.shape[0] - 1
+    if a.dim() != 2 or b.dim() != (3 if groups else 2):
+        _bad(ESHAPE, "a is [t][k]; b is [n][k], with offs [G][n][k]")
+    t, k = a.shape
+    n = b.shape[-2]
+    dev = _device(a, "a")
+    lead = (groups,) if groups else ()
+    ap = _arg(a, "a", (t, k), _E4M3, dev)
+    sap = _arg(sa, "sa", (t, -(-k // 128)), _E8M0, dev)
+    bp = _whole(b, "b", lead + (n, k), _E4M3, dev)
+    sbp = _whole(sb, "sb", lead + (-(-n // 128), -(-k // 128)), _E8M0, dev)
+    op = _arg(out, "out", (t, n), _FLOATS, dev)
+    fp = None if offs is None else _whole(offs, "offs", (groups + 1,), _I32, dev)
+    lds = sa.stride(0)
+    if t == 1 and lds % 4:  # one row: only what it holds can be read
+        lds = -(-lds // 4) * 4
+    if t and sa.untyped_storage().nbytes() < sa.storage_offset() + t * lds:
+        _bad(EINVAL, "sa's last row is not held whole")
+    _check(lib().moe_mm8(ap, _ld(a), sap, lds, t, bp, sbp, n, k, op, _FLOATS[out.dtype], _ld(out), fp, groups, flags,
+                         _whole(status, "status", (1,), _I32, dev), _stream(stream)))
+
+
+class Layer8:
+    """Routed experts in 8 bits: gate_up e4m3 [E][2 * inter][hidden] (the gate rows first), down e4m3
+    [E][hidden][inter], with E8M0 scales per 128 x 128 block (quant8 with block_rows=128, expert by expert)."""
+
+    def __init__(self, gate_up: torch.Tensor, gate_up_s: torch.Tensor, down: torch.Tensor, down_s: torch.Tensor):
+        if gate_up.dim() != 3 or gate_up.shape[1] % 2:
+            _bad(ESHAPE, "gate_up is [E][2 * inter][hidden]")
+        e, i2, h = gate_up.shape
+        i = i2 // 2
+        if h % 128 or i % 128:
+            _bad(ESHAPE, f"hidden {h} and inter {i} must be multiples of 128")
+        dev = _device(gate_up, "gate_up")
+        self.hidden, self.n_experts, self.inter, self.device = h, e, i, dev
+        self.keep = (gate_up, gate_up_s, down, down_s)
+        self.c = MoeLayer8(h, e, i, _whole(gate_up, "gate_up", (e, i2, h), _E4M3, dev),
+                           _whole(gate_up_s, "gate_up_s", (e, i2 // 128, h // 128), _E8M0, dev),
+                           _whole(down, "down", (e, h, i), _E4M3, dev),
+                           _whole(down_s, "down_s", (e, h // 128, i // 128), _E8M0, dev))
+
+
+def experts8_workspace(layer: Layer8, t: int, top_k: int) -> int:
+    return int(lib().moe_experts8_workspace(layer.c, t, top_k))
+
+
+def experts8(layer: Layer8, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, out: torch.Tensor,
+             work: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """moe_experts8: x float32 / bfloat16 [t][hidden] through the experts topk_idx int32 [t][k] (ids outside
+    0 .. E - 1 contribute nothing) with weights topk_w -> out float32 / bfloat16 [t][hidden]."""
+    t, k = topk_idx.shape
+    dev = _device(x, "x")
+    shape = (t, layer.hidden)
+    wp, wb = _aligned(work)
+    if layer.device != dev or work.device != dev:
+        _bad(EINVAL, f"layer on {layer.device}, work on {work.device}, x on {dev}")
+    _check(lib().moe_experts8(layer.c, _whole(x, "x", shape, _FLOATS, dev), _FLOATS[x.dtype], t,
+                              _whole(topk_idx, "topk_idx", (t, k), _I32, dev), _whole(topk_w, "topk_w", (t, k), _F32, dev), k,
+                              _whole(out, "out", shape, _FLOATS, dev), _FLOATS[out.dtype], wp, wb,
+                              _whole(status, "status", (1,), _I32, dev), _stream(stream)))
 
 
 class Tier:
