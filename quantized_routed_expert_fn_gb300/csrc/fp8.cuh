@@ -42,8 +42,9 @@ cudaError_t launch_quant8_blocks(const Quant8P &p, cudaStream_t st);
 
 // ---- products (mm8.cu)
 struct Mm8P {
-  // tokens: boxes of 128 bytes x 128 / 32 rows; weights [G * n][k]: 128 bytes x 128 rows; 128B swizzle
-  CUtensorMap tm_a128, tm_a32, tm_b;
+  // tokens: boxes of 128 bytes x a full tile's, 64, 32 and 16 rows; weights [G * n][k]:
+  // 128 bytes x 128 rows; 128B swizzle
+  CUtensorMap tm_a[4], tm_b;
   const uint8_t *a, *sa, *b, *sb;
   int64_t lda, lds;
   int t, n, k, nk, nb;  // nk = ceil(k / 128), nb = ceil(n / 128)
@@ -53,6 +54,8 @@ struct Mm8P {
   int64_t ldo;
   uint8_t *hs;          // silu: scales of h8
   int64_t ldhs;
+  int wmax;             // token rows of a tile at most
+  int wide;             // rows of out start on 16 bytes
   int withhold;
   int *status;
   unsigned long long timeout_ns;
@@ -60,7 +63,7 @@ struct Mm8P {
 enum { kOutF32 = 0, kOutBf16 = 1, kOutSilu8 = 2 };
 // rows the few-row kernel takes (weights streamed once, mma.sync)
 constexpr int kMm8SmallRows = 32;
-int mm8_tensor_maps(Mm8P &p, const char **why);
+int mm8_tensor_maps(Mm8P &p, int out_kind, const char **why);
 cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st);
 cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st);
 

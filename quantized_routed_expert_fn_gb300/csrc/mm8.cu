@@ -119,49 +119,59 @@ __global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant
 
 // ------------------------------------------------------------ tensor cores
 //
-// One CTA per SM walks the tiles blockIdx.x, + gridDim.x, ...  A tile is
-// MB blocks of 128 weight rows (the M side: one TMEM lane a weight row) by
-// up to kTcN / MB token rows of one group (the N side).  Weights on the M
-// side keep M full whatever the group's size; N follows it in steps of 16.
+// Persistent: CTA (or CTA pair) i walks the tiles i, i + grid, ...  A tile is
+// MB blocks of 128 weight rows (the M side: one TMEM lane a weight row) by up
+// to N token rows of one group (the N side).  Weights on the M side keep M
+// full whatever the group's size; N follows it in steps of 16 (32).
+// CG = 2 (the usual form): a cluster of two CTAs takes two neighbouring
+// weight tiles and shares the token rows, each CTA holding half of them
+// (cta_group::2, M = 256).  A CTA then reads 30 KB a k block instead of 44 for
+// the same products: the one-CTA form moved 14 TB/s from L2 to the SMs and
+// was bound by that (8192 x 8192 x 2048 without its MMAs: 120 of 130 us).
 // MB = 2 (silu): 128 gate rows and the 128 up rows of the same channels
 // share the token tile, and the epilogue has a whole 128-channel scale block
 // of h in its four warps.
-//   warp 0    issues the scale copies and MMAs of a stage, commits them
-//   warp 1    TMA: 128 weight rows x 128 k a block, the tile's token rows
-//   warp 2    scale words of the token rows -> shared memory
-//   warp 3    scale words of the weight blocks -> shared memory
+//   warps 0-3 scales: E8M0 bytes -> words in TMEM, each warp its own 32 lanes
+//             (the tensor cores read a row's scale from every quadrant)
 //   warps 4-7 epilogue: TMEM -> registers -> global, from one of two
 //             accumulators while the MMAs fill the other
-// A stage is one k block: 16 KB of weights per M block, up to 28 KB (14 KB)
-// of tokens, their scale words.  Its scale copies go to TMEM columns of the
-// stage's own, so a copy never overwrites scales an MMA in flight reads
-// (the stage's barriers order both).
-constexpr int kTcThreads = 256;
-constexpr int kTcStages = 4;
-constexpr int kTcN = 224;              // accumulator columns of a buffer: two buffers and the scales fill 512
-constexpr int kTcScaleCol = 2 * kTcN;  // first scale column; 16 a stage
-static_assert(kTcScaleCol + 16 * kTcStages <= 512, "tensor memory");
+//   warp 8    (even CTA) issues a stage's MMAs once its operands are there
+//   warp 9    TMA: 128 weight rows x 128 k a block, the CTA's share of the token rows
+// A stage is one k block.  A scale word holds the bytes of four consecutive
+// blocks, as they stand in memory; the MMAs of block kb name byte kb % 4, so
+// scales are written once in four blocks, into one of four slots of TMEM
+// columns with barriers of their own.  The full, scale and acc_empty
+// barriers of a pair are the even CTA's, and the odd CTA's warps
+// arrive on them: what those arrivals order is TMEM accesses (tcgen05
+// fences), no shared memory.  (Scales passed through shared memory needed a
+// release across the cluster every stage, 0.7 us each: 190 us at 8192 x 8192
+// x 2048.)  The others are each CTA's own, committed to both.
+constexpr int kTcThreads = 320;
 constexpr int kMaxGroups = 1024;
 
 struct TcBars {
-  uint64_t full[kTcStages], empty[kTcStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[6], empty[6], sc_full[4], sc_empty[4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int bad;
 };
 
-template <int MB>
+template <int MB, int CG>
 struct TcLay {
-  static constexpr int N = kTcN / MB;                         // token columns of a tile
-  static constexpr int tok = (N + 31) / 32 * 4096;            // bytes of tokens a stage: whole 32-row boxes
-  static constexpr int offW = tok;                            // weights: MB x 16 KB
-  static constexpr int offS = offW + MB * 16384;              // scale words: tokens 2 x 512, weights MB x 512
-  static constexpr int stage = offS + 2048;
-  static constexpr int offEpi = kTcStages * stage;            // silu: h bytes [N][128], maxima [4][N]
-  static constexpr int epi = MB == 2 ? N * 128 + 4 * N * 4 + N * 4 : 0;
-  static constexpr int offTab = (offEpi + epi + 15) & ~15;    // int [G + 1] first row, [G + 1] first token tile
-  static constexpr int offBars = offTab + (2 * (kMaxGroups + 1) + 2) * 4 + 8;
-  static constexpr int smem = ((offBars + 7) & ~7) + (int)sizeof(TcBars) + 1024;
-  static_assert(tok % 1024 == 0 && stage % 1024 == 0, "swizzled stages");
+  static constexpr int step = 16 * CG;                           // tile widths
+  static constexpr int N = MB == 1 ? 224 : (CG == 1 ? 112 : 96); // token columns of a tile
+  static constexpr int accCols = MB * N;                         // of each of two buffers
+  static constexpr int scaleCol = 2 * accCols;                   // then four slots of 12 scale columns
+  static_assert(scaleCol + 12 * 4 <= 512, "tensor memory");
+  static constexpr int stages = CG == 1 ? 4 : (MB == 1 ? 6 : 5);
+  static constexpr int tok = N / CG * 128;                       // this CTA's token rows
+  static constexpr int offW = (tok + 1023) / 1024 * 1024;        // weights: MB x 16 KB
+  static constexpr int stage = offW + MB * 16384;
+  static constexpr int offEpi = stages * stage;  // silu: h bytes [N][128], maxima [4][N]; else 32 x 32 values a warp
+  static constexpr int epi = MB == 2 ? N * 128 + 4 * N * 4 : 4 * 4096;
+  static constexpr int offTab = (offEpi + epi + 15) & ~15;       // int [G + 1] first row, [G + 1] first token tile
+  static constexpr int offBars = (offTab + 2 * (kMaxGroups + 1) * 4 + 15) & ~15;
+  static constexpr int smem = offBars + (int)sizeof(TcBars) + 1024;
+  static_assert(stage % 1024 == 0, "swizzled stages");
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
@@ -169,10 +179,12 @@ struct Tile {
   int g, mt, n0, nlen, N;
 };
 
+template <int CG>
 __device__ bool tc_wait(uint64_t *bar, uint32_t par, const Mm8P &P) {
-  if (mbar_try_wait(bar, par)) return true;
+  auto done = [&] { return CG == 1 ? mbar_try_wait(bar, par) : tc05::mbar_try_wait_cluster(bar, par); };
+  if (done()) return true;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, par)) {
+  while (!done()) {
     if (globaltimer() - t0 > P.timeout_ns) {
       atomicCAS(P.status, 0, kStatusTimeout);
       return false;
@@ -180,41 +192,54 @@ __device__ bool tc_wait(uint64_t *bar, uint32_t par, const Mm8P &P) {
   }
   return true;
 }
+template <int CG>
 __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t par, const Mm8P &P) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = tc_wait(bar, par, P);
+  if ((threadIdx.x & 31) == 0) ok = tc_wait<CG>(bar, par, P);
   return __shfl_sync(FULLM, ok ? 1 : 0, 0) != 0;
 }
 
-template <int MB, int KIND>
+template <int MB, int KIND, int CG>
 __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ Mm8P P) {
   pdl_launch_next();
   extern __shared__ __align__(1024) uint8_t smraw[];
+  // the same offset in both CTAs of a pair: dynamic shared memory starts alike
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~(uintptr_t)1023);
-  using LY = TcLay<MB>;
-  TcBars &B = *reinterpret_cast<TcBars *>(sm + ((LY::offBars + 7) & ~7));
+  using LY = TcLay<MB, CG>;
+  constexpr int S = LY::stages;
+  TcBars &B = *reinterpret_cast<TcBars *>(sm + LY::offBars);
   int *s_off = reinterpret_cast<int *>(sm + LY::offTab), *s_tile = s_off + kMaxGroups + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CG == 1 ? 0 : (int)tc05::cluster_rank();
   const int G = P.G > 0 ? P.G : 1, nk = P.nk;
-  const int nmt = MB == 2 ? P.n / 256 : P.nb;  // weight tiles a group
+  const int nmt = MB == 2 ? P.n / 256 : P.nb;   // weight tiles a group
+  const int nmp = (nmt + CG - 1) / CG;          // taken CG at a time
 
   if (tid == 0) {
-    for (int s = 0; s < kTcStages; s++) {
-      mbar_init(&B.full[s], 3);
+    for (int s = 0; s < S; s++) {
+      mbar_init(&B.full[s], 1);
       mbar_init(&B.empty[s], 1);
+    }
+    for (int s = 0; s < 4; s++) {
+      mbar_init(&B.sc_full[s], 4 * CG);
+      mbar_init(&B.sc_empty[s], 1);
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(&B.acc_full[b], 1);
-      mbar_init(&B.acc_empty[b], 4);
+      mbar_init(&B.acc_empty[b], 4 * CG);
     }
     mbar_init(&B.drain, 1);
     fence_mbar_init();
     B.bad = 0;
   }
-  if (warp == 0) tc05::alloc(&B.tmem, 512);
+  if (warp == 8) {
+    if constexpr (CG == 1) tc05::alloc(&B.tmem, 512);
+    else tc05::alloc_pair(&B.tmem, 512);
+  }
   pdl_wait_prev();  // the offsets and the operands may be the previous kernel's
   tc05::fence_before();
-  __syncthreads();
+  if constexpr (CG == 1) __syncthreads();
+  else tc05::cluster_sync();
   tc05::fence_after();
   const uint32_t tmem = B.tmem;
   // group table: first row and first token tile of every group
@@ -224,16 +249,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
     for (int g = tid; g < G; g += kTcThreads)
       if (s_off[g] < 0 || s_off[g] > s_off[g + 1] || s_off[g + 1] > P.t) B.bad = 1;
     __syncthreads();
-    if (B.bad) {
-      if (tid == 0) atomicCAS(P.status, 0, kStatusDevice);
-      if (warp == 0) tc05::dealloc(tmem, 512);
-      return;
-    }
     if (warp == 0) {
       int base = 0;
       for (int g0 = 0; g0 < G; g0 += 32) {
         const int g = g0 + lane;
-        const int c = g < G ? (s_off[g + 1] - s_off[g] + LY::N - 1) / LY::N : 0;
+        const int c = g < G && !B.bad ? (s_off[g + 1] - s_off[g] + P.wmax - 1) / P.wmax : 0;
         int x = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -245,199 +265,215 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       }
       if (lane == 0) s_tile[G] = base;
     }
+    if (B.bad && tid == 0) atomicCAS(P.status, 0, kStatusDevice);
   } else if (tid == 0) {
     s_off[0] = 0, s_off[1] = P.t;
-    s_tile[0] = 0, s_tile[1] = (P.t + LY::N - 1) / LY::N;
+    s_tile[0] = 0, s_tile[1] = (P.t + P.wmax - 1) / P.wmax;
   }
   __syncthreads();
-  const int ntiles = s_tile[G] * nmt;
-  const int my_tiles = (int)blockIdx.x < ntiles ? (ntiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const int ntiles = s_tile[G] * nmp, cl = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
+  const int my_tiles = cl < ntiles ? (ntiles - 1 - cl) / ncl + 1 : 0;
   // tile i: the weight tiles of a token tile follow one another (their token
   // rows stay in L2); the rows of a group are cut into equal tiles
   auto tile_of = [&](int lt) {
-    const int i = (int)blockIdx.x + lt * (int)gridDim.x, tt = i / nmt;
+    const int i = cl + lt * ncl, tt = i / nmp;
     int lo = 0, hi = G;  // the last group whose first token tile is <= tt
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_tile[mid] <= tt) lo = mid; else hi = mid;
     }
     const int m = s_off[lo + 1] - s_off[lo], c = s_tile[lo + 1] - s_tile[lo];
-    const int w = ((m + c - 1) / c + 15) & ~15, r0 = (tt - s_tile[lo]) * w;
+    const int w = ((m + c - 1) / c + LY::step - 1) / LY::step * LY::step, r0 = (tt - s_tile[lo]) * w;
     Tile T;
-    T.g = lo, T.mt = i - tt * nmt;
+    T.g = lo, T.mt = (i - tt * nmp) * CG + rank;
     T.n0 = s_off[lo] + r0;
     T.nlen = max(0, min(w, m - r0));
-    T.N = max(16, (T.nlen + 15) & ~15);
+    T.N = max(LY::step, (T.nlen + LY::step - 1) / LY::step * LY::step);
     return T;
   };
+  auto weight_row = [&](const Tile &T, int m) { return T.g * P.n + (MB == 2 ? m * (P.n / 2) : 0) + T.mt * 128; };
+  // arrive on a barrier of the even CTA (this CTA's, without a pair)
+  auto arrive_even = [&](uint64_t *bar) {
+    if constexpr (CG == 1) tc05::mbar_arrive(bar);
+    else tc05::mbar_arrive_cluster(tc05::map_rank(bar, 0));
+  };
+  // a pair's last tile may have no weight tile for the odd CTA: its rows are
+  // some others' (or none), and nothing of them is stored
 
-  if (warp == 0) {
+  if (warp == 8) {
     // ---------------------------------------------------------------- MMA issue
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int lt = 0; lt < my_tiles && ok; lt++) {
-      const Tile T = tile_of(lt);
-      const int b = lt & 1;
-      if (!tc_warp_wait(&B.acc_empty[b], (uint32_t)(((lt >> 1) & 1) ^ 1), P)) break;
-      tc05::fence_after();
-      const uint32_t d = tmem + (uint32_t)(b * kTcN), idesc = tc05::idesc_mx_e4m3(T.N);
-      for (int kb = 0; kb < nk; kb++) {
-        if (!tc_warp_wait(&B.full[s], ph, P)) {
-          ok = false;
-          break;
-        }
+    // one thread walks the loop: no exchange with the rest of the warp
+    // between a stage's arrival and its MMAs
+    if (rank == 0 && tc05::elect_one()) {
+      int s = 0, sl = 0;
+      uint32_t ph = 0, slp = 0;
+      bool ok = true;
+      Tile Tn;
+      if (my_tiles > 0) Tn = tile_of(0);
+      const uint32_t base = smem_u32(sm);
+      for (int lt = 0; lt < my_tiles && ok; lt++) {
+        const Tile T = Tn;
+        const int b = lt & 1;
+        if (!tc_wait<CG>(&B.acc_empty[b], (uint32_t)(((lt >> 1) & 1) ^ 1), P)) break;
         tc05::fence_after();
-        if (tc05::elect_one()) {
-          const uint32_t st = smem_u32(sm) + (uint32_t)(s * LY::stage), sc = st + LY::offS;
-          const uint32_t sfb = tmem + (uint32_t)(kTcScaleCol + 16 * s), sfa = sfb + 8;
-          tc05::cp_scales(sfb, tc05::sdesc_scales(sc));
-          if (T.N > 128) tc05::cp_scales(sfb + 4, tc05::sdesc_scales(sc + 512));
-#pragma unroll
-          for (int m = 0; m < MB; m++) tc05::cp_scales(sfa + 4 * m, tc05::sdesc_scales(sc + 1024 + 512 * m));
+        const uint32_t d = tmem + (uint32_t)(b * LY::accCols), idesc = tc05::idesc_mx_e4m3(128 * CG, T.N);
+        for (int kb = 0; kb < nk; kb++) {
+          if (((kb & 3) == 0 && !tc_wait<CG>(&B.sc_full[sl], slp, P)) || !tc_wait<CG>(&B.full[s], ph, P)) {
+            ok = false;
+            break;
+          }
+          tc05::fence_after();
+          const uint32_t st = base + (uint32_t)(s * LY::stage);
+          const uint32_t sfb = tmem + (uint32_t)(LY::scaleCol + 12 * sl), sfa = sfb + (MB == 1 ? 8 : 4);
+          const uint32_t id = idesc | tc05::idesc_scale_byte(kb & 3);
           const uint64_t bd = tc05::sdesc(st);
 #pragma unroll
           for (int m = 0; m < MB; m++) {
             const uint64_t ad = tc05::sdesc(st + LY::offW + 16384 * m);
 #pragma unroll
             for (int j = 0; j < 4; j++)
-              tc05::mma_mx(d + (uint32_t)(m * LY::N), ad + 2 * j, bd + 2 * j, idesc, sfa + 4 * m, sfb, (kb | j) != 0);
+              tc05::mma_mx<CG>(d + (uint32_t)(m * LY::N), ad + 2 * j, bd + 2 * j, id, sfa + 4 * m, sfb, (kb | j) != 0);
           }
-          tc05::commit(&B.empty[s]);
+          if constexpr (CG == 1) tc05::commit(&B.empty[s]);
+          else tc05::commit_pair(&B.empty[s]);
+          if (++s == S) s = 0, ph ^= 1;
+          if ((kb & 3) == 3 || kb == nk - 1) {
+            if constexpr (CG == 1) tc05::commit(&B.sc_empty[sl]);
+            else tc05::commit_pair(&B.sc_empty[sl]);
+            if (++sl == 4) sl = 0, slp ^= 1;
+          }
+          if (kb == 0 && lt + 1 < my_tiles) Tn = tile_of(lt + 1);  // while the MMAs run
         }
-        __syncwarp();
-        if (++s == kTcStages) s = 0, ph ^= 1;
+        if (ok) {
+          if constexpr (CG == 1) tc05::commit(&B.acc_full[b]);
+          else tc05::commit_pair(&B.acc_full[b]);
+        }
       }
-      if (ok) {
-        if (tc05::elect_one()) tc05::commit(&B.acc_full[b]);
-        __syncwarp();
-      }
+      // every MMA issued here has completed before TMEM is released
+      if constexpr (CG == 1) tc05::commit(&B.drain);
+      else tc05::commit_pair(&B.drain);
+      tc_wait<CG>(&B.drain, 0, P);
     }
-    // every MMA issued here has completed before TMEM is released
-    if (tc05::elect_one()) tc05::commit(&B.drain);
     __syncwarp();
-    tc_warp_wait(&B.drain, 0, P);
-  } else if (warp == 1) {
+  } else if (warp == 9) {
     // ---------------------------------------------------------------- TMA
     int f = 0;
     bool ok = true;
     for (int lt = 0; lt < my_tiles && ok; lt++) {
       const Tile T = tile_of(lt);
-      const int n128 = T.N >> 7, n32 = ((T.N & 127) + 31) >> 5, ntok = n128 + n32;
-      const uint32_t bytes = (uint32_t)((n128 * 128 + n32 * 32) * 128 + MB * 16384);
+      // this CTA's token rows of the tile: one box of a full tile's rows, or
+      // boxes of 64, 32 and 16 rows.  One lane issues them all: the copy's operands are uniform registers,
+      // and lanes with operands of their own would be served one by one
+      // (per-lane boxes took longer to issue than a stage's MMAs take)
+      const int rows = T.N / CG, first = T.n0 + rank * rows;
+      const uint32_t bytes = (uint32_t)(rows * 128 + MB * 16384) * CG;
       for (int kb = 0; kb < nk; kb++, f++) {
-        const int s = f % kTcStages;
-        if (!tc_warp_wait(&B.empty[s], (uint32_t)(((f / kTcStages) & 1) ^ 1), P)) {
+        const int s = f % S;
+        if (!tc_warp_wait<CG>(&B.empty[s], (uint32_t)(((f / S) & 1) ^ 1), P)) {
           ok = false;
           break;
         }
-        uint8_t *st = sm + s * LY::stage;
         // (failure-detection test: CTA 0 never expects its first stage's
         // copies, so the MMA warp's bounded wait runs out)
-        const bool withheld = P.withhold && blockIdx.x == 0 && f == 0;
-        if (withheld) {
+        if (P.withhold && blockIdx.x == 0 && f == 0) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_expect_tx(&B.full[s], bytes);
-        __syncwarp();
-        if (lane < ntok) {
-          const int r0 = lane < n128 ? 128 * lane : 128 * n128 + 32 * (lane - n128);
-          tc05::tma_load_2d(st + r0 * 128, lane < n128 ? &P.tm_a128 : &P.tm_a32, kb * 128, T.n0 + r0, &B.full[s]);
-        } else if (lane < ntok + MB) {
-          const int m = lane - ntok;
-          const int row = T.g * P.n + (MB == 2 ? m * (P.n / 2) : 0) + T.mt * 128;
-          tc05::tma_load_2d(st + LY::offW + 16384 * m, &P.tm_b, kb * 128, row, &B.full[s]);
+        if (tc05::elect_one()) {
+          uint8_t *st = sm + s * LY::stage;
+          if (rank == 0) mbar_expect_tx(&B.full[s], bytes);
+          const uint32_t bar = CG == 1 ? smem_u32(&B.full[s]) : tc05::map_rank(&B.full[s], 0);
+          auto load = [&](void *dst, const CUtensorMap *map, int y) { tc05::tma_load_2d_cg<CG>(dst, map, kb * 128, y, bar); };
+#pragma unroll
+          for (int m = 0; m < MB; m++) load(st + LY::offW + 16384 * m, &P.tm_b, weight_row(T, m));
+          if (rows == LY::N / CG) {
+            load(st, &P.tm_a[0], first);
+          } else {
+            int r0 = 0;
+            for (; r0 + 64 <= rows; r0 += 64) load(st + r0 * 128, &P.tm_a[1], first + r0);
+            if (rows & 32) load(st + r0 * 128, &P.tm_a[2], first + r0), r0 += 32;
+            if (rows & 16) load(st + r0 * 128, &P.tm_a[3], first + r0);
+          }
         }
+        __syncwarp();
       }
     }
-    // copies still in flight land before the CTA ends
-    if (lane == 0)
-      for (int g = f > kTcStages ? f - kTcStages : 0; g < f; g++)
-        tc_wait(&B.full[g % kTcStages], (uint32_t)((g / kTcStages) & 1), P);
+    // copies still in flight land before the CTA (the pair) ends
+    if (lane == 0 && rank == 0)
+      for (int g = f > S ? f - S : 0; g < f; g++) tc_wait<CG>(&B.full[g % S], (uint32_t)((g / S) & 1), P);
     __syncwarp();
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- token scales
-    // lane l: rows l, l + 32, ... of the tile; four blocks' bytes a load
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- scales
+    // Tokens: lane l has the rows l, l + 32, ... of the tile, four blocks'
+    // bytes a word, the next four (the next tile's first) on their way;
+    // weights: lane l has block (kb & ~31) + l of the tile's weight rows.
     int f = 0;
     bool ok = true;
-    for (int lt = 0; lt < my_tiles && ok; lt++) {
-      const Tile T = tile_of(lt);
-      uint32_t cur[7], nxt[7];
-      auto fetch = [&](int kb, uint32_t (&v)[7]) {
+    constexpr int R = (LY::N + 31) / 32, WB = MB == 1 ? 8 : 4;
+    uint32_t nxt[R], wv[MB];
+    auto fetch = [&](const Tile &T, int kb) {
 #pragma unroll
-        for (int i = 0; i < 7; i++) {
-          const int r = T.n0 + lane + 32 * i;
-          v[i] = 32 * i < T.N && r < P.t && kb < nk
-                     ? *reinterpret_cast<const uint32_t *>(P.sa + (size_t)r * P.lds + kb) : 0x7f7f7f7fu;
-        }
-      };
-      fetch(0, nxt);
-      for (int kb = 0; kb < nk; kb++, f++) {
-        if ((kb & 3) == 0) {
-#pragma unroll
-          for (int i = 0; i < 7; i++) cur[i] = nxt[i];
-          fetch(kb + 4, nxt);
-        }
-        const int s = f % kTcStages;
-        if (!tc_warp_wait(&B.empty[s], (uint32_t)(((f / kTcStages) & 1) ^ 1), P)) {
-          ok = false;
-          break;
-        }
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = i < 7 ? ((cur[i < 7 ? i : 0] >> (8 * (kb & 3))) & 0xffu) * 0x01010101u : 0x7f7f7f7fu;
-        uint4 *dst = reinterpret_cast<uint4 *>(sm + s * LY::stage + LY::offS) + lane;
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (T.N > 128) dst[32] = make_uint4(w[4], w[5], w[6], w[7]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc05::mbar_arrive(&B.full[s]);
+      for (int i = 0; i < R; i++) {
+        const int r = T.n0 + lane + 32 * i;
+        nxt[i] = 32 * i < T.N && r < P.t ? *reinterpret_cast<const uint32_t *>(P.sa + (size_t)r * P.lds + kb) : 0u;
       }
-    }
-  } else if (warp == 3) {
-    // ---------------------------------------------------------------- weight scales
-    int f = 0;
-    bool ok = true;
+    };
+    Tile T, Tn;
+    if (my_tiles > 0) Tn = tile_of(0), fetch(Tn, 0);
     for (int lt = 0; lt < my_tiles && ok; lt++) {
-      const Tile T = tile_of(lt);
-      const uint8_t *sb[MB];
-      uint32_t v[MB];
-#pragma unroll
-      for (int m = 0; m < MB; m++)
-        sb[m] = P.sb + ((size_t)T.g * P.nb + (MB == 2 ? m * (P.nb / 2) : 0) + T.mt) * nk;
-      for (int kb = 0; kb < nk; kb++, f++) {
+      T = Tn;
+      if (lt + 1 < my_tiles) Tn = tile_of(lt + 1);
+      for (int kb = 0; kb < nk; kb += 4, f++) {
         if ((kb & 31) == 0)
 #pragma unroll
-          for (int m = 0; m < MB; m++) v[m] = kb + lane < nk ? sb[m][kb + lane] : 127u;
-        const int s = f % kTcStages;
-        if (!tc_warp_wait(&B.empty[s], (uint32_t)(((f / kTcStages) & 1) ^ 1), P)) {
+          for (int m = 0; m < MB; m++)
+            wv[m] = kb + lane < nk && T.mt < nmt
+                        ? P.sb[((size_t)T.g * P.nb + (MB == 2 ? m * (P.nb / 2) : 0) + T.mt) * nk + kb + lane] : 0u;
+        uint32_t w[12];  // token rows 0-31, 32-63, ...; then the weight blocks, the same for all rows
+#pragma unroll
+        for (int i = 0; i < WB; i++) w[i] = i < R ? nxt[i < R ? i : 0] : 0u;
+        if (kb + 4 < nk) fetch(T, kb + 4);
+        else if (lt + 1 < my_tiles) fetch(Tn, 0);
+#pragma unroll
+        for (int m = 0; m < MB; m++) {
+          uint32_t x = 0;
+#pragma unroll
+          for (int i = 0; i < 4; i++) x |= __shfl_sync(FULLM, wv[m], (kb + i) & 31) << (8 * i);
+#pragma unroll
+          for (int i = 0; i < 4; i++) w[WB + 4 * m + i] = x;
+        }
+        const int sl = f & 3;
+        if (!tc_warp_wait<CG>(&B.sc_empty[sl], (uint32_t)(((f >> 2) & 1) ^ 1), P)) {
           ok = false;
           break;
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(sm + s * LY::stage + LY::offS + 1024) + lane;
-#pragma unroll
-        for (int m = 0; m < MB; m++) {
-          const uint32_t w = __shfl_sync(FULLM, v[m], kb & 31) * 0x01010101u;
-          dst[32 * m] = make_uint4(w, w, w, w);
-        }
-        fence_proxy_async_smem();
+        tc05::fence_after();
+        tc05::st12(tmem + (uint32_t)(LY::scaleCol + 12 * sl) + ((uint32_t)(32 * warp) << 16), w);
+        tc05::wait_st();
+        tc05::fence_before();
         __syncwarp();
-        if (lane == 0) tc05::mbar_arrive(&B.full[s]);
+        if (lane == 0) arrive_even(&B.sc_full[sl]);
       }
     }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;    // TMEM lane quadrant this warp may read
     const int et = tid - 128;  // 0..127 over the epilogue warps: the tile's weight row (channel)
+    auto release = [&](int b) {  // the accumulator is read: the MMAs may fill it again
+      tc05::fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_even(&B.acc_empty[b]);
+    };
     for (int lt = 0; lt < my_tiles; lt++) {
       const Tile T = tile_of(lt);
       const int b = lt & 1;
       // the four epilogue warps stop together (they share named barriers)
-      if (!tc05::named_and(2, 128, tc_warp_wait(&B.acc_full[b], (uint32_t)((lt >> 1) & 1), P))) break;
+      if (!tc05::named_and(2, 128, tc_warp_wait<CG>(&B.acc_full[b], (uint32_t)((lt >> 1) & 1), P))) break;
       tc05::fence_after();
-      const uint32_t tl = tmem + (uint32_t)(b * kTcN) + ((uint32_t)(32 * q) << 16);
-      if constexpr (KIND == kOutSilu8) {
+      const uint32_t tl = tmem + (uint32_t)(b * LY::accCols) + ((uint32_t)(32 * q) << 16);
+      if (T.mt >= nmt) {
+        release(b);
+      } else if constexpr (KIND == kOutSilu8) {
         uint8_t *hb = sm + LY::offEpi;                                     // [N][128] h in e4m3
         uint32_t *mx = reinterpret_cast<uint32_t *>(hb + LY::N * 128);     // [4][N] warp maxima
         // channel scale blocks are whole: 128 channels = this tile's rows
@@ -465,38 +501,58 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
             hb[(c0 + j) * 128 + et] = (uint8_t)e4m3x2(v, 0.f);
           }
         }
-        // the accumulator is read: the next tile's MMAs may fill it
-        tc05::fence_before();
-        __syncwarp();
-        if (lane == 0) tc05::mbar_arrive(&B.acc_empty[b]);
+        release(b);
         tc05::named_sync(1, 128);
         for (int i = et; i < T.nlen * 8; i += 128)
           *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(P.out) + (size_t)(T.n0 + (i >> 3)) * P.ldo + T.mt * 128 +
                                      (i & 7) * 16) = *reinterpret_cast<const uint4 *>(hb + i * 16);
         tc05::named_sync(1, 128);  // hb and the maxima are free again
       } else {
+        // 32 tokens at a time: the warp's 32 x 32 piece is turned in shared
+        // memory so that a lane stores 16 bytes of a token's row (a store a
+        // token of 64 bytes each took 17 cycles an instruction and bound the
+        // kernel); rows that do not allow that are stored value by value
         using O = typename std::conditional<KIND == kOutF32, float, uint16_t>::type;
-        const int row = T.mt * 128 + et;
-        O *o = static_cast<O *>(P.out) + (size_t)T.n0 * P.ldo + row;
-        for (int c0 = 0; c0 < T.N; c0 += 16) {
-          float v[16];
-          tc05::ld16(tl + c0, v);
-          if (row < P.n) {
+        constexpr int V = 16 / sizeof(O), per = 32 / V;  // values a 16-byte piece, pieces a token
+        O *stg = reinterpret_cast<O *>(sm + LY::offEpi) + q * 1024;
+        const int row0 = T.mt * 128 + 32 * q;
+        O *o = static_cast<O *>(P.out) + (size_t)T.n0 * P.ldo + row0;
+        const bool wide = P.wide && row0 + 32 <= P.n;
+        for (int c0 = 0; c0 < T.N; c0 += 32) {
+          float v[32];
+          if (c0 + 32 <= T.N) tc05::ld32(tl + c0, v);
+          else tc05::ld16(tl + c0, v);
+          if (wide) {
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; j++)
-              if (c0 + j < T.nlen) store_out(o + (int64_t)(c0 + j) * P.ldo, v[j]);
+            for (int j = 0; j < 32; j++) store_out(stg + j * 32 + lane, v[j]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < per; i++) {
+              const int tok = i * (32 / per) + lane / per, piece = lane % per;
+              if (c0 + tok < T.nlen)
+                *reinterpret_cast<uint4 *>(o + (int64_t)(c0 + tok) * P.ldo + piece * V) =
+                    *reinterpret_cast<const uint4 *>(stg + tok * 32 + piece * V);
+            }
+          } else if (row0 + lane < P.n) {
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+              if (c0 + j < T.nlen) store_out(o + (int64_t)(c0 + j) * P.ldo + lane, v[j]);
           }
         }
-        tc05::fence_before();
-        __syncwarp();
-        if (lane == 0) tc05::mbar_arrive(&B.acc_empty[b]);
+        release(b);
       }
     }
   }
 
   tc05::fence_before();
-  __syncthreads();
-  if (warp == 0) tc05::dealloc(tmem, 512);
+  if constexpr (CG == 1) {
+    __syncthreads();
+    if (warp == 8) tc05::dealloc(tmem, 512);
+  } else {
+    tc05::cluster_sync();
+    if (warp == 8) tc05::dealloc_pair(tmem, 512);
+  }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -527,33 +583,51 @@ bool make_map8(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, u
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MB, int KIND>
+template <int MB, int KIND, int CG>
 cudaError_t launch_tc(const Mm8P &p, int grid, bool pdl, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcLay<MB>::smem);
+  constexpr int smem = TcLay<MB, CG>::smem;
+  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (CG == 2) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = 2, at[n].val.clusterDim.y = 1, at[n].val.clusterDim.z = 1;
+    n++;
+  }
+  if (pdl) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    n++;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = TcLay<MB>::smem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = at;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, mm8_tc<MB, KIND>, p);
+  cfg.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&cfg, mm8_tc<MB, KIND, CG>, p);
 }
+
+// weight tiles of a group, and whether CTA pairs take them two at a time
+int weight_tiles(const Mm8P &p, int out_kind) { return out_kind == kOutSilu8 ? p.n / 256 : p.nb; }
+bool use_pairs(const Mm8P &p, int out_kind) { return weight_tiles(p, out_kind) > 1; }
 
 }  // namespace
 
-int mm8_tensor_maps(Mm8P &p, const char **why) {
+int mm8_tensor_maps(Mm8P &p, int out_kind, const char **why) {
   if (!encode_fn()) {
     *why = "cuTensorMapEncodeTiled is not available from the driver";
     return -1;
   }
   const uint64_t rows_b = (uint64_t)(p.G > 0 ? p.G : 1) * p.n;
-  if (!make_map8(&p.tm_a128, p.a, p.k, p.t, p.lda, 128) || !make_map8(&p.tm_a32, p.a, p.k, p.t, p.lda, 32) ||
-      !make_map8(&p.tm_b, p.b, p.k, rows_b, p.k, 128)) {
+  const bool pairs = use_pairs(p, out_kind);
+  const uint32_t full = out_kind == kOutSilu8 ? (pairs ? TcLay<2, 2>::N / 2 : TcLay<2, 1>::N)
+                                              : (pairs ? TcLay<1, 2>::N / 2 : TcLay<1, 1>::N);
+  bool ok = make_map8(&p.tm_b, p.b, p.k, rows_b, p.k, 128);
+  for (int i = 0; i < 4; i++) ok = ok && make_map8(&p.tm_a[i], p.a, p.k, p.t, p.lda, i ? 128u >> i : full);
+  if (!ok) {
     *why = "cuTensorMapEncodeTiled rejected a tensor map";
     return -1;
   }
@@ -573,15 +647,23 @@ cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st) {
+template <int MB, int KIND>
+cudaError_t launch_tc_form(Mm8P p, int n_sms, bool pdl, cudaStream_t st) {
+  const bool pairs = use_pairs(p, KIND);
+  p.wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ldo * (KIND == kOutF32 ? 4 : 2))) & 15) == 0;
+  p.wmax = pairs ? TcLay<MB, 2>::N : TcLay<MB, 1>::N;
   // no more CTAs than tiles (grouped: the bound of one partial tile a group)
-  const int64_t nmax = kTcN / (out_kind == kOutSilu8 ? 2 : 1);
-  const int64_t tt = (p.t + nmax - 1) / nmax + (p.offs ? p.G : 0);
-  const int64_t tiles = tt * (out_kind == kOutSilu8 ? p.n / 256 : p.nb);
-  const int grid = (int)(tiles < n_sms ? tiles : n_sms);
-  if (out_kind == kOutF32) return launch_tc<1, kOutF32>(p, grid, pdl, st);
-  if (out_kind == kOutBf16) return launch_tc<1, kOutBf16>(p, grid, pdl, st);
-  return launch_tc<2, kOutSilu8>(p, grid, pdl, st);
+  const int cg = pairs ? 2 : 1;
+  const int64_t tt = (p.t + p.wmax - 1) / p.wmax + (p.offs ? p.G : 0);
+  const int64_t tiles = tt * ((weight_tiles(p, KIND) + cg - 1) / cg);
+  const int grid = (int)(tiles < n_sms / cg ? tiles : n_sms / cg) * cg;
+  return pairs ? launch_tc<MB, KIND, 2>(p, grid, pdl, st) : launch_tc<MB, KIND, 1>(p, grid, pdl, st);
+}
+
+cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st) {
+  if (out_kind == kOutF32) return launch_tc_form<1, kOutF32>(p, n_sms, pdl, st);
+  if (out_kind == kOutBf16) return launch_tc_form<1, kOutBf16>(p, n_sms, pdl, st);
+  return launch_tc_form<2, kOutSilu8>(p, n_sms, pdl, st);
 }
 
 }  // namespace moe

@@ -47,35 +47,88 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
 }
 
 // Instruction descriptor, kind::mxf8f6f4 with block scaling: D fp32, A and B
-// e4m3 (format 0), both K-major, E8M0 scales (bit 23), scale byte 0 of each
-// scale word, M = 128, N = n (multiple of 16, 16..256).
-__host__ __device__ __forceinline__ uint32_t idesc_mx_e4m3(int n) {
-  return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24);
+// e4m3 (format 0), both K-major, E8M0 scales (bit 23), byte 0 of each scale
+// word (idesc_scale_byte: byte i of both operands' words), M = m (128, or 256 over a CTA pair), N = n (a multiple of 16,
+// of 32 for a pair, up to 256).
+__host__ __device__ __forceinline__ uint32_t idesc_mx_e4m3(int m, int n) {
+  return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
+}
+__host__ __device__ __forceinline__ uint32_t idesc_scale_byte(int i) {
+  return ((uint32_t)i << 4) | ((uint32_t)i << 29);
 }
 
-// Shared-memory descriptor of 32 rows x 16 bytes, rows 16 bytes apart (no
-// swizzle; 8-row groups 128 bytes apart): the source of a scale copy.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t smem_addr) {
-  return (uint64_t)((smem_addr >> 4) & 0x3fffu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
-}
-
-// One thread: 32 rows x 16 bytes of shared memory into four TMEM columns,
-// the same in each of the four 32-lane quadrants.  MMAs issued after it by
-// the same thread read what it wrote.
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
+// CG = 2 in the functions below: the pair form (cta_group::2).  Two CTAs of
+// a cluster hold one 256 x N tile, 128 lanes each; one thread of the even
+// CTA issues, and every operand address means the same offset in both CTAs'
+// shared and tensor memory: each holds its own 128 rows of A and their
+// scales, half the rows of B, and the scales of all of B.
 
 // One thread: D[tmem] (+)= (A * scale A) (B * scale B)^T over k = 32 e4m3
 // values.  The scale word of row r (of A, or of B = column r of D) is in
-// column r / 32 of its scale columns, lane r % 32.
+// column r / 32 of its scale columns, lane r % 32 of every 32-lane quadrant.
+template <int CG>
 __device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// One warp of each CTA of the pair: TMEM for both
+__device__ __forceinline__ void alloc_pair(uint32_t *dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// One thread: arrive on the mbarrier at this offset in both CTAs of the pair
+// once all MMAs issued so far complete.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
       : "memory");
+}
+// shared::cluster address of this offset in the cluster's CTA `rank`
+__device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// Arrive on a barrier of another CTA (release at CTA scope: it orders this
+// thread's tcgen05 accesses, which its fences put before it, and no memory
+// of the other CTA)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // One warp: allocate ncols TMEM columns (power of two >= 32); the address is
@@ -139,6 +192,17 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&v)[32]) {
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Warp: 12 consecutive 32-bit columns of its 32 TMEM lanes from registers;
+// wait_st() before they are overwritten or read.
+__device__ __forceinline__ void st12(uint32_t taddr, const uint32_t (&v)[12]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr + 8), "r"(v[8]), "r"(v[9]),
+               "r"(v[10]), "r"(v[11])
+               : "memory");
+}
+
 // One thread: arrive on the mbarrier once all MMAs issued so far complete.
 __device__ __forceinline__ void commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -165,7 +229,8 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
 }
 
 // Warp: 16 consecutive fp32 columns of the warp's 32 TMEM lanes.
-__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
+template <int NV>
+__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[NV]) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -188,6 +253,31 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
           "r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
+}
+
+// The same with the barrier as a shared::cluster address; CG = 2: it may be
+// the other CTA's of the pair.
+template <int CG>
+__device__ __forceinline__ void tma_load_2d_cg(void *dst, const void *tmap, int x, int y, uint32_t bar) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// 2-D tile into L2 only
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {

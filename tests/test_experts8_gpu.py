@@ -255,7 +255,8 @@ def check_mm8(got, ref, mag, k, out):
 
 SIZES = [(1, 16, 128), (1, 1, 16), (2, 2048, 2048), (4, 100, 144), (7, 129, 4112), (8, 16, 256), (9, 300, 400), (16, 128, 2048),
          (31, 33, 1008), (32, 257, 640), (33, 128, 128), (64, 128, 16), (100, 1, 512), (129, 130, 272), (224, 256, 2048),
-         (225, 100, 384), (449, 384, 1024), (1000, 333, 2000)]
+         (225, 100, 384), (449, 384, 1024), (1000, 333, 2000),
+         (34, 256, 1280), (48, 300, 144), (97, 640, 2048), (193, 129, 128), (700, 1000, 528)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
@@ -335,11 +336,12 @@ def test_mm8_reports_bad_offsets_and_writes_nothing(moe, offs):
     assert status == 0
 
 
-def test_mm8_bounded_wait_reports(moe, monkeypatch):
+@pytest.mark.parametrize("n", [128, 256])
+def test_mm8_bounded_wait_reports(moe, monkeypatch, n):
     """A stage whose copies are never issued: the waits give up, the status says so, the context stays usable."""
     monkeypatch.setenv("MOE_TIMEOUT_MS", "50")
     g = np.random.default_rng(1)
-    a, sa, b, sb = operands(g, 64, 128, 256)
+    a, sa, b, sb = operands(g, 64, n, 256)
     _, status = run_mm8(moe, a, sa, b, sb, "f32", flags=moe.TEST_WITHHOLD)
     assert status == moe.ETIMEOUT
     monkeypatch.delenv("MOE_TIMEOUT_MS")
