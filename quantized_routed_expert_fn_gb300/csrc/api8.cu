@@ -80,7 +80,9 @@ int moe_gate(const moe_gate_cfg *c, const void *logits, int logit_dtype, int64_t
   p.gs = p.E / p.ng, p.top_groups = (int)c->top_groups, p.group_top = (int)c->group_top;
   p.scale = c->scale;
   p.idx = topk_idx, p.w = topk_w;
-  const cudaError_t e = moe::launch_gate(p, (cudaStream_t)stream);
+  int n_sms = 0;
+  if (int r = sm_count(&n_sms)) return r;
+  const cudaError_t e = moe::launch_gate(p, n_sms, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return MOE_OK;
 }
@@ -218,16 +220,17 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
     at += bytes;
     return r;
   };
-  p.h8 = take(z.h8), p.h8s = take(z.h8s);
-  if (moe::ex8_small(H, I, t, top_k)) {
-    e = moe::launch_ex8_small(p, st);
-    return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
-  }
-  p.x8 = take(z.x8), p.x8s = take(z.x8s);
-  p.counts = (int *)take(z.counts), p.offs = (int *)take(z.offs), p.place = (int *)take(z.place);
-  p.y = take(z.y);
   int n_sms = 0;
   if (int r = sm_count(&n_sms)) return r;
+  if (moe::ex8_small(H, I, t, top_k)) {
+    p.h32 = (float *)take(z.h32);
+    p.timeout_ns = moe::timeout_ns();
+    e = moe::launch_ex8_small(p, n_sms, st);
+    return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+  }
+  p.h8 = take(z.h8), p.h8s = take(z.h8s), p.x8 = take(z.x8), p.x8s = take(z.x8s);
+  p.counts = (int *)take(z.counts), p.offs = (int *)take(z.offs), p.place = (int *)take(z.place);
+  p.y = take(z.y);
   moe::Mm8P u, d;
   memset(&u, 0, sizeof u);
   u.a = p.x8, u.lda = H, u.sa = p.x8s, u.lds = p.ldh, u.b = p.gu, u.sb = p.gus;

@@ -2,58 +2,74 @@
 // and weights.
 //
 // Few rows (decode, verify): two kernels that stream the union's weights
-// once.  Every row is a column of the m16n8 tiles, whether it chose the
-// expert or not, so no row lists are built; a CTA whose expert stands
-// earlier in the id table leaves at once, so no union is built either.
-//   gate_up  a cluster of 8 CTAs per (entry, 128 channels): each CTA streams
-//            16 gate and 16 up rows, its warps split k; the cluster shares
-//            the 128 channels' maxima and every CTA writes its h in e4m3
-//   down     a CTA per 16 output rows over all experts of the union: its
-//            warps split (expert, k block), sums meet in a fixed order
+// once, by bulk copies through a ring of shared-memory stages that a warp of
+// its own keeps full, so that HBM is read without a pause between a CTA's
+// tiles.  A stage is a few whole weight rows, contiguous in memory.  Each
+// kernel takes half of an SM's shared memory, so that the second one's CTAs
+// are there, their first weights on the way, while the first ends.
+// Every row is a column of the m16n8 tiles, whether it chose the expert or
+// not, so no row lists are built.
+//   gate_up  persistent; an item is 8 channels of one expert (its 8 gate and
+//            8 up rows are one M = 16 tile), its k blocks shared out over 16
+//            warps, their sums met by a warp of its own; writes h in fp32
+//   down     a CTA per 16 output rows over all experts of the union, the
+//            (expert, k block) items shared out over 16 warps; it quantises h
+//            while its weights arrive; sums meet in a fixed order
 // Many rows: the entries are grouped by expert (count, scan), x is quantised
 // once per row and written to its entries' places, mm8_tc computes h8 and
 // the outputs y, and a last kernel sums a row's weighted outputs in the
 // order of its entries.
-#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
-
-namespace cg = cooperative_groups;
+#include "tc05.cuh"
 
 namespace moe {
 namespace {
 
 constexpr unsigned FULLM = 0xffffffffu;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;  // many rows
+
 
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// One k block of 128: 16 weight rows (eight from lo, eight from hi on, ld
+// bytes apart) times eight rows of x or h.  Lane (g, q) = (lane / 4, lane %
+// 4) takes the bytes 32q .. 32q + 31 of weight rows g and g + 8 and of row g
+// of x (`col`): the k order inside a block is permuted alike on both sides.
+// (Weight rows are a multiple of 128 bytes apart, so two rows of a load meet
+// in a bank; the MMAs take longer than that.  Converting the weights to f16
+// by hand, by the conversion instruction or by integer operations, was 10 to
+// 25% slower than the 8-bit MMA.)
+__device__ __forceinline__ void mma_block(float (&d)[4], const uint8_t *lo, const uint8_t *hi, int ld, int g, int q,
+                                          const uint8_t *col, bool have) {
+  const uint8_t *r0 = lo + g * ld + 32 * q, *r1 = hi + g * ld + 32 * q;
+  uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+  if (have) b0 = *reinterpret_cast<const uint4 *>(col), b1 = *reinterpret_cast<const uint4 *>(col + 16);
+  const uint4 a0 = *reinterpret_cast<const uint4 *>(r0), a2 = *reinterpret_cast<const uint4 *>(r0 + 16);
+  const uint4 a1 = *reinterpret_cast<const uint4 *>(r1), a3 = *reinterpret_cast<const uint4 *>(r1 + 16);
+  mma_e4m3(d, a0.x, a1.x, a0.y, a1.y, b0.x, b0.y);
+  mma_e4m3(d, a0.z, a1.z, a0.w, a1.w, b0.z, b0.w);
+  mma_e4m3(d, a2.x, a3.x, a2.y, a3.y, b1.x, b1.y);
+  mma_e4m3(d, a2.z, a3.z, a2.w, a3.w, b1.z, b1.w);
 }
 
-// one k block of 128: 16 weight rows (pieces at 16q and 64 + 16q of rows g
-// and g + 8) times eight rows of x (the same pieces of row g)
-struct Frag {
-  uint4 a[2][2];
-};
-__device__ __forceinline__ void load_frag(Frag &f, const uint8_t *row_g, size_t ld8) {
-  f.a[0][0] = ldg_stream4(row_g);
-  f.a[0][1] = ldg_stream4(row_g + ld8);
-  f.a[1][0] = ldg_stream4(row_g + 64);
-  f.a[1][1] = ldg_stream4(row_g + 64 + ld8);
+// bounded wait on an mbarrier phase, of a thread and of a warp; false (and
+// the status) once the limit passes
+__device__ bool thread_wait(uint64_t *bar, uint32_t par, const Ex8P &P) {
+  if (mbar_try_wait(bar, par)) return true;
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, par))
+    if (globaltimer() - t0 > P.timeout_ns) {
+      atomicCAS(P.status, 0, kStatusTimeout);
+      return false;
+    }
+  return true;
 }
-__device__ __forceinline__ void mma_frag(float (&d)[4], const Frag &f, const uint4 &b0, const uint4 &b1) {
-  mma_e4m3(d, f.a[0][0].x, f.a[0][1].x, f.a[0][0].y, f.a[0][1].y, b0.x, b0.y);
-  mma_e4m3(d, f.a[0][0].z, f.a[0][1].z, f.a[0][0].w, f.a[0][1].w, b0.z, b0.w);
-  mma_e4m3(d, f.a[1][0].x, f.a[1][1].x, f.a[1][0].y, f.a[1][1].y, b1.x, b1.y);
-  mma_e4m3(d, f.a[1][0].z, f.a[1][1].z, f.a[1][0].w, f.a[1][1].w, b1.z, b1.w);
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t par, const Ex8P &P) {
+  if (__all_sync(FULLM, mbar_try_wait(bar, par))) return true;
+  return __all_sync(FULLM, thread_wait(bar, par, P));
 }
 
 // eight consecutive values of x
@@ -85,197 +101,372 @@ __device__ __forceinline__ uint2 quant128(const float (&v)[8], uint32_t &e) {
 
 // ------------------------------------------------------------ few rows
 
-__host__ __device__ constexpr int xs_stride(int H) { return H + 64; }  // rows 64 bytes apart in the banks
-size_t gate_up_smem(int H) { return (size_t)kEx8SmallRows * (xs_stride(H) + (H / 128) * 4); }
+constexpr int kMaxEntries = kEx8SmallRows * 32;
+constexpr int kMaxStages = 24;
+constexpr int kDownWarps = 16;
+constexpr size_t kSmemCap = 112 * 1024;
 
-template <bool BF16>
-__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kThreads) ex8_gate_up(const __grid_constant__ Ex8P P) {
-  pdl_launch_next();
-  extern __shared__ __align__(16) uint8_t xs[];  // [8][H + 64] e4m3 rows of x, then float [8][H / 128] scales
-  __shared__ float red[kWarps][32][9];
-  __shared__ uint32_t amax[8];  // this CTA's maxima of h per row
-  float *sx = reinterpret_cast<float *>(xs + kEx8SmallRows * xs_stride(P.H));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int H = P.H, I = P.I, K = P.K, nk = H / 128, n = P.t * K, entry = blockIdx.y;
-  if (blockIdx.x == 0 && entry == 0 && tid == 0) *P.status = 0;
-  const uint32_t ex = P.idx[entry];
-  // the cluster leaves as one: its CTAs share the entry
-  bool dup = false;
-  for (int j = tid; j < entry; j += kThreads) dup |= P.idx[j] == ex;
-  if (__syncthreads_or(dup) || ex >= (uint32_t)P.E) return;
-  unsigned used = 0;  // rows that chose this expert
-  for (int j = 0; j < n; j++)
-    if (P.idx[j] == ex) used |= 1u << (j / K);
-
-  const int c0 = blockIdx.x * 16;  // first of this CTA's channels
-  const uint8_t *wg = P.gu + ((size_t)ex * 2 * I + c0 + g) * H + q * 16, *wu = wg + (size_t)I * H;
-  const size_t ld8 = (size_t)8 * H;
-  Frag fg, fu;
-  if (warp < nk) {
-    load_frag(fg, wg + (size_t)warp * 128, ld8);
-    load_frag(fu, wu + (size_t)warp * 128, ld8);
-  }
-  // the rows that chose the expert, in e4m3 (the others' columns are zeros)
-  for (int b = warp * 2; b < kEx8SmallRows * nk; b += 2 * kWarps) {
-    const int bb = b + (lane >> 4), r = bb / nk, kb = bb - r * nk, c = kb * 128 + (lane & 15) * 8;
-    const bool on = bb < kEx8SmallRows * nk && ((used >> r) & 1u);
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) load_x8<BF16>(P.x, (int64_t)r * H + c, v);
-    uint32_t e;
-    const uint2 u = quant128(v, e);
-    if (bb < kEx8SmallRows * nk) {
-      *reinterpret_cast<uint2 *>(xs + r * xs_stride(H) + c) = u;
-      if ((lane & 15) == 0) sx[r * nk + kb] = e8m0_f(e);
-    }
-  }
-  __syncthreads();
-  const uint8_t *sgp = P.gus + ((size_t)ex * (2 * I / 128) + c0 / 128) * nk, *sup = sgp + (size_t)(I / 128) * nk;
-  float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int kb = warp; kb < nk; kb += kWarps) {
-    const Frag cg_ = fg, cu_ = fu;
-    if (kb + kWarps < nk) {
-      load_frag(fg, wg + (size_t)(kb + kWarps) * 128, ld8);
-      load_frag(fu, wu + (size_t)(kb + kWarps) * 128, ld8);
-    }
-    const uint8_t *xr = xs + g * xs_stride(H) + kb * 128 + q * 16;
-    const uint4 b0 = *reinterpret_cast<const uint4 *>(xr), b1 = *reinterpret_cast<const uint4 *>(xr + 64);
-    float dg[4] = {0.f, 0.f, 0.f, 0.f}, du[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_frag(dg, cg_, b0, b1);
-    mma_frag(du, cu_, b0, b1);
-    const float s0 = sx[2 * q * nk + kb], s1 = sx[(2 * q + 1) * nk + kb];
-    const float bg = e8m0_f(sgp[kb]), bu = e8m0_f(sup[kb]);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const float s = (i & 1) ? s1 : s0;
-      ag[i] += dg[i] * s * bg;
-      au[i] += du[i] * s * bu;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    red[warp][g + 8 * (i >> 1)][2 * q + (i & 1)] = ag[i];
-    red[warp][16 + g + 8 * (i >> 1)][2 * q + (i & 1)] = au[i];
-  }
-  __syncthreads();
-  // thread (row of x r, channel c): h, its maximum over the CTA's 16
-  // channels, then over the cluster's 128
-  const int r = tid >> 4, c = tid & 15;  // the first four warps
-  float h = 0.f;
-  if (tid < 128) {
-    float gv = 0.f, uv = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) gv += red[w][c][r], uv += red[w][16 + c][r];
-    h = gv / (1.f + expf(-gv)) * uv;
-    uint32_t a = mag_bits(h);
-#pragma unroll
-    for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(FULLM, a, o));
-    if (c == 0) amax[r] = a;
-  }
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  if (tid < 128) {
-    // lane c < 8 of a row reads CTA c's maximum
-    uint32_t a = c < 8 ? *cl.map_shared_rank(&amax[r], c) : 0u;
-#pragma unroll
-    for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(FULLM, a, o));
-    const uint32_t e = e8m0_of_amax(a);
-    const uint8_t v = (uint8_t)e4m3x2(h * e8m0_inv(e), 0.f);
-    if (r < P.t && ((used >> r) & 1u)) {
-      // at the row's first entry with this expert
-      int j = r * K;
-      while (P.idx[j] != ex) j++;
-      P.h8[(size_t)j * I + c0 + c] = v;
-      if ((blockIdx.x & 7) == 0 && c == 0) P.h8s[(size_t)j * P.ldi + c0 / 128] = (uint8_t)e;
-    }
-  }
-  cl.sync();  // no CTA ends while another may read its maxima
+// The union of the rows' experts, as each kernel builds it for itself (in
+// the order of the id table; ids below E, once each).
+struct Union {
+  uint32_t *ids, *ex;                // [n entries], the experts
+  float *wt;                         // [n entries]
+  float (*w)[kEx8SmallRows];         // [experts] sum of a row's weights for the expert
+  short (*ent)[kEx8SmallRows];       // a row's first entry with that expert, or -1
+  uint8_t *own;                      // [n entries] is a row's first entry with its expert
+  int *n;
+};
+__host__ __device__ constexpr size_t union_bytes(int n) { return (size_t)n * (4 + 4 + 4 + 4 * 8 + 2 * 8 + 1) + 16 + 15; }
+__device__ __forceinline__ Union union_at(void *p, int n) {
+  Union U;
+  U.n = static_cast<int *>(p);
+  U.ids = reinterpret_cast<uint32_t *>(U.n + 4), U.ex = U.ids + n;
+  U.wt = reinterpret_cast<float *>(U.ex + n);
+  U.w = reinterpret_cast<float(*)[kEx8SmallRows]>(U.wt + n);
+  U.ent = reinterpret_cast<short(*)[kEx8SmallRows]>(U.w + n);
+  U.own = reinterpret_cast<uint8_t *>(U.ent + n);
+  return U;
 }
 
-constexpr int kMaxEntries = kEx8SmallRows * 32;
-
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) ex8_down(const __grid_constant__ Ex8P P) {
-  __shared__ uint32_t ids[kMaxEntries];
-  __shared__ int uni[kMaxEntries];  // entries that name an expert first
-  __shared__ int nuni, wsum[kWarps];
-  __shared__ float red[kWarps][16][9];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int H = P.H, I = P.I, K = P.K, nk = I / 128, n = P.t * K, n0 = blockIdx.x * 16;
-  if (tid < n) ids[tid] = P.idx[tid];
-  __syncthreads();
-  bool first = tid < n && ids[tid] < (uint32_t)P.E;
-  for (int j = 0; j < tid && first; j++) first = ids[j] != ids[tid];
-  const unsigned bal = __ballot_sync(FULLM, first);
-  if (lane == 0) wsum[warp] = __popc(bal);
-  __syncthreads();
-  int base = 0;
-  for (int w = 0; w < warp; w++) base += wsum[w];
-  if (first) uni[base + __popc(bal & ((1u << lane) - 1u))] = tid;
-  if (tid == kThreads - 1) nuni = base + __popc(bal);
-  __syncthreads();
-
-  const int items = nuni * nk;  // (expert, k block), k fastest
-  auto wrow = [&](int it) {
-    const int u = it / nk, kb = it - u * nk;
-    return P.dn + ((size_t)ids[uni[u]] * H + n0 + g) * I + kb * 128 + q * 16;
-  };
-  const size_t ld8 = (size_t)8 * I;
-  Frag f;
-  if (warp < items) load_frag(f, wrow(warp), ld8);
-  pdl_wait_prev();  // h8 is the previous kernel's; the weights above are not
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int it = warp; it < items; it += kWarps) {
-    const Frag c = f;
-    if (it + kWarps < items) load_frag(f, wrow(it + kWarps), ld8);
-    const int u = it / nk, kb = it - u * nk;
-    const uint32_t ex = ids[uni[u]];
-    // row g's first entry with this expert, and the sum of its weights
-    auto entry_of = [&](int r, float *wt) {
-      int at = -1;
-      float s = 0.f;
-      if (r < P.t)
-        for (int j = r * K; j < (r + 1) * K; j++)
-          if (ids[j] == ex) {
-            if (at < 0) at = j;
-            s += P.w[j];
-          }
-      *wt = s;
-      return at;
-    };
-    float wg;
-    const int eg = entry_of(g, &wg);
-    uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-    float sg = 0.f;
-    if (eg >= 0) {
-      const uint8_t *hr = P.h8 + (size_t)eg * I + kb * 128 + q * 16;
-      b0 = *reinterpret_cast<const uint4 *>(hr);
-      b1 = *reinterpret_cast<const uint4 *>(hr + 64);
-      sg = e8m0_f(P.h8s[(size_t)eg * P.ldi + kb]) * wg;
-    }
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_frag(d, c, b0, b1);
-    // scales of columns 2q, 2q + 1: lanes with g = 2q, 2q + 1 hold them
-    const float s0 = __shfl_sync(FULLM, sg, 8 * q), s1 = __shfl_sync(FULLM, sg, 8 * q + 4);
-    const float fb = e8m0_f(P.dns[((size_t)ex * (H / 128) + (n0 >> 7)) * nk + kb]);
+// One warp: ids, ex and n.  32 entries at a time: the first of each id among
+// them by a match, those of earlier groups by comparison.
+__device__ void union_warp(const Union &U, const Ex8P &P) {
+  const int lane = threadIdx.x & 31, n = P.t * P.K;
+  uint32_t id[kMaxEntries / 32];
+  float wt[kMaxEntries / 32];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      // a column whose row did not choose the expert adds nothing, whatever
-      // the product is (a NaN weight times zero)
-      const float s = (i & 1) ? s1 : s0;
-      const int col = 2 * q + (i & 1);
-      const bool on = __shfl_sync(FULLM, eg, 4 * col) >= 0;
-      if (on) acc[i] += d[i] * fb * s;
+  for (int i = 0; i < kMaxEntries / 32; i++) {
+    id[i] = 32 * i + lane < n ? P.idx[32 * i + lane] : 0xffffffffu;
+    wt[i] = 32 * i + lane < n ? P.w[32 * i + lane] : 0.f;
+  }
+  int cnt = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxEntries / 32; i++) {
+    if (32 * i >= n) break;
+    if (32 * i + lane < n) U.ids[32 * i + lane] = id[i], U.wt[32 * i + lane] = wt[i], U.own[32 * i + lane] = 0;
+    bool first = __ffs(__match_any_sync(FULLM, id[i])) - 1 == lane && id[i] < (uint32_t)P.E;
+    for (int j = 0; j < cnt; j++) first &= U.ex[j] != id[i];
+    const unsigned bal = __ballot_sync(FULLM, first);
+    if (first) U.ex[cnt + __popc(bal & ((1u << lane) - 1u))] = id[i];
+    cnt += __popc(bal);
+    __syncwarp();
+  }
+  if (lane == 0) *U.n = cnt;
+  __syncwarp();
+}
+// Threads tid of count: ent, w and own, once the union is there.
+__device__ void union_rows(const Union &U, const Ex8P &P, int tid, int count) {
+  for (int i = tid; i < *U.n * kEx8SmallRows; i += count) {
+    const int u = i / kEx8SmallRows, r = i - u * kEx8SmallRows;
+    const uint32_t ex = U.ex[u];
+    int at = -1;
+    float s = 0.f;
+    if (r < P.t)
+      for (int j = r * P.K; j < (r + 1) * P.K; j++)
+        if (U.ids[j] == ex) {
+          if (at < 0) at = j;
+          s += U.wt[j];
+        }
+    U.ent[u][r] = (short)at, U.w[u][r] = s;
+    if (at >= 0) U.own[at] = 1;
+  }
+}
+
+__host__ __device__ constexpr int row_stride(int k) { return k + 16; }  // e4m3 rows of x, h: 16 bytes apart in the banks
+
+// ---- gate_up: dynamic shared memory: ring | x rows | their scales | sums | union
+constexpr int kGuWarps = 16, kGuThreads = 32 * (kGuWarps + 2);
+struct GuLay {
+  int stage, ns;  // bytes of a stage (8 rows), stages (even: an item is two)
+  size_t xs, sx, red, un, total;
+};
+__host__ __device__ inline GuLay gu_layout(int H, int t, int K) {
+  GuLay l{};
+  l.stage = 8 * H;
+  const size_t xs = (size_t)t * row_stride(H), sx = ((size_t)t * (H / 128) * 4 + 15) / 16 * 16, red = 2 * kGuWarps * 512;
+  const size_t rest = xs + sx + red + union_bytes(t * K);
+  const size_t room = kSmemCap > rest ? (kSmemCap - rest) / l.stage : 0;
+  l.ns = (int)(room < kMaxStages ? room : kMaxStages) & ~1;
+  l.xs = (size_t)l.ns * l.stage, l.sx = l.xs + xs, l.red = l.sx + sx, l.un = l.red + red;
+  l.total = (size_t)l.ns * l.stage + rest;
+  return l;
+}
+
+// The warps' steps over the items are counted, not divided: an item costs a
+// warp some 150 instructions, and HBM brings one in 1400 cycles.
+template <bool BF16>
+__global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_constant__ Ex8P P) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], red_full[2], red_empty[2];
+  const GuLay L = gu_layout(P.H, P.t, P.K);
+  uint8_t *xs = sm + L.xs;
+  float *sx = reinterpret_cast<float *>(sm + L.sx);
+  float4 *red = reinterpret_cast<float4 *>(sm + L.red);
+  const Union U = union_at(sm + L.un, P.t * P.K);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int H = P.H, I = P.I, nk = H / 128, nct = I / 8;
+  pdl_launch_next();
+
+  if (warp == kGuWarps) {
+    // ---- the union, then the producer: gate rows, up rows of every item
+    if (lane == 0) {
+      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], kGuWarps);
+      for (int b = 0; b < 2; b++) mbar_init(&red_full[b], kGuWarps), mbar_init(&red_empty[b], 1);
+      fence_mbar_init();
+      if (blockIdx.x == 0) *P.status = 0;
+    }
+    union_warp(U, P);
+    tc05::named_arrive(3, kGuThreads);  // the union and the barriers are there
+    if (lane == 0) {
+      int f = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      const int items = *U.n * nct;
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const int u = it / nct, ct = it - u * nct;
+        const uint8_t *src = P.gu + ((size_t)U.ex[u] * 2 * I + ct * 8) * H;
+        for (int h = 0; h < 2; h++) {
+          ok = thread_wait(&empty[s], ph ^ 1, P);
+          if (!ok) break;
+          mbar_expect_tx(&full[s], (uint32_t)L.stage);
+          bulk_g2s(sm + (size_t)s * L.stage, src + (size_t)h * I * H, (uint32_t)L.stage, &full[s]);
+          f++;
+          if (++s == L.ns) s = 0, ph ^= 1;
+        }
+      }
+      // copies still in flight land before the CTA ends
+      for (int i = f > L.ns ? f - L.ns : 0; i < f; i++) thread_wait(&full[i % L.ns], (uint32_t)((i / L.ns) & 1), P);
+    }
+    return;
+  }
+  if (warp == kGuWarps + 1) {
+    // ---- sums: lane (c, q) adds the warps' parts of channel c, columns 2q
+    // and 2q + 1, in the order of the warps
+    tc05::named_sync(3, kGuThreads);
+    const int items = *U.n * nct;
+    int turn = 0;
+    uint32_t ph = 0;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+      const int u = it / nct, ct = it - u * nct;
+      // the columns' entries: a row's first with this expert
+      int e0 = -1, e1 = -1;
+      for (int r = 0; r < P.t; r++) {
+        const unsigned m = __ballot_sync(FULLM, lane < P.K && U.ids[r * P.K + min(lane, P.K - 1)] == U.ex[u]);
+        const int e = m ? r * P.K + __ffs(m) - 1 : -1;
+        if (r == 2 * q) e0 = e;
+        if (r == 2 * q + 1) e1 = e;
+      }
+      if (!warp_wait(&red_full[turn], ph, P)) break;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kGuWarps; w++) {
+        const float4 p = red[(turn * kGuWarps + w) * 32 + lane];
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&red_empty[turn]);
+      turn ^= 1;
+      if (turn == 0) ph ^= 1;
+      const size_t c = (size_t)ct * 8 + g;
+      if (e0 >= 0) P.h32[(size_t)e0 * I + c] = v.x / (1.f + expf(-v.x)) * v.z;
+      if (e1 >= 0) P.h32[(size_t)e1 * I + c] = v.y / (1.f + expf(-v.y)) * v.w;
+    }
+    return;
+  }
+  // ---- the rows of x in e4m3, half a warp a block, the loads
+  // of two rounds together
+  for (int b = warp * 2; b < P.t * nk; b += 4 * kGuWarps) {
+    float v[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int bb = b + 2 * kGuWarps * i + (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[i][j] = 0.f;
+      if (bb < P.t * nk) load_x8<BF16>(P.x, (int64_t)bb * 128 + (lane & 15) * 8, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int bb = b + 2 * kGuWarps * i + (lane >> 4), r = bb / nk;
+      if (b + 2 * kGuWarps * i >= P.t * nk) break;  // warp-uniform
+      uint32_t e;
+      const uint2 w = quant128(v[i], e);
+      if (bb < P.t * nk) {
+        *reinterpret_cast<uint2 *>(xs + (size_t)r * row_stride(H) + (bb - r * nk) * 128 + (lane & 15) * 8) = w;
+        if ((lane & 15) == 0) sx[bb] = e8m0_f(e);
+      }
     }
   }
+  tc05::named_sync(3, kGuThreads);
+  tc05::named_sync(1, 32 * kGuWarps);
+  const int items = *U.n * nct, step_u = (int)gridDim.x / nct, step_c = (int)gridDim.x - step_u * nct;
+  const bool have = g < P.t, have0 = 2 * q < P.t, have1 = 2 * q + 1 < P.t;
+  const uint8_t *col = xs + (size_t)(have ? g : 0) * row_stride(H) + q * 32;
+  const float *sx0 = sx + (have0 ? 2 * q : 0) * nk, *sx1 = sx + (have1 ? 2 * q + 1 : 0) * nk;
+  const size_t up_s = (size_t)(I / 128) * nk;  // from a gate scale to its up scale
+  int u = (int)blockIdx.x / nct, ct = (int)blockIdx.x - u * nct;
+  // the weight scales of the warp's first k block, loaded an item ahead
+  uint32_t ng = 0, nu = 0;
+  auto prefetch = [&](int uu, int cc) {
+    const uint8_t *sg = P.gus + ((size_t)U.ex[uu] * (2 * I / 128) + cc / 16) * nk + warp;
+    ng = sg[0], nu = sg[up_s];
+  };
+  if ((int)blockIdx.x < items && warp < nk) prefetch(u, ct);
+  int s = 0, turn = 0;
+  uint32_t ph = 0, rph = 0;
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const int u0 = u, ct0 = ct;
+    uint32_t wg = ng, wu = nu;
+    u += step_u, ct += step_c;
+    if (ct >= nct) ct -= nct, u++;
+    if (it + (int)gridDim.x < items && warp < nk) prefetch(u, ct);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!warp_wait(&full[s], ph, P) || !warp_wait(&full[s + 1], ph, P)) break;
+    const uint8_t *gr = sm + (size_t)s * L.stage, *ur = gr + L.stage;
+    for (int kb = warp; kb < nk; kb += kGuWarps) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_block(d, gr + kb * 128, ur + kb * 128, H, g, q, col + kb * 128, have);
+      if (kb >= kGuWarps) {
+        const uint8_t *sg = P.gus + ((size_t)U.ex[u0] * (2 * I / 128) + ct0 / 16) * nk + kb;
+        wg = sg[0], wu = sg[up_s];
+      }
+      const float fg = e8m0_f(wg), fu = e8m0_f(wu), x0 = have0 ? sx0[kb] : 0.f, x1 = have1 ? sx1[kb] : 0.f;
+      acc.x += d[0] * x0 * fg, acc.y += d[1] * x1 * fg, acc.z += d[2] * x0 * fu, acc.w += d[3] * x1 * fu;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]), mbar_arrive(&empty[s + 1]);
+    s += 2;
+    if (s == L.ns) s = 0, ph ^= 1;
+    if (!warp_wait(&red_empty[turn], rph ^ 1, P)) break;
+    red[(turn * kGuWarps + warp) * 32 + lane] = acc;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&red_full[turn]);
+    turn ^= 1;
+    if (turn == 0) rph ^= 1;
+  }
+}
+
+// ---- down: dynamic shared memory: ring | h rows | their scales | weight scales | union | sums
+struct DnLay {
+  int stage, ns;
+  size_t hs, sh, sd, un, red, total;
+};
+__host__ __device__ inline DnLay dn_layout(int I, int n) {
+  DnLay l{};
+  const int nk = I / 128;
+  l.stage = 16 * I;
+  const size_t hs = (size_t)n * row_stride(I), sh = ((size_t)n * nk * 4 + 15) / 16 * 16, red = kDownWarps * 16 * 9 * 4;
+  const size_t un = union_bytes(n) / 16 * 16, rest = hs + 2 * sh + un + red;
+  const size_t room = kSmemCap > rest ? (kSmemCap - rest) / l.stage : 0;
+  l.ns = (int)(room < kMaxStages ? room : kMaxStages);
+  l.hs = (size_t)l.ns * l.stage, l.sh = l.hs + hs, l.sd = l.sh + sh, l.un = l.sd + sh, l.red = l.un + un;
+  l.total = (size_t)l.ns * l.stage + rest;
+  return l;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid_constant__ Ex8P P) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  const int n = P.t * P.K;
+  const DnLay L = dn_layout(P.I, n);
+  uint8_t *hs = sm + L.hs;
+  float *sh = reinterpret_cast<float *>(sm + L.sh), *sd = reinterpret_cast<float *>(sm + L.sd);
+  float *red = reinterpret_cast<float *>(sm + L.red);
+  const Union U = union_at(sm + L.un, n);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int H = P.H, I = P.I, nk = I / 128, n0 = blockIdx.x * 16;
+  if (warp == kDownWarps) {
+    // ---- the union, then the producer: this CTA's rows of every expert
+    if (lane == 0) {
+      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], (uint32_t)nk);
+      fence_mbar_init();
+    }
+    union_warp(U, P);
+    tc05::named_arrive(3, 32 * kDownWarps + 32);
+    if (lane == 0) {
+      int u = 0;
+      const int nu = *U.n;
+      for (; u < nu; u++) {
+        const int s = u % L.ns;
+        if (!thread_wait(&empty[s], (uint32_t)(((u / L.ns) & 1) ^ 1), P)) break;
+        mbar_expect_tx(&full[s], (uint32_t)L.stage);
+        bulk_g2s(sm + (size_t)s * L.stage, P.dn + ((size_t)U.ex[u] * H + n0) * I, (uint32_t)L.stage, &full[s]);
+      }
+      // copies still in flight land before the CTA ends
+      for (int i = u > L.ns ? u - L.ns : 0; i < u; i++) thread_wait(&full[i % L.ns], (uint32_t)((i / L.ns) & 1), P);
+    }
+    return;
+  }
+  tc05::named_sync(3, 32 * kDownWarps + 32);
+  union_rows(U, P, tid, 32 * kDownWarps);
+  const int items = *U.n * nk;  // (expert, k block), k fastest
+  for (int i = tid; i < items; i += 32 * kDownWarps) {
+    const int u = i / nk, kb = i - u * nk;
+    sd[i] = e8m0_f(P.dns[((size_t)U.ex[u] * (H / 128) + (n0 >> 7)) * nk + kb]);
+  }
+  tc05::named_sync(1, 32 * kDownWarps);
+  pdl_wait_prev();  // h is the previous kernel's; the weights on their way are not
+  // h of every entry that has one (of an expert twice in a row: the first) ->
+  // e4m3, half a warp a block, the loads of four rounds together
+  for (int b = warp * 2; b < n * nk; b += 8 * kDownWarps) {
+    float v[4][8];
 #pragma unroll
-  for (int i = 0; i < 4; i++) red[warp][g + 8 * (i >> 1)][2 * q + (i & 1)] = acc[i];
-  __syncthreads();
+    for (int i = 0; i < 4; i++) {
+      const int bb = b + 2 * kDownWarps * i + (lane >> 4), e = bb / nk;
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[i][j] = 0.f;
+      if (bb < n * nk && U.own[e]) load_x8<false>(P.h32, (int64_t)bb * 128 + (lane & 15) * 8, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int bb = b + 2 * kDownWarps * i + (lane >> 4), e = bb / nk;
+      if (b + 2 * kDownWarps * i >= n * nk) break;  // warp-uniform
+      uint32_t x;
+      const uint2 w = quant128(v[i], x);
+      if (bb < n * nk) {
+        *reinterpret_cast<uint2 *>(hs + (size_t)e * row_stride(I) + (bb - e * nk) * 128 + (lane & 15) * 8) = w;
+        if ((lane & 15) == 0) sh[bb] = e8m0_f(x);
+      }
+    }
+  }
+  tc05::named_sync(1, 32 * kDownWarps);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int step_u = kDownWarps / nk, step_k = kDownWarps - step_u * nk;
+  int u = warp / nk, kb = warp - u * nk, s = u % L.ns;
+  uint32_t ph = (uint32_t)((u / L.ns) & 1);
+  for (int it = warp; it < items; it += kDownWarps) {
+    const int e = U.ent[u][g], e0 = U.ent[u][2 * q], e1 = U.ent[u][2 * q + 1];
+    if (!warp_wait(&full[s], ph, P)) break;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint8_t *wr = sm + (size_t)s * L.stage + kb * 128;
+    mma_block(d, wr, wr + 8 * I, I, g, q, hs + (size_t)max(e, 0) * row_stride(I) + kb * 128 + q * 32, e >= 0);
+    // a column whose row did not choose the expert adds nothing, whatever
+    // the product is (a NaN weight times zero)
+    if (e0 >= 0) {
+      const float sc = sh[e0 * nk + kb] * sd[it] * U.w[u][2 * q];
+      acc[0] += d[0] * sc, acc[2] += d[2] * sc;
+    }
+    if (e1 >= 0) {
+      const float sc = sh[e1 * nk + kb] * sd[it] * U.w[u][2 * q + 1];
+      acc[1] += d[1] * sc, acc[3] += d[3] * sc;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    int du = step_u;
+    kb += step_k;
+    if (kb >= nk) kb -= nk, du++;
+    u += du, s += du;
+    while (s >= L.ns) s -= L.ns, ph ^= 1;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) red[(warp * 16 + g + 8 * (i >> 1)) * 9 + 2 * q + (i & 1)] = acc[i];
+  tc05::named_sync(1, 32 * kDownWarps);
   if (tid < 128) {
     const int row = tid & 15, r = tid >> 4;
     if (r < P.t) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; w++) v += red[w][row][r];
+      for (int w = 0; w < kDownWarps; w++) v += red[(w * 16 + row) * 9 + r];
       const size_t o = (size_t)r * H + n0 + row;
       if (BF16) {
         uint16_t b;
@@ -435,34 +626,39 @@ cudaError_t launch_pdl(F f, dim3 grid, unsigned block, size_t smem, cudaStream_t
 
 }  // namespace
 
-bool ex8_small(int H, int I, int t, int K) { return t <= kEx8SmallRows && gate_up_smem(H) <= 200 * 1024; }
+bool ex8_small(int H, int I, int t, int K) {
+  // an item is two of gate_up's stages
+  return t <= kEx8SmallRows && gu_layout(H, t, K).ns >= 4 && dn_layout(I, t * K).ns >= 3;
+}
 
 Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size) {
   const size_t n = (size_t)t * K;
   const size_t ldi = (size_t)(I / 128 + 3) / 4 * 4, ldh = (size_t)(H / 128 + 3) / 4 * 4;
   Ex8Sizes s{};
-  s.h8 = al(n * I), s.h8s = al(n * ldi);
-  s.total = s.h8 + s.h8s;
-  if (!ex8_small(H, I, t, K)) {
-    s.x8 = al(n * H), s.x8s = al(n * ldh);
-    s.counts = al((size_t)(E + 1) * 4), s.offs = al((size_t)(E + 1) * 4), s.place = al(n * 4);
-    s.y = al(n * H * out_size);
-    s.total += s.x8 + s.x8s + s.counts + s.offs + s.place + s.y;
+  if (ex8_small(H, I, t, K)) {
+    s.total = s.h32 = al(n * I * 4);
+    return s;
   }
+  s.h8 = al(n * I), s.h8s = al(n * ldi);
+  s.x8 = al(n * H), s.x8s = al(n * ldh);
+  s.counts = al((size_t)(E + 1) * 4), s.offs = al((size_t)(E + 1) * 4), s.place = al(n * 4);
+  s.y = al(n * H * out_size);
+  s.total = s.h8 + s.h8s + s.x8 + s.x8s + s.counts + s.offs + s.place + s.y;
   return s;
 }
 
-cudaError_t launch_ex8_small(const Ex8P &p, cudaStream_t st) {
-  const size_t smem = gate_up_smem(p.H);
+cudaError_t launch_ex8_small(const Ex8P &p, int n_sms, cudaStream_t st) {
+  const GuLay l = gu_layout(p.H, p.t, p.K);
+  const DnLay d = dn_layout(p.I, p.t * p.K);
   auto f = p.x_bf16 ? ex8_gate_up<true> : ex8_gate_up<false>;
-  if (smem > 32 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  f<<<dim3((unsigned)(p.I / 16), (unsigned)(p.t * p.K)), kThreads, smem, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  auto h = p.out_bf16 ? ex8_down<true> : ex8_down<false>;
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.total);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(h, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)d.total);
   if (e != cudaSuccess) return e;
-  return launch_pdl(p.out_bf16 ? ex8_down<true> : ex8_down<false>, dim3((unsigned)(p.H / 16)), kThreads, 0, st, p);
+  const int items = p.t * p.K * (p.I / 8);
+  f<<<(unsigned)(items < n_sms ? items : n_sms), kGuThreads, l.total, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_pdl(h, dim3((unsigned)(p.H / 16)), 32 * kDownWarps + 32, d.total, st, p);
 }
 
 cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st) {

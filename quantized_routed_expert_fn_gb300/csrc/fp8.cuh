@@ -24,7 +24,7 @@ struct GateP {
   uint32_t *idx;
   float *w;
 };
-cudaError_t launch_gate(const GateP &p, cudaStream_t st);
+cudaError_t launch_gate(const GateP &p, int n_sms, cudaStream_t st);
 
 // ---- quantisation (quant8.cu)
 struct Quant8P {
@@ -104,6 +104,14 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(h), "f"(l));
   return r;
 }
+// D(16x8 f32) += A(16x32 e4m3, row) * B(32x8 e4m3, col)
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | e4m3x2(c, d) << 16;
 }
@@ -116,6 +124,7 @@ namespace moe {
 
 // ---- the routed experts' step (experts8.cu)
 struct Ex8P {
+  unsigned long long timeout_ns;
   int H, E, I, t, K;
   const uint8_t *gu, *gus, *dn, *dns;
   const void *x;
@@ -125,6 +134,7 @@ struct Ex8P {
   void *out;            // [t][H]
   int *status;
   // workspace
+  float *h32;           // few rows: [t * K][I]
   uint8_t *h8, *h8s;    // [t * K][I] e4m3 and [t * K][ldi] scales
   int ldi, ldh;         // scale bytes of a row of h8 / x8
   uint8_t *x8, *x8s;    // many rows: [t * K][H] grouped rows, [t * K][ldh]
@@ -134,12 +144,12 @@ struct Ex8P {
   void *y;              // [t * K][H] weighted outputs in out's type
 };
 struct Ex8Sizes {
-  size_t h8, h8s, x8, x8s, counts, offs, place, y, total;
+  size_t h32, h8, h8s, x8, x8s, counts, offs, place, y, total;
 };
 constexpr int kEx8SmallRows = 8;  // rows of the few-row path: one column each of an m16n8 tile
 bool ex8_small(int H, int I, int t, int K);
 Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size);
-cudaError_t launch_ex8_small(const Ex8P &p, cudaStream_t st);
+cudaError_t launch_ex8_small(const Ex8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_ex8_combine(const Ex8P &p, cudaStream_t st);
 

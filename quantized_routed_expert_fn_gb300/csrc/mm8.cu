@@ -39,14 +39,6 @@ __device__ __forceinline__ void store_out<uint16_t>(uint16_t *p, float v) {
 
 // ------------------------------------------------------------ few rows
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 constexpr int kSmWarps = 8;
 
 // One CTA: 16 weight rows, 8 * NT token columns.  Lane (g, q) = (lane / 4,
@@ -71,32 +63,49 @@ __global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant
   for (int j = 0; j < NT; j++)
 #pragma unroll
     for (int i = 0; i < 4; i++) acc[j][i] = 0.f;
-  for (int kb = warp; kb < P.nk; kb += kSmWarps) {
+  // two blocks' weights in flight: of k = 2048 all that the warp takes
+  uint4 a[2][2][2];  // [block][piece][row g, g + 8]
+  auto load = [&](uint4 (&x)[2][2], int kb) {
     const int k0 = kb * 128 + q * 16, k1 = k0 + 64;
-    uint4 a[2][2];  // [piece][row g, g + 8]
-    a[0][0] = ok0 && k0 < P.k ? ldg_stream4(w0 + k0) : zero;
-    a[0][1] = ok1 && k0 < P.k ? ldg_stream4(w1 + k0) : zero;
-    a[1][0] = ok0 && k1 < P.k ? ldg_stream4(w0 + k1) : zero;
-    a[1][1] = ok1 && k1 < P.k ? ldg_stream4(w1 + k1) : zero;
+    x[0][0] = ok0 && k0 < P.k ? ldg_stream4(w0 + k0) : zero;
+    x[0][1] = ok1 && k0 < P.k ? ldg_stream4(w1 + k0) : zero;
+    x[1][0] = ok0 && k1 < P.k ? ldg_stream4(w0 + k1) : zero;
+    x[1][1] = ok1 && k1 < P.k ? ldg_stream4(w1 + k1) : zero;
+  };
+  auto step = [&](const uint4 (&x)[2][2], int kb) {
+    const int k0 = kb * 128 + q * 16, k1 = k0 + 64;
     const float fb = e8m0_f(sb[kb]);
 #pragma unroll
     for (int j = 0; j < NT; j++) {
       const int r = 8 * j + g;
-      const uint8_t *x = P.a + (size_t)r * P.lda;
-      const uint4 b0 = r < P.t && k0 < P.k ? *reinterpret_cast<const uint4 *>(x + k0) : zero;
-      const uint4 b1 = r < P.t && k1 < P.k ? *reinterpret_cast<const uint4 *>(x + k1) : zero;
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_e4m3(d, a[0][0].x, a[0][1].x, a[0][0].y, a[0][1].y, b0.x, b0.y);
-      mma_e4m3(d, a[0][0].z, a[0][1].z, a[0][0].w, a[0][1].w, b0.z, b0.w);
-      mma_e4m3(d, a[1][0].x, a[1][1].x, a[1][0].y, a[1][1].y, b1.x, b1.y);
-      mma_e4m3(d, a[1][0].z, a[1][1].z, a[1][0].w, a[1][1].w, b1.z, b1.w);
+      const uint8_t *xr = P.a + (size_t)r * P.lda;
+      const uint4 b0 = r < P.t && k0 < P.k ? *reinterpret_cast<const uint4 *>(xr + k0) : zero;
+      const uint4 b1 = r < P.t && k1 < P.k ? *reinterpret_cast<const uint4 *>(xr + k1) : zero;
       const int c = 8 * j + 2 * q;
       const float s0 = c < P.t ? e8m0_f(P.sa[(size_t)c * P.lds + kb]) : 0.f;
       const float s1 = c + 1 < P.t ? e8m0_f(P.sa[(size_t)(c + 1) * P.lds + kb]) : 0.f;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_e4m3(d, x[0][0].x, x[0][1].x, x[0][0].y, x[0][1].y, b0.x, b0.y);
+      mma_e4m3(d, x[0][0].z, x[0][1].z, x[0][0].w, x[0][1].w, b0.z, b0.w);
+      mma_e4m3(d, x[1][0].x, x[1][1].x, x[1][0].y, x[1][1].y, b1.x, b1.y);
+      mma_e4m3(d, x[1][0].z, x[1][1].z, x[1][0].w, x[1][1].w, b1.z, b1.w);
       acc[j][0] += d[0] * s0 * fb;
       acc[j][1] += d[1] * s1 * fb;
       acc[j][2] += d[2] * s0 * fb;
       acc[j][3] += d[3] * s1 * fb;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 2; i++)
+    if (warp + i * kSmWarps < P.nk) load(a[i], warp + i * kSmWarps);
+  for (int kb = warp; kb < P.nk; kb += 2 * kSmWarps) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int k1 = kb + i * kSmWarps, k2 = k1 + 2 * kSmWarps;
+      if (k1 < P.nk) {
+        step(a[i], k1);
+        if (k2 < P.nk) load(a[i], k2);
+      }
     }
   }
 #pragma unroll
@@ -652,8 +661,21 @@ cudaError_t launch_tc_form(Mm8P p, int n_sms, bool pdl, cudaStream_t st) {
   const bool pairs = use_pairs(p, KIND);
   p.wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ldo * (KIND == kOutF32 ? 4 : 2))) & 15) == 0;
   p.wmax = pairs ? TcLay<MB, 2>::N : TcLay<MB, 1>::N;
-  // no more CTAs than tiles (grouped: the bound of one partial tile a group)
   const int cg = pairs ? 2 : 1;
+  if (!p.offs) {
+    // dense: the tile width with the least (rounds of tiles) x (width + what
+    // a tile costs whatever its width, some 48 columns' worth).  333 x 1000 x
+    // 2000: 32 columns instead of 192 keep 44 pairs busy instead of 8
+    const int64_t nmp = (weight_tiles(p, KIND) + cg - 1) / cg;
+    int64_t best = INT64_MAX;
+    int pick = p.wmax;
+    for (int w = p.wmax; w >= 16 * cg; w -= 16 * cg) {
+      const int64_t rounds = ((p.t + w - 1) / w * nmp + n_sms / cg - 1) / (n_sms / cg), cost = rounds * (w + 48);
+      if (cost < best) best = cost, pick = w;
+    }
+    p.wmax = pick;
+  }
+  // no more CTAs than tiles (grouped: the bound of one partial tile a group)
   const int64_t tt = (p.t + p.wmax - 1) / p.wmax + (p.offs ? p.G : 0);
   const int64_t tiles = tt * ((weight_tiles(p, KIND) + cg - 1) / cg);
   const int grid = (int)(tiles < n_sms / cg ? tiles : n_sms / cg) * cg;

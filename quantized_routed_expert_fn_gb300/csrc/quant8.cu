@@ -56,29 +56,40 @@ __device__ __forceinline__ void store8(uint8_t *q, int n, const float (&v)[8], f
   }
 }
 
-// Half a warp per row block of 128, eight values a lane.
+// Half a warp per row block of 128, eight values a lane; U blocks' loads are
+// in flight before the first is used (one block at a time left HBM at a
+// third of its rate).  A thread block takes 16 * U consecutive blocks.
+constexpr int kRowBlocks = 4;
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows(const __grid_constant__ Quant8P P) {
-  const int cb = (P.cols + 127) / 128, sub = threadIdx.x & 15;
-  const int64_t blocks = (int64_t)P.rows * cb, stride = (int64_t)gridDim.x * 16;
+  const int cb = (P.cols + 127) / 128, sub = threadIdx.x & 15, half = threadIdx.x >> 4;
+  const int64_t blocks = (int64_t)P.rows * cb, stride = (int64_t)gridDim.x * (16 * kRowBlocks);
   // every lane of a warp takes part in the exchange below: the loop bound is
-  // the same for both halves, the second half's work is masked
-  for (int64_t i0 = (int64_t)blockIdx.x * 16 + ((threadIdx.x >> 5) << 1); i0 < blocks; i0 += stride) {
-    const int64_t i = i0 + ((threadIdx.x >> 4) & 1);
-    const bool on = i < blocks;
-    const int64_t row = on ? i / cb : 0;
-    const int b = on ? (int)(i - row * cb) : 0, c = b * 128 + sub * 8;
-    const int n = on ? min(8, P.cols - c) : 0;
-    float v[8];
-    load8<BF16, VEC>(P.x, row * P.ldx + c, n, v);
-    uint32_t a = 0;
+  // the same for all, what lies past the end is masked
+  for (int64_t i0 = (int64_t)blockIdx.x * (16 * kRowBlocks); i0 < blocks; i0 += stride) {
+    int64_t row[kRowBlocks];
+    int b[kRowBlocks], n[kRowBlocks];
+    float v[kRowBlocks][8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) a = max(a, mag_bits(v[j]));
+    for (int u = 0; u < kRowBlocks; u++) {
+      const int64_t i = i0 + 16 * u + half;
+      const bool on = i < blocks;
+      row[u] = on ? (blocks < (1ll << 31) ? (int64_t)((uint32_t)i / (uint32_t)cb) : i / cb) : 0;
+      b[u] = on ? (int)(i - row[u] * cb) : 0;
+      n[u] = on ? min(8, P.cols - b[u] * 128 - sub * 8) : 0;
+      load8<BF16, VEC>(P.x, row[u] * P.ldx + b[u] * 128 + sub * 8, n[u], v[u]);
+    }
 #pragma unroll
-    for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(FULLM, a, o));
-    const uint32_t e = e8m0_of_amax(a);
-    store8<VEC>(P.q + row * P.ldq + c, n, v, e8m0_inv(e));
-    if (on && sub == 0) P.s[row * P.lds + b] = (uint8_t)e;
+    for (int u = 0; u < kRowBlocks; u++) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 8; j++) a = max(a, mag_bits(v[u][j]));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(FULLM, a, o));
+      const uint32_t e = e8m0_of_amax(a);
+      store8<VEC>(P.q + row[u] * P.ldq + b[u] * 128 + sub * 8, n[u], v[u], e8m0_inv(e));
+      if (i0 + 16 * u + half < blocks && sub == 0) P.s[row[u] * P.lds + b[u]] = (uint8_t)e;
+    }
   }
 }
 
@@ -124,7 +135,7 @@ bool vec_ok(const Quant8P &p) {
 
 cudaError_t launch_quant8_rows(const Quant8P &p, int n_sms, cudaStream_t st) {
   const int64_t blocks = (int64_t)p.rows * ((p.cols + 127) / 128);
-  const int64_t need = (blocks + 15) / 16, cap = (int64_t)n_sms * 8;
+  const int64_t need = (blocks + 16 * kRowBlocks - 1) / (16 * kRowBlocks), cap = (int64_t)n_sms * 16;
   const unsigned grid = (unsigned)(need < cap ? need : cap);
   const bool v = vec_ok(p);
   if (p.bf16) {

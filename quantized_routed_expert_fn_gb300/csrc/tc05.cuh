@@ -289,6 +289,11 @@ __device__ __forceinline__ void named_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// arrive on a named barrier without waiting
+__device__ __forceinline__ void named_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // named barrier that also ANDs a predicate over its `count` threads
 __device__ __forceinline__ bool named_and(int id, int count, bool pred) {
   uint32_t r;

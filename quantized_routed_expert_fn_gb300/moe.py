@@ -321,37 +321,55 @@ def _bad(code: int, msg: str):
     raise MoeError(code, msg)
 
 
-def _arg(t, name: str, shape: tuple, dtypes, dev=None) -> int:
+def _arg(t, name: str, shape: tuple, dtypes, dev: int) -> int:
     """Address of a CUDA tensor after checking type, shape, device and that its
     last dimension is contiguous (the strides of the others are the caller's)."""
     if t.dtype not in dtypes:
         _bad(EINVAL, f"{name} is {t.dtype}")
     if t.shape != shape:
         _bad(ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != dev:
-        _bad(EINVAL, f"{name} is on {t.device}, expected {dev}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+    if t.get_device() != dev:
+        _bad(EINVAL, f"{name} is on {t.device}, expected cuda:{dev}")
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         _bad(EINVAL, f"{name}'s last dimension is not contiguous")
     return t.data_ptr()
 
 
-def _whole(t, name: str, shape: tuple, dtypes, dev) -> int:
-    p = _arg(t, name, shape, dtypes, dev)
+def _whole(t, name: str, shape: tuple, dtypes, dev: int) -> int:
+    if t.dtype not in dtypes:
+        _bad(EINVAL, f"{name} is {t.dtype}")
+    if t.shape != shape:
+        _bad(ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        _bad(EINVAL, f"{name} is on {t.device}, expected cuda:{dev}")
     if not t.is_contiguous():
         _bad(EINVAL, f"{name} is not contiguous")
-    return p
+    return t.data_ptr()
 
 
-def _device(t, name: str) -> torch.device:
+def _device(t, name: str) -> int:
     """The call's device: the current one, where the stream and every tensor have to be."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         _bad(EINVAL, f"{name} is on {t.device}, not on the current CUDA device")
-    return t.device
+    return dev
+
+
+# The current stream's handle without a torch.cuda.Stream object around it
+# (the object costs as much as a small call), where torch has that call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _ld(t) -> int:
     """Row stride; of a single row, whose stride means nothing, its length."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    s, n = t.stride(0), t.shape[1]
+    return s if s > n or t.shape[0] > 1 else n
 
 
 @functools.lru_cache(maxsize=64)
@@ -376,7 +394,7 @@ def gate(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, bia
     wp = _whole(topk_w, "topk_w", (t, k), _F32, dev)
     bp = None if bias is None else _whole(bias, "bias", (e,), _F32, dev)
     cfg = _gate_cfg(e, k, score, n_groups, top_groups, group_top, GATE_RENORM if renorm else 0, scale)
-    _check(lib().moe_gate(cfg, lp, _FLOATS[logits.dtype], _ld(logits), bp, t, ip, wp, _stream(stream)))
+    _check((_lib or lib()).moe_gate(cfg, lp, _FLOATS[logits.dtype], _ld(logits), bp, t, ip, wp, _stream_on(stream, dev)))
 
 
 def quant8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 1, stream=None) -> None:
@@ -389,8 +407,8 @@ def quant8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 
     xp = _arg(x, "x", (rows, cols), _FLOATS, dev)
     qp = _arg(q, "q", (rows, cols), _E4M3, dev)
     sp = _arg(s, "s", (-(-rows // block_rows), -(-cols // 128)), _E8M0, dev)
-    _check(lib().moe_quant8(xp, _FLOATS[x.dtype], _ld(x), rows, cols, block_rows, qp, _ld(q), sp, _ld(s),
-                            _stream(stream)))
+    _check((_lib or lib()).moe_quant8(xp, _FLOATS[x.dtype], _ld(x), rows, cols, block_rows, qp, _ld(q), sp, _ld(s),
+                                      _stream_on(stream, dev)))
 
 
 def mm8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, out: torch.Tensor, status: torch.Tensor,
@@ -414,10 +432,11 @@ def mm8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, ou
     lds = sa.stride(0)
     if t == 1 and lds % 4:  # one row: only what it holds can be read
         lds = -(-lds // 4) * 4
-    if t and sa.untyped_storage().nbytes() < sa.storage_offset() + t * lds:
-        _bad(EINVAL, "sa's last row is not held whole")
-    _check(lib().moe_mm8(ap, _ld(a), sap, lds, t, bp, sbp, n, k, op, _FLOATS[out.dtype], _ld(out), fp, groups, flags,
-                         _whole(status, "status", (1,), _I32, dev), _stream(stream)))
+    if t and not (lds == sa.shape[1] and sa.is_contiguous()):
+        if sa.untyped_storage().nbytes() < sa.storage_offset() + t * lds:
+            _bad(EINVAL, "sa's last row is not held whole")
+    _check((_lib or lib()).moe_mm8(ap, _ld(a), sap, lds, t, bp, sbp, n, k, op, _FLOATS[out.dtype], _ld(out), fp, groups,
+                                   flags, _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
 
 
 class Layer8:
@@ -452,12 +471,13 @@ def experts8(layer: Layer8, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: tor
     dev = _device(x, "x")
     shape = (t, layer.hidden)
     wp, wb = _aligned(work)
-    if layer.device != dev or work.device != dev:
-        _bad(EINVAL, f"layer on {layer.device}, work on {work.device}, x on {dev}")
-    _check(lib().moe_experts8(layer.c, _whole(x, "x", shape, _FLOATS, dev), _FLOATS[x.dtype], t,
-                              _whole(topk_idx, "topk_idx", (t, k), _I32, dev), _whole(topk_w, "topk_w", (t, k), _F32, dev), k,
-                              _whole(out, "out", shape, _FLOATS, dev), _FLOATS[out.dtype], wp, wb,
-                              _whole(status, "status", (1,), _I32, dev), _stream(stream)))
+    if layer.device != dev or work.get_device() != dev:
+        _bad(EINVAL, f"layer on cuda:{layer.device}, work on {work.device}, x on cuda:{dev}")
+    _check((_lib or lib()).moe_experts8(layer.c, _whole(x, "x", shape, _FLOATS, dev), _FLOATS[x.dtype], t,
+                                        _whole(topk_idx, "topk_idx", (t, k), _I32, dev),
+                                        _whole(topk_w, "topk_w", (t, k), _F32, dev), k,
+                                        _whole(out, "out", shape, _FLOATS, dev), _FLOATS[out.dtype], wp, wb,
+                                        _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
 
 
 class Tier:

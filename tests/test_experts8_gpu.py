@@ -123,11 +123,11 @@ def test_gate_special_rows(moe, o):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("groups", [1, 4])
-def test_gate_scores_a_last_place_apart(moe, score, groups):
+@pytest.mark.parametrize("groups,e", [(1, 64), (4, 64), (1, 20), (1, 32), (4, 24)])
+def test_gate_scores_a_last_place_apart(moe, score, groups, e):
     """Logits one 32-bit step apart under a bias: 32-bit scores cannot tell them, the choice has to."""
     g = np.random.default_rng(3)
-    t, e, k = 200, 64, 4
+    t, k = 200, 4
     base = g.normal(size=(t, 1)).astype(np.float32)
     lg = np.repeat(base, e, axis=1)
     steps = g.integers(-3, 4, size=(t, e))
@@ -135,6 +135,7 @@ def test_gate_scores_a_last_place_apart(moe, score, groups):
         lg = np.where(steps > 0, np.nextafter(lg, np.float32(np.inf)), np.where(steps < 0, np.nextafter(lg, np.float32(-np.inf)), lg))
         steps = steps - np.sign(steps)
     bias = cuda(np.zeros(e, np.float32))
+    lg[::3, : e // 2] -= 1  # half of the experts out of reach
     check_gate(moe, cuda(lg), k, bias, score=score, n_groups=groups, top_groups=1 if groups == 1 else 2, group_top=2, renorm=True)
 
 
@@ -389,7 +390,8 @@ EX = [  # t, H, I, E, k, x type, out type
     (1, 128, 128, 1, 1, "f32", "f32"), (1, 256, 128, 8, 2, "f32", "bf16"), (1, 2048, 768, 16, 8, "bf16", "bf16"),
     (3, 384, 256, 5, 5, "f32", "f32"), (4, 1024, 512, 40, 10, "f32", "bf16"), (8, 256, 384, 12, 4, "bf16", "f32"),
     (9, 256, 128, 8, 2, "f32", "f32"), (12, 384, 256, 64, 3, "f32", "bf16"), (40, 256, 256, 3, 2, "bf16", "bf16"),
-    (150, 128, 128, 2, 1, "f32", "f32"),
+    (150, 128, 128, 2, 1, "f32", "f32"), (2, 1152, 1152, 6, 2, "f32", "f32"), (8, 640, 128, 20, 8, "bf16", "bf16"),
+    (7, 1408, 896, 9, 3, "f32", "bf16"), (8, 128, 512, 64, 32, "f32", "f32"),
 ]
 
 
@@ -454,6 +456,29 @@ def test_experts8_nan_row_stays_alone(moe, t):
     assert np.isnan(got[2]).all() and np.isnan(got[3]).all()
     rest = [r for r in range(t) if r not in (2, 3)]
     assert np.array_equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("t", [4, 40])
+def test_experts8_nan_weights_stay_in_their_channels(moe, t):
+    """A NaN weight of one expert: the rows that chose it become NaN (its channel's h is), a NaN in its down rows only
+    that output; rows that did not choose it are as they were."""
+    g = np.random.default_rng(t + 1)
+    gu, gus, dn, dns = make_experts(g, 6, 256, 128)
+    x = cuda(g.normal(size=(t, 256)).astype(np.float32))
+    idx = np.stack([g.choice(5, size=2, replace=False) for _ in range(t)])
+    idx[::2, 1] = 5
+    w = g.random(size=(t, 2)).astype(np.float32) + 0.1
+    clean = run_experts(moe, (gu, gus, dn, dns), x, idx, w)
+    dn2 = dn.copy()
+    dn2[5, 77, 100] = 0xFF
+    got = run_experts(moe, (gu, gus, dn2, dns), x, idx, w)
+    want = np.zeros(got.shape, bool)
+    want[::2, 77] = True
+    assert np.array_equal(np.isnan(got), want) and np.array_equal(got[~want], clean[~want])
+    gu2 = gu.copy()
+    gu2[5, 130, 3] = 0x7F
+    got = run_experts(moe, (gu2, gus, dn, dns), x, idx, w)
+    assert np.isnan(got[::2]).all() and np.array_equal(got[1::2], clean[1::2])
 
 
 @pytest.mark.parametrize("t", [4, 300])
