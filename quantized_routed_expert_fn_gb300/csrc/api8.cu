@@ -154,15 +154,18 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
   p.status = dev_status;
   p.timeout_ns = moe::timeout_ns();
   const int kind = out_dtype == MOE_F32 ? moe::kOutF32 : moe::kOutBf16;
-  if (t > 0 && !offs && t <= moe::kMm8SmallRows && !p.withhold) {
+  if (t > 0 && !offs && moe::mm8_small(t, n, k) && !p.withhold) {
     e = moe::launch_mm8_small(p, kind, st);
   } else {
-    e = cudaMemsetAsync(dev_status, 0, 4, st);
-    if (e == cudaSuccess && t > 0) {
+    e = cudaSuccess;
+    p.zero_status = 1;
+    // a wait may give up no sooner than the status is zeroed
+    if (p.timeout_ns < 1000000) p.timeout_ns = 1000000;
+    if (t == 0) {
+      e = cudaMemsetAsync(dev_status, 0, 4, st);
+    } else {
       int n_sms = 0;
-      const char *why = "";
       if (int r = sm_count(&n_sms)) return r;
-      if (moe::mm8_tensor_maps(p, kind, &why) != 0) return fail(MOE_ECUDA, "%s", why);
       e = moe::launch_mm8_tc(p, kind, n_sms, false, st);
     }
   }
@@ -242,15 +245,11 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   d.a = p.h8, d.lda = I, d.sa = p.h8s, d.lds = p.ldi, d.b = p.dn, d.sb = p.dns;
   d.n = H, d.k = I, d.nk = I / 128, d.nb = H / 128;
   d.out = p.y, d.ldo = H, d.hs = nullptr;
-  const char *why = "";
   const int yk = p.out_bf16 ? moe::kOutBf16 : moe::kOutF32;
-  if (moe::mm8_tensor_maps(u, moe::kOutSilu8, &why) != 0 || moe::mm8_tensor_maps(d, yk, &why) != 0)
-    return fail(MOE_ECUDA, "%s", why);
-  e = cudaMemsetAsync(dev_status, 0, 4, st);
-  if (e == cudaSuccess) e = moe::launch_ex8_group(p, n_sms, st);
+  e = moe::launch_ex8_group(p, n_sms, st);
   if (e == cudaSuccess) e = moe::launch_mm8_tc(u, moe::kOutSilu8, n_sms, false, st);
   if (e == cudaSuccess) e = moe::launch_mm8_tc(d, yk, n_sms, true, st);
-  if (e == cudaSuccess) e = moe::launch_ex8_combine(p, st);
+  if (e == cudaSuccess) e = moe::launch_ex8_combine(p, n_sms, st);
   if (e != cudaSuccess) return fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return MOE_OK;
 }

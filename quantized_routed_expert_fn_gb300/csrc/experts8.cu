@@ -89,14 +89,9 @@ __device__ __forceinline__ void load_x8(const void *x, int64_t i, float (&v)[8])
 
 // Half a warp: the 128 values its lanes hold eight each of -> e4m3, scale byte
 __device__ __forceinline__ uint2 quant128(const float (&v)[8], uint32_t &e) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int j = 0; j < 8; j++) a = max(a, mag_bits(v[j]));
-#pragma unroll
-  for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(FULLM, a, o));
-  e = e8m0_of_amax(a);
-  const float f = e8m0_inv(e);
-  return make_uint2(e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f), e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+  uint32_t w[2];
+  quant_block<8>(v, w, e);
+  return make_uint2(w[0], w[1]);
 }
 
 // ------------------------------------------------------------ few rows
@@ -491,6 +486,7 @@ __global__ void __launch_bounds__(256) ex8_count(const __grid_constant__ Ex8P P)
   extern __shared__ int hist[];  // [E]
   __shared__ int last, part[9];
   const int tid = threadIdx.x, lane = tid & 31, n = P.t * P.K, E = P.E;
+  if (blockIdx.x == 0 && tid == 0) *P.status = 0;
   for (int e = tid; e < E; e += 256) hist[e] = 0;
   __syncthreads();
   uint32_t ex[4];
@@ -545,59 +541,77 @@ __global__ void __launch_bounds__(256) ex8_count(const __grid_constant__ Ex8P P)
   if (E == 1024 && tid == 255) P.offs[E] = base;
 }
 
-// x rows -> e4m3, written to the places of their entries: a warp per row.
+// x rows -> e4m3, written to the places of their entries: a warp per row,
+// 16 values a lane (eight lanes a block), 16-byte stores.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) ex8_scatter(const __grid_constant__ Ex8P P) {
   const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= P.t) return;
   const int K = P.K, H = P.H;
+  float v[2][16];
+  auto load = [&](float (&x)[16], int c) {
+#pragma unroll
+    for (int j = 0; j < 16; j++) x[j] = 0.f;
+    if (c < H) {
+      float lo[8], hi[8];
+      load_x8<BF16>(P.x, (int64_t)row * H + c, lo);
+      load_x8<BF16>(P.x, (int64_t)row * H + c + 8, hi);
+#pragma unroll
+      for (int j = 0; j < 8; j++) x[j] = lo[j], x[8 + j] = hi[j];
+    }
+  };
+  load(v[0], lane * 16);
   int at = -1;
   if (lane < K) {
     const int j = row * K + lane, pl = P.place[j];
     if (pl >= 0) at = P.offs[P.idx[j]] + pl;
     P.place[j] = at;  // from here on: the entry's row
   }
-  for (int c0 = 0; c0 < H; c0 += 256) {
-    const int c = c0 + lane * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < H) load_x8<BF16>(P.x, (int64_t)row * H + c, v);
-    uint32_t e;
-    const uint2 u = quant128(v, e);
-    for (int j = 0; j < K; j++) {
-      const int a = __shfl_sync(FULLM, at, j);
-      if (a >= 0 && c < H) {
-        *reinterpret_cast<uint2 *>(P.x8 + (size_t)a * H + c) = u;
-        if ((lane & 15) == 0) P.x8s[(size_t)a * P.ldh + c / 128] = (uint8_t)e;
+  for (int c0 = 0; c0 < H; c0 += 1024) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int c = c0 + 512 * i + lane * 16;
+      load(v[i ^ 1], c + 512);
+      uint32_t w[4], e;
+      quant_block<16>(v[i], w, e);
+      for (int j = 0; j < K; j++) {
+        const int to = __shfl_sync(FULLM, at, j);
+        if (to >= 0 && c < H) {
+          *reinterpret_cast<uint4 *>(P.x8 + (size_t)to * H + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          if ((lane & 7) == 0) P.x8s[(size_t)to * P.ldh + c / 128] = (uint8_t)e;
+        }
       }
     }
   }
 }
 
-// out[row] = sum over the row's entries, in order, of weight * y
+// out[row] = sum over the row's entries, in order, of weight * y: a warp per
+// row and 256 columns, eight a lane.
 template <bool BF16>
 __global__ void __launch_bounds__(256) ex8_combine(const __grid_constant__ Ex8P P) {
-  __shared__ int at[32];
-  __shared__ float wt[32];
   pdl_wait_prev();
-  const int row = blockIdx.x, K = P.K, H = P.H;
-  if (threadIdx.x < K) {
-    at[threadIdx.x] = P.place[row * K + threadIdx.x];
-    wt[threadIdx.x] = P.w[row * K + threadIdx.x];
-  }
-  __syncthreads();
-  for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
+  const int lane = threadIdx.x & 31, K = P.K, H = P.H, segs = (H + 255) / 256;
+  const int64_t total = (int64_t)P.t * segs, step = (int64_t)gridDim.x * 8;
+  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += step) {
+    const int row = (int)(i / segs), c = (int)(i - (int64_t)row * segs) * 256 + lane * 8;
+    const int at = lane < K ? P.place[(size_t)row * K + lane] : -1;
+    const float wt = lane < K ? P.w[(size_t)row * K + lane] : 0.f;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
     for (int j = 0; j < K; j++) {
-      if (at[j] < 0) continue;
+      const int a = __shfl_sync(FULLM, at, j);
+      const float w = __shfl_sync(FULLM, wt, j);
+      if (a < 0 || c >= H) continue;
       float v[8];
-      load_x8<BF16>(P.y, (int64_t)at[j] * H + c, v);
+      load_x8<BF16>(P.y, (int64_t)a * H + c, v);
 #pragma unroll
-      for (int i = 0; i < 8; i++) s[i] += wt[j] * v[i];
+      for (int k = 0; k < 8; k++) s[k] += w * v[k];
     }
+    if (c >= H) continue;
     if (BF16) {
       uint32_t u[4];
 #pragma unroll
-      for (int i = 0; i < 4; i++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(s[2 * i + 1]), "f"(s[2 * i]));
+      for (int k = 0; k < 4; k++) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[k]) : "f"(s[2 * k + 1]), "f"(s[2 * k]));
       *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(P.out) + (size_t)row * H + c) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
       float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(P.out) + (size_t)row * H + c);
@@ -673,8 +687,10 @@ cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_ex8_combine(const Ex8P &p, cudaStream_t st) {
-  return launch_pdl(p.out_bf16 ? ex8_combine<true> : ex8_combine<false>, dim3((unsigned)p.t), 256, 0, st, p);
+cudaError_t launch_ex8_combine(const Ex8P &p, int n_sms, cudaStream_t st) {
+  const int64_t need = ((int64_t)p.t * ((p.H + 255) / 256) + 7) / 8, cap = (int64_t)n_sms * 8;
+  return launch_pdl(p.out_bf16 ? ex8_combine<true> : ex8_combine<false>, dim3((unsigned)(need < cap ? need : cap)), 256, 0,
+                    st, p);
 }
 
 }  // namespace moe

@@ -42,9 +42,9 @@ cudaError_t launch_quant8_blocks(const Quant8P &p, cudaStream_t st);
 
 // ---- products (mm8.cu)
 struct Mm8P {
-  // tokens: boxes of 128 bytes x a full tile's, 64, 32 and 16 rows; weights [G * n][k]:
-  // 128 bytes x 128 rows; 128B swizzle
-  CUtensorMap tm_a[4], tm_b;
+  // tokens: boxes of 1, 2, ... times 16 (or 32) rows; weights [G * n][k]:
+  // boxes of 128 rows; 128 bytes of k a block, 128B swizzle
+  CUtensorMap tm_a[7], tm_b;
   const uint8_t *a, *sa, *b, *sb;
   int64_t lda, lds;
   int t, n, k, nk, nb;  // nk = ceil(k / 128), nb = ceil(n / 128)
@@ -56,14 +56,22 @@ struct Mm8P {
   int64_t ldhs;
   int wmax;             // token rows of a tile at most
   int wide;             // rows of out start on 16 bytes
+  int tok, stage, stages;  // ring: token bytes a k block, bytes a stage, stages
   int withhold;
+  int zero_status;      // the kernel zeroes *status first
   int *status;
   unsigned long long timeout_ns;
 };
 enum { kOutF32 = 0, kOutBf16 = 1, kOutSilu8 = 2 };
-// rows the few-row kernel takes (weights streamed once, mma.sync)
-constexpr int kMm8SmallRows = 32;
-int mm8_tensor_maps(Mm8P &p, int out_kind, const char **why);
+// Whether the few-row kernel (weights streamed once into mma.sync) takes t
+// rows: its MMAs are slow, so the larger the weights and the more its groups
+// of eight rows, the sooner the tensor-core kernel, which starts slower, wins.
+// us at n x k, few-row / tensor-core: 16 rows 2048 x 2048 3.9 / 7.3, 8192 x
+// 2048 8.4 / 8.5, 16384 x 4096 23.7 / 15.9; 32 rows 5.4 / 7.4, 16.4 / 8.7,
+// 49.9 / 16.0; 8 rows 16384 x 4096 17.0 / 16.1.
+inline bool mm8_small(int64_t t, int64_t n, int64_t k) {
+  return t <= 8 || (t <= 16 && n * k <= 1 << 24) || (t <= 32 && n * k <= 1 << 23);
+}
 cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st);
 cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st);
 
@@ -96,14 +104,48 @@ __device__ __forceinline__ uint32_t mag_bits(float v) {
   return u < 0x7f800000u ? u : 0u;
 }
 
-// two values, scaled, to two e4m3 bytes (nearest, ties to even; infinities
-// and NaN to NaN: an infinity times 0 is the NaN the conversion keeps)
+// two values, scaled, to two e4m3 bytes (nearest, ties to even); SAFE:
+// infinities become NaN (an infinity times 0 is the NaN the conversion keeps)
+template <bool SAFE>
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
-  const float l = lo + 0.f * lo, h = hi + 0.f * hi;
+  const float l = SAFE ? lo + 0.f * lo : lo, h = SAFE ? hi + 0.f * hi : hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(h), "f"(l));
   return r;
 }
+template <bool SAFE>
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2<SAFE>(a, b) | e4m3x2<SAFE>(c, d) << 16;
+}
+
+// Warp: the 128 values of a scale block, N in each of 128 / N neighbouring
+// lanes, to e4m3 words; e: the scale byte.  Values that are not finite are
+// rare: a maximum that says one is there makes the warp do it with care.
+template <int N>
+__device__ __forceinline__ void quant_block(const float (&v)[N], uint32_t (&w)[N / 4], uint32_t &e) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < N; j++) a = max(a, __float_as_uint(v[j]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 64 / N; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if (__any_sync(0xffffffffu, a >= 0x7f800000u)) {
+    a = 0;
+#pragma unroll
+    for (int j = 0; j < N; j++) a = max(a, mag_bits(v[j]));
+#pragma unroll
+    for (int o = 64 / N; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    e = e8m0_of_amax(a);
+    const float f = e8m0_inv(e);
+#pragma unroll
+    for (int j = 0; j < N / 4; j++) w[j] = e4m3x4<true>(v[4 * j] * f, v[4 * j + 1] * f, v[4 * j + 2] * f, v[4 * j + 3] * f);
+    return;
+  }
+  e = e8m0_of_amax(a);
+  const float f = e8m0_inv(e);
+#pragma unroll
+  for (int j = 0; j < N / 4; j++) w[j] = e4m3x4<false>(v[4 * j] * f, v[4 * j + 1] * f, v[4 * j + 2] * f, v[4 * j + 3] * f);
+}
+
 // D(16x8 f32) += A(16x32 e4m3, row) * B(32x8 e4m3, col)
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -111,9 +153,6 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return e4m3x2(a, b) | e4m3x2(c, d) << 16;
 }
 
 #endif
@@ -151,6 +190,6 @@ bool ex8_small(int H, int I, int t, int K);
 Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size);
 cudaError_t launch_ex8_small(const Ex8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st);
-cudaError_t launch_ex8_combine(const Ex8P &p, cudaStream_t st);
+cudaError_t launch_ex8_combine(const Ex8P &p, int n_sms, cudaStream_t st);
 
 }  // namespace moe

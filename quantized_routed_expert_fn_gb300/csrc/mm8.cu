@@ -2,7 +2,7 @@
 // kb of 128 k of 2^(sa[r][kb] + sb[j / 128][kb] - 254) * (a[r] . b[j] in kb).
 //
 // Two kernels:
-//   small  up to kMm8SmallRows rows: the weights are streamed once from HBM
+//   small  up to 32 rows: the weights are streamed once from HBM
 //          straight into the fragments of mma.sync (no shared memory), the
 //          few rows come from L1; a CTA takes 16 weight rows and splits k
 //          over its warps.
@@ -146,7 +146,9 @@ __global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant
 //             accumulators while the MMAs fill the other
 //   warp 8    (even CTA) issues a stage's MMAs once its operands are there
 //   warp 9    TMA: 128 weight rows x 128 k a block, the CTA's share of the token rows
-// A stage is one k block.  A scale word holds the bytes of four consecutive
+// A stage is KB k blocks (one, or two where k allows: half as many copies,
+// twice as long), as many stages as fit for the launch's tile width.  A scale
+// word holds the bytes of four consecutive
 // blocks, as they stand in memory; the MMAs of block kb name byte kb % 4, so
 // scales are written once in four blocks, into one of four slots of TMEM
 // columns with barriers of their own.  The full, scale and acc_empty
@@ -157,9 +159,10 @@ __global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant
 // x 2048.)  The others are each CTA's own, committed to both.
 constexpr int kTcThreads = 320;
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxStages = 12;
 
 struct TcBars {
-  uint64_t full[6], empty[6], sc_full[4], sc_empty[4], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], sc_full[4], sc_empty[4], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   int bad;
 };
@@ -171,17 +174,13 @@ struct TcLay {
   static constexpr int accCols = MB * N;                         // of each of two buffers
   static constexpr int scaleCol = 2 * accCols;                   // then four slots of 12 scale columns
   static_assert(scaleCol + 12 * 4 <= 512, "tensor memory");
-  static constexpr int stages = CG == 1 ? 4 : (MB == 1 ? 6 : 5);
-  static constexpr int tok = N / CG * 128;                       // this CTA's token rows
-  static constexpr int offW = (tok + 1023) / 1024 * 1024;        // weights: MB x 16 KB
-  static constexpr int stage = offW + MB * 16384;
-  static constexpr int offEpi = stages * stage;  // silu: h bytes [N][128], maxima [4][N]; else 32 x 32 values a warp
+  static constexpr int unit = 16 * CG == 32 ? 16 : 32;           // token boxes: multiples of this many rows
+  // front: silu: h bytes [N][128], maxima [4][N]; else 32 x 32 values a warp
   static constexpr int epi = MB == 2 ? N * 128 + 4 * N * 4 : 4 * 4096;
-  static constexpr int offTab = (offEpi + epi + 15) & ~15;       // int [G + 1] first row, [G + 1] first token tile
+  static constexpr int offTab = (epi + 15) & ~15;                // int [G + 1] first row, [G + 1] first token tile
   static constexpr int offBars = (offTab + 2 * (kMaxGroups + 1) * 4 + 15) & ~15;
-  static constexpr int smem = offBars + (int)sizeof(TcBars) + 1024;
-  static_assert(stage % 1024 == 0, "swizzled stages");
-  static_assert(smem <= 227 * 1024, "shared memory");
+  static constexpr int offRing = (offBars + (int)sizeof(TcBars) + 1023) / 1024 * 1024;
+  static constexpr int room = 226 * 1024 - offRing;              // for the ring, the base rounded up
 };
 
 struct Tile {
@@ -208,14 +207,15 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t par, const 
   return __shfl_sync(FULLM, ok ? 1 : 0, 0) != 0;
 }
 
-template <int MB, int KIND, int CG>
+template <int MB, int KIND, int CG, int KB>
 __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ Mm8P P) {
   pdl_launch_next();
   extern __shared__ __align__(1024) uint8_t smraw[];
   // the same offset in both CTAs of a pair: dynamic shared memory starts alike
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~(uintptr_t)1023);
   using LY = TcLay<MB, CG>;
-  constexpr int S = LY::stages;
+  const int S = P.stages;
+  uint8_t *ring = sm + LY::offRing;
   TcBars &B = *reinterpret_cast<TcBars *>(sm + LY::offBars);
   int *s_off = reinterpret_cast<int *>(sm + LY::offTab), *s_tile = s_off + kMaxGroups + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -274,12 +274,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       }
       if (lane == 0) s_tile[G] = base;
     }
-    if (B.bad && tid == 0) atomicCAS(P.status, 0, kStatusDevice);
   } else if (tid == 0) {
     s_off[0] = 0, s_off[1] = P.t;
     s_tile[0] = 0, s_tile[1] = (P.t + P.wmax - 1) / P.wmax;
   }
   __syncthreads();
+  // the status of the call: one CTA's to set (a wait gives up long after)
+  if (tid == 0 && blockIdx.x == 0) {
+    if (P.zero_status) *P.status = B.bad ? kStatusDevice : 0;
+    else if (B.bad) atomicCAS(P.status, 0, kStatusDevice);
+  }
   const int ntiles = s_tile[G] * nmp, cl = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
   const int my_tiles = cl < ntiles ? (ntiles - 1 - cl) / ncl + 1 : 0;
   // tile i: the weight tiles of a token tile follow one another (their token
@@ -319,39 +323,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       bool ok = true;
       Tile Tn;
       if (my_tiles > 0) Tn = tile_of(0);
-      const uint32_t base = smem_u32(sm);
+      const uint32_t base = smem_u32(ring);
       for (int lt = 0; lt < my_tiles && ok; lt++) {
         const Tile T = Tn;
         const int b = lt & 1;
         if (!tc_wait<CG>(&B.acc_empty[b], (uint32_t)(((lt >> 1) & 1) ^ 1), P)) break;
         tc05::fence_after();
         const uint32_t d = tmem + (uint32_t)(b * LY::accCols), idesc = tc05::idesc_mx_e4m3(128 * CG, T.N);
-        for (int kb = 0; kb < nk; kb++) {
-          if (((kb & 3) == 0 && !tc_wait<CG>(&B.sc_full[sl], slp, P)) || !tc_wait<CG>(&B.full[s], ph, P)) {
+        const uint32_t panel = (uint32_t)((T.N / CG + LY::unit - 1) / LY::unit * LY::unit * 128);  // token bytes a block
+        for (int k0 = 0; k0 < nk; k0 += KB) {
+          if (!tc_wait<CG>(&B.full[s], ph, P)) {
             ok = false;
             break;
           }
-          tc05::fence_after();
-          const uint32_t st = base + (uint32_t)(s * LY::stage);
-          const uint32_t sfb = tmem + (uint32_t)(LY::scaleCol + 12 * sl), sfa = sfb + (MB == 1 ? 8 : 4);
-          const uint32_t id = idesc | tc05::idesc_scale_byte(kb & 3);
-          const uint64_t bd = tc05::sdesc(st);
+          const uint32_t st = base + (uint32_t)(s * P.stage);
 #pragma unroll
-          for (int m = 0; m < MB; m++) {
-            const uint64_t ad = tc05::sdesc(st + LY::offW + 16384 * m);
+          for (int kk = 0; kk < KB; kk++) {
+            const int kb = k0 + kk;
+            if ((kb & 3) == 0 && !tc_wait<CG>(&B.sc_full[sl], slp, P)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+            const uint32_t sfb = tmem + (uint32_t)(LY::scaleCol + 12 * sl), sfa = sfb + (MB == 1 ? 8 : 4);
+            const uint32_t id = idesc | tc05::idesc_scale_byte(kb & 3);
+            const uint64_t bd = tc05::sdesc(st + kk * panel);
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-              tc05::mma_mx<CG>(d + (uint32_t)(m * LY::N), ad + 2 * j, bd + 2 * j, id, sfa + 4 * m, sfb, (kb | j) != 0);
+            for (int m = 0; m < MB; m++) {
+              const uint64_t ad = tc05::sdesc(st + (uint32_t)(KB * P.tok) + 16384 * (KB * m + kk));
+#pragma unroll
+              for (int j = 0; j < 4; j++)
+                tc05::mma_mx<CG>(d + (uint32_t)(m * LY::N), ad + 2 * j, bd + 2 * j, id, sfa + 4 * m, sfb, (kb | j) != 0);
+            }
+            if ((kb & 3) == 3 || kb == nk - 1) {
+              if constexpr (CG == 1) tc05::commit(&B.sc_empty[sl]);
+              else tc05::commit_pair(&B.sc_empty[sl]);
+              if (++sl == 4) sl = 0, slp ^= 1;
+            }
           }
+          if (!ok) break;
           if constexpr (CG == 1) tc05::commit(&B.empty[s]);
           else tc05::commit_pair(&B.empty[s]);
           if (++s == S) s = 0, ph ^= 1;
-          if ((kb & 3) == 3 || kb == nk - 1) {
-            if constexpr (CG == 1) tc05::commit(&B.sc_empty[sl]);
-            else tc05::commit_pair(&B.sc_empty[sl]);
-            if (++sl == 4) sl = 0, slp ^= 1;
-          }
-          if (kb == 0 && lt + 1 < my_tiles) Tn = tile_of(lt + 1);  // while the MMAs run
+          if (k0 == 0 && lt + 1 < my_tiles) Tn = tile_of(lt + 1);  // while the MMAs run
         }
         if (ok) {
           if constexpr (CG == 1) tc05::commit(&B.acc_full[b]);
@@ -366,45 +380,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------------- TMA
-    int f = 0;
+    int f = 0, s = 0;
+    uint32_t ph = 0;
     bool ok = true;
     for (int lt = 0; lt < my_tiles && ok; lt++) {
       const Tile T = tile_of(lt);
-      // this CTA's token rows of the tile: one box of a full tile's rows, or
-      // boxes of 64, 32 and 16 rows.  One lane issues them all: the copy's operands are uniform registers,
-      // and lanes with operands of their own would be served one by one
-      // (per-lane boxes took longer to issue than a stage's MMAs take)
-      const int rows = T.N / CG, first = T.n0 + rank * rows;
-      const uint32_t bytes = (uint32_t)(rows * 128 + MB * 16384) * CG;
-      for (int kb = 0; kb < nk; kb++, f++) {
-        const int s = f % S;
-        if (!tc_warp_wait<CG>(&B.empty[s], (uint32_t)(((f / S) & 1) ^ 1), P)) {
-          ok = false;
-          break;
-        }
+      // this CTA's token rows of the tile: one box of as many rows (64 + 32 +
+      // 16 in three boxes cost 7% at 8192 x 8192 x 2048).  One lane issues
+      // the copies: their operands are uniform registers, and lanes with
+      // operands of their own would be served one by one
+      const int rows = T.N / CG, box = (rows + LY::unit - 1) / LY::unit, first = T.n0 + rank * rows;
+      const uint32_t bytes = (uint32_t)(KB * (box * LY::unit * 128 + MB * 16384)) * CG;
+      const CUtensorMap *map_a = &P.tm_a[box - 1];
+      for (int kb = 0; kb < nk; kb += KB, f++) {
         // (failure-detection test: CTA 0 never expects its first stage's
         // copies, so the MMA warp's bounded wait runs out)
-        if (P.withhold && blockIdx.x == 0 && f == 0) {
+        if (!tc_warp_wait<CG>(&B.empty[s], ph ^ 1, P) || (P.withhold && blockIdx.x == 0 && f == 0)) {
           ok = false;
           break;
         }
         if (tc05::elect_one()) {
-          uint8_t *st = sm + s * LY::stage;
+          uint8_t *st = ring + s * P.stage;
           if (rank == 0) mbar_expect_tx(&B.full[s], bytes);
           const uint32_t bar = CG == 1 ? smem_u32(&B.full[s]) : tc05::map_rank(&B.full[s], 0);
-          auto load = [&](void *dst, const CUtensorMap *map, int y) { tc05::tma_load_2d_cg<CG>(dst, map, kb * 128, y, bar); };
 #pragma unroll
-          for (int m = 0; m < MB; m++) load(st + LY::offW + 16384 * m, &P.tm_b, weight_row(T, m));
-          if (rows == LY::N / CG) {
-            load(st, &P.tm_a[0], first);
-          } else {
-            int r0 = 0;
-            for (; r0 + 64 <= rows; r0 += 64) load(st + r0 * 128, &P.tm_a[1], first + r0);
-            if (rows & 32) load(st + r0 * 128, &P.tm_a[2], first + r0), r0 += 32;
-            if (rows & 16) load(st + r0 * 128, &P.tm_a[3], first + r0);
-          }
+          for (int m = 0; m < MB; m++)
+            tc05::tma_load_cg<CG, KB>(st + KB * P.tok + 16384 * KB * m, &P.tm_b, kb, weight_row(T, m), bar);
+          tc05::tma_load_cg<CG, KB>(st, map_a, kb, first, bar);
         }
         __syncwarp();
+        if (++s == S) s = 0, ph ^= 1;
       }
     }
     // copies still in flight land before the CTA (the pair) ends
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       if (T.mt >= nmt) {
         release(b);
       } else if constexpr (KIND == kOutSilu8) {
-        uint8_t *hb = sm + LY::offEpi;                                     // [N][128] h in e4m3
+        uint8_t *hb = sm;                                     // [N][128] h in e4m3
         uint32_t *mx = reinterpret_cast<uint32_t *>(hb + LY::N * 128);     // [4][N] warp maxima
         // channel scale blocks are whole: 128 channels = this tile's rows
         for (int c0 = 0; c0 < T.N; c0 += 16) {
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
 #pragma unroll
           for (int j = 0; j < 16; j++) {
             const float v = h[j] * __shfl_sync(FULLM, fe, j);
-            hb[(c0 + j) * 128 + et] = (uint8_t)e4m3x2(v, 0.f);
+            hb[(c0 + j) * 128 + et] = (uint8_t)e4m3x2<true>(v, 0.f);
           }
         }
         release(b);
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
         // kernel); rows that do not allow that are stored value by value
         using O = typename std::conditional<KIND == kOutF32, float, uint16_t>::type;
         constexpr int V = 16 / sizeof(O), per = 32 / V;  // values a 16-byte piece, pieces a token
-        O *stg = reinterpret_cast<O *>(sm + LY::offEpi) + q * 1024;
+        O *stg = reinterpret_cast<O *>(sm) + q * 1024;
         const int row0 = T.mt * 128 + 32 * q;
         O *o = static_cast<O *>(P.out) + (size_t)T.n0 * P.ldo + row0;
         const bool wide = P.wide && row0 + 32 <= P.n;
@@ -581,21 +586,39 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bytes [rows] x cols, rows ld apart, box 128 bytes x box_rows, 128B swizzle, zeros outside
-bool make_map8(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_rows) {
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {ld};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+// bytes [rows] x cols, rows ld apart, 128B swizzle, zeros outside: boxes of
+// 128 bytes x box_rows, or (kb == 2; cols % 128 == 0) x 2 k blocks as well
+bool make_map8(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_rows, int kb) {
+  const cuuint64_t dims2[2] = {cols, rows}, dims3[3] = {128, rows, cols / 128};
+  const cuuint64_t strides[2] = {ld, 128};
+  const cuuint32_t box[3] = {128, box_rows, 2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)kb + 1, const_cast<void *>(base),
+                     kb == 2 ? dims3 : dims2, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MB, int KIND, int CG>
-cudaError_t launch_tc(const Mm8P &p, int grid, bool pdl, cudaStream_t st) {
-  constexpr int smem = TcLay<MB, CG>::smem;
-  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// weight tiles of a group, and whether CTA pairs take them two at a time
+int weight_tiles(const Mm8P &p, int out_kind) { return out_kind == kOutSilu8 ? p.n / 256 : p.nb; }
+bool use_pairs(const Mm8P &p, int out_kind) { return weight_tiles(p, out_kind) > 1; }
+
+// The launch of one form: the ring for the tile width p.wmax, the tensor
+// maps, the kernel.
+template <int MB, int KIND, int CG, int KB>
+cudaError_t launch_tc(Mm8P &p, int grid, bool pdl, cudaStream_t st) {
+  using LY = TcLay<MB, CG>;
+  const int rows = (p.wmax / CG + LY::unit - 1) / LY::unit * LY::unit;
+  p.tok = rows * 128;
+  p.stage = (KB * (p.tok + MB * 16384) + 1023) / 1024 * 1024;
+  p.stages = LY::room / p.stage < kMaxStages ? LY::room / p.stage : kMaxStages;
+  bool ok = encode_fn() != nullptr;
+  ok = ok && make_map8(&p.tm_b, p.b, p.k, (uint64_t)(p.G > 0 ? p.G : 1) * p.n, p.k, 128, KB);
+  for (int i = 0; i < rows / LY::unit; i++)
+    ok = ok && make_map8(&p.tm_a[i], p.a, p.k, p.t, p.lda, (uint32_t)((i + 1) * LY::unit), KB);
+  if (!ok) return cudaErrorNotSupported;
+  const int smem = LY::offRing + p.stages * p.stage + 1024;
+  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[2];
   int n = 0;
@@ -616,32 +639,10 @@ cudaError_t launch_tc(const Mm8P &p, int grid, bool pdl, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = (unsigned)n;
-  return cudaLaunchKernelEx(&cfg, mm8_tc<MB, KIND, CG>, p);
+  return cudaLaunchKernelEx(&cfg, mm8_tc<MB, KIND, CG, KB>, p);
 }
-
-// weight tiles of a group, and whether CTA pairs take them two at a time
-int weight_tiles(const Mm8P &p, int out_kind) { return out_kind == kOutSilu8 ? p.n / 256 : p.nb; }
-bool use_pairs(const Mm8P &p, int out_kind) { return weight_tiles(p, out_kind) > 1; }
 
 }  // namespace
-
-int mm8_tensor_maps(Mm8P &p, int out_kind, const char **why) {
-  if (!encode_fn()) {
-    *why = "cuTensorMapEncodeTiled is not available from the driver";
-    return -1;
-  }
-  const uint64_t rows_b = (uint64_t)(p.G > 0 ? p.G : 1) * p.n;
-  const bool pairs = use_pairs(p, out_kind);
-  const uint32_t full = out_kind == kOutSilu8 ? (pairs ? TcLay<2, 2>::N / 2 : TcLay<2, 1>::N)
-                                              : (pairs ? TcLay<1, 2>::N / 2 : TcLay<1, 1>::N);
-  bool ok = make_map8(&p.tm_b, p.b, p.k, rows_b, p.k, 128);
-  for (int i = 0; i < 4; i++) ok = ok && make_map8(&p.tm_a[i], p.a, p.k, p.t, p.lda, i ? 128u >> i : full);
-  if (!ok) {
-    *why = "cuTensorMapEncodeTiled rejected a tensor map";
-    return -1;
-  }
-  return 0;
-}
 
 cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.n + 15) / 16);
@@ -679,7 +680,10 @@ cudaError_t launch_tc_form(Mm8P p, int n_sms, bool pdl, cudaStream_t st) {
   const int64_t tt = (p.t + p.wmax - 1) / p.wmax + (p.offs ? p.G : 0);
   const int64_t tiles = tt * ((weight_tiles(p, KIND) + cg - 1) / cg);
   const int grid = (int)(tiles < n_sms / cg ? tiles : n_sms / cg) * cg;
-  return pairs ? launch_tc<MB, KIND, 2>(p, grid, pdl, st) : launch_tc<MB, KIND, 1>(p, grid, pdl, st);
+  if (!pairs) return launch_tc<MB, KIND, 1, 1>(p, grid, pdl, st);
+  if constexpr (MB == 1)
+    if (p.k % 256 == 0) return launch_tc<MB, KIND, 2, 2>(p, grid, pdl, st);
+  return launch_tc<MB, KIND, 2, 1>(p, grid, pdl, st);
 }
 
 cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st) {

@@ -44,9 +44,7 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int n, float (&v
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(uint8_t *q, int n, const float (&v)[8], float f) {
-  const uint32_t lo = e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
-  const uint32_t hi = e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);
+__device__ __forceinline__ void store8(uint8_t *q, int n, uint32_t lo, uint32_t hi) {
   if (VEC) {
     if (n > 0) *reinterpret_cast<uint2 *>(q) = make_uint2(lo, hi);
   } else {
@@ -56,40 +54,36 @@ __device__ __forceinline__ void store8(uint8_t *q, int n, const float (&v)[8], f
   }
 }
 
-// Half a warp per row block of 128, eight values a lane; U blocks' loads are
-// in flight before the first is used (one block at a time left HBM at a
-// third of its rate).  A thread block takes 16 * U consecutive blocks.
-constexpr int kRowBlocks = 4;
+// Half a warp per row block of 128, eight values a lane; the half warps walk
+// the blocks of all rows in turn, the next block's load in flight while one
+// is converted.  The step from block to block is counted, not divided: some
+// 80 instructions a block are what bounds this kernel beside HBM.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows(const __grid_constant__ Quant8P P) {
-  const int cb = (P.cols + 127) / 128, sub = threadIdx.x & 15, half = threadIdx.x >> 4;
-  const int64_t blocks = (int64_t)P.rows * cb, stride = (int64_t)gridDim.x * (16 * kRowBlocks);
-  // every lane of a warp takes part in the exchange below: the loop bound is
-  // the same for all, what lies past the end is masked
-  for (int64_t i0 = (int64_t)blockIdx.x * (16 * kRowBlocks); i0 < blocks; i0 += stride) {
-    int64_t row[kRowBlocks];
-    int b[kRowBlocks], n[kRowBlocks];
-    float v[kRowBlocks][8];
+  const int cb = (P.cols + 127) / 128, sub = threadIdx.x & 15;
+  const int step = gridDim.x * 16, step_r = step / cb, step_b = step - step_r * cb;
+  const int i0 = blockIdx.x * 16 + (threadIdx.x >> 4);
+  int row = i0 / cb, b = i0 - row * cb;
+  float next[8];
+  auto load = [&](int r, int bb) {
+    const int c = bb * 128 + sub * 8;
+    load8<BF16, VEC>(P.x, (int64_t)r * P.ldx + c, r < P.rows ? min(8, P.cols - c) : 0, next);
+  };
+  load(row, b);
+  // both halves of a warp take part in the exchange: it walks on while either
+  // has a block
+  while (__any_sync(FULLM, row < P.rows)) {
+    const int r = row, bb = b, n = r < P.rows ? min(8, P.cols - bb * 128 - sub * 8) : 0;
+    float v[8];
 #pragma unroll
-    for (int u = 0; u < kRowBlocks; u++) {
-      const int64_t i = i0 + 16 * u + half;
-      const bool on = i < blocks;
-      row[u] = on ? (blocks < (1ll << 31) ? (int64_t)((uint32_t)i / (uint32_t)cb) : i / cb) : 0;
-      b[u] = on ? (int)(i - row[u] * cb) : 0;
-      n[u] = on ? min(8, P.cols - b[u] * 128 - sub * 8) : 0;
-      load8<BF16, VEC>(P.x, row[u] * P.ldx + b[u] * 128 + sub * 8, n[u], v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kRowBlocks; u++) {
-      uint32_t a = 0;
-#pragma unroll
-      for (int j = 0; j < 8; j++) a = max(a, mag_bits(v[u][j]));
-#pragma unroll
-      for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(FULLM, a, o));
-      const uint32_t e = e8m0_of_amax(a);
-      store8<VEC>(P.q + row[u] * P.ldq + b[u] * 128 + sub * 8, n[u], v[u], e8m0_inv(e));
-      if (i0 + 16 * u + half < blocks && sub == 0) P.s[row[u] * P.lds + b[u]] = (uint8_t)e;
-    }
+    for (int j = 0; j < 8; j++) v[j] = next[j];
+    b += step_b, row = min(row + step_r, P.rows);
+    if (b >= cb) b -= cb, row = min(row + 1, P.rows);
+    load(row, b);
+    uint32_t w[2], e;
+    quant_block<8>(v, w, e);
+    store8<VEC>(P.q + (int64_t)r * P.ldq + bb * 128 + sub * 8, n, w[0], w[1]);
+    if (r < P.rows && sub == 0) P.s[(int64_t)r * P.lds + bb] = (uint8_t)e;
   }
 }
 
@@ -120,7 +114,9 @@ __global__ void __launch_bounds__(256) quant_blocks(const __grid_constant__ Quan
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int row = r0 + 16 * i;
-    if (row < P.rows) store8<VEC>(P.q + (int64_t)row * P.ldq + c, min(8, P.cols - c), v[i], f);
+    const uint32_t lo = e4m3x4<true>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
+    const uint32_t hi = e4m3x4<true>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f);
+    if (row < P.rows) store8<VEC>(P.q + (int64_t)row * P.ldq + c, min(8, P.cols - c), lo, hi);
   }
   if (threadIdx.x == 0) P.s[(int64_t)blockIdx.y * P.lds + blockIdx.x] = (uint8_t)e;
 }
@@ -134,9 +130,10 @@ bool vec_ok(const Quant8P &p) {
 }  // namespace
 
 cudaError_t launch_quant8_rows(const Quant8P &p, int n_sms, cudaStream_t st) {
-  const int64_t blocks = (int64_t)p.rows * ((p.cols + 127) / 128);
-  const int64_t need = (blocks + 16 * kRowBlocks - 1) / (16 * kRowBlocks), cap = (int64_t)n_sms * 16;
-  const unsigned grid = (unsigned)(need < cap ? need : cap);
+  // as many thread blocks as stay resident, each with the same number of rounds
+  const int64_t need = ((int64_t)p.rows * ((p.cols + 127) / 128) + 15) / 16, cap = (int64_t)n_sms * 8;
+  const int64_t rounds = (need + cap - 1) / cap;
+  const unsigned grid = (unsigned)((need + rounds - 1) / rounds);
   const bool v = vec_ok(p);
   if (p.bf16) {
     if (v) quant_rows<true, true><<<grid, 256, 0, st>>>(p);

@@ -255,29 +255,31 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
       : "memory");
 }
 
-// The same with the barrier as a shared::cluster address; CG = 2: it may be
-// the other CTA's of the pair.
-template <int CG>
-__device__ __forceinline__ void tma_load_2d_cg(void *dst, const void *tmap, int x, int y, uint32_t bar) {
-  if constexpr (CG == 1)
+// Rows y, ... of k block kb (128 bytes), or KB = 2: of the blocks kb and kb +
+// 1 (a 3-D map), completing on an mbarrier given as a shared::cluster
+// address; CG = 2: it may be the other CTA's of the pair.
+template <int CG, int KB>
+__device__ __forceinline__ void tma_load_cg(void *dst, const void *tmap, int kb, int y, uint32_t bar) {
+  const uint64_t map = reinterpret_cast<uint64_t>(tmap);
+  const uint32_t to = smem_u32(dst);
+  if constexpr (KB == 1 && CG == 1)
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        "[%4];" ::"r"(to),
+        "l"(map), "r"(kb * 128), "r"(y), "r"(bar)
+        : "memory");
+  else if constexpr (KB == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(to),
+        "l"(map), "r"(kb * 128), "r"(y), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-        "%3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(to),
+        "l"(map), "r"(0), "r"(y), "r"(kb), "r"(bar)
         : "memory");
-}
-// 2-D tile into L2 only
-__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(tmap)),
-               "r"(x), "r"(y)
-               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
