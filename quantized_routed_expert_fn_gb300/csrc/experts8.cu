@@ -4,17 +4,19 @@
 // Few rows (decode, verify): two kernels that stream the union's weights
 // once, by bulk copies through a ring of shared-memory stages that a warp of
 // its own keeps full, so that HBM is read without a pause between a CTA's
-// tiles.  A stage is a few whole weight rows, contiguous in memory.  Each
-// kernel takes half of an SM's shared memory, so that the second one's CTAs
-// are there, their first weights on the way, while the first ends.
+// tiles.  A stage is a few whole weight rows, contiguous in memory.
 // Every row is a column of the m16n8 tiles, whether it chose the expert or
 // not, so no row lists are built.
 //   gate_up  persistent; an item is 8 channels of one expert (its 8 gate and
-//            8 up rows are one M = 16 tile), its k blocks shared out over 16
-//            warps, their sums met by a warp of its own; writes h in fp32
+//            8 up rows are one M = 16 tile); four teams of four warps take
+//            the items in turn, a team shares out an item's k blocks, its
+//            sums are met by a warp of its own; writes h in fp32
 //   down     a CTA per 16 output rows over all experts of the union, the
-//            (expert, k block) items shared out over 16 warps; it quantises h
-//            while its weights arrive; sums meet in a fixed order
+//            (expert, two k blocks) items shared out over 16 warps; it
+//            quantises h while its weights arrive; sums meet in a fixed order
+// An item's chain of wait, loads, MMAs and arrival takes a warp some 1000
+// cycles, in which HBM brings 23 KB to an SM: so several items are worked on
+// at once, and two k blocks' MMAs are interleaved.
 // Many rows: the entries are grouped by expert (count, scan), x is quantised
 // once per row and written to its entries' places, mm8_tc computes h8 and
 // the outputs y, and a last kernel sums a row's weighted outputs in the
@@ -42,17 +44,27 @@ __device__ __forceinline__ void pdl_wait_prev() { asm volatile("griddepcontrol.w
 // in a bank; the MMAs take longer than that.  Converting the weights to f16
 // by hand, by the conversion instruction or by integer operations, was 10 to
 // 25% slower than the 8-bit MMA.)
-__device__ __forceinline__ void mma_block(float (&d)[4], const uint8_t *lo, const uint8_t *hi, int ld, int g, int q,
-                                          const uint8_t *col, bool have) {
+struct Block {
+  uint4 a0, a1, a2, a3, b0, b1;
+};
+__device__ __forceinline__ void load_block(Block &x, const uint8_t *lo, const uint8_t *hi, int ld, int g, int q,
+                                           const uint8_t *col, bool have) {
   const uint8_t *r0 = lo + g * ld + 32 * q, *r1 = hi + g * ld + 32 * q;
-  uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-  if (have) b0 = *reinterpret_cast<const uint4 *>(col), b1 = *reinterpret_cast<const uint4 *>(col + 16);
-  const uint4 a0 = *reinterpret_cast<const uint4 *>(r0), a2 = *reinterpret_cast<const uint4 *>(r0 + 16);
-  const uint4 a1 = *reinterpret_cast<const uint4 *>(r1), a3 = *reinterpret_cast<const uint4 *>(r1 + 16);
-  mma_e4m3(d, a0.x, a1.x, a0.y, a1.y, b0.x, b0.y);
-  mma_e4m3(d, a0.z, a1.z, a0.w, a1.w, b0.z, b0.w);
-  mma_e4m3(d, a2.x, a3.x, a2.y, a3.y, b1.x, b1.y);
-  mma_e4m3(d, a2.z, a3.z, a2.w, a3.w, b1.z, b1.w);
+  x.b0 = x.b1 = make_uint4(0, 0, 0, 0);
+  if (have) x.b0 = *reinterpret_cast<const uint4 *>(col), x.b1 = *reinterpret_cast<const uint4 *>(col + 16);
+  x.a0 = *reinterpret_cast<const uint4 *>(r0), x.a2 = *reinterpret_cast<const uint4 *>(r0 + 16);
+  x.a1 = *reinterpret_cast<const uint4 *>(r1), x.a3 = *reinterpret_cast<const uint4 *>(r1 + 16);
+}
+// the MMAs of two blocks, in turn
+__device__ __forceinline__ void mma_blocks(float (&d)[4], const Block &x, float (&e)[4], const Block &y) {
+  mma_e4m3(d, x.a0.x, x.a1.x, x.a0.y, x.a1.y, x.b0.x, x.b0.y);
+  mma_e4m3(e, y.a0.x, y.a1.x, y.a0.y, y.a1.y, y.b0.x, y.b0.y);
+  mma_e4m3(d, x.a0.z, x.a1.z, x.a0.w, x.a1.w, x.b0.z, x.b0.w);
+  mma_e4m3(e, y.a0.z, y.a1.z, y.a0.w, y.a1.w, y.b0.z, y.b0.w);
+  mma_e4m3(d, x.a2.x, x.a3.x, x.a2.y, x.a3.y, x.b1.x, x.b1.y);
+  mma_e4m3(e, y.a2.x, y.a3.x, y.a2.y, y.a3.y, y.b1.x, y.b1.y);
+  mma_e4m3(d, x.a2.z, x.a3.z, x.a2.w, x.a3.w, x.b1.z, x.b1.w);
+  mma_e4m3(e, y.a2.z, y.a3.z, y.a2.w, y.a3.w, y.b1.z, y.b1.w);
 }
 
 // bounded wait on an mbarrier phase, of a thread and of a warp; false (and
@@ -99,7 +111,7 @@ __device__ __forceinline__ uint2 quant128(const float (&v)[8], uint32_t &e) {
 constexpr int kMaxEntries = kEx8SmallRows * 32;
 constexpr int kMaxStages = 24;
 constexpr int kDownWarps = 16;
-constexpr size_t kSmemCap = 112 * 1024;
+constexpr size_t kSmemCap = 226 * 1024;
 
 // The union of the rows' experts, as each kernel builds it for itself (in
 // the order of the id table; ids below E, once each).
@@ -170,18 +182,16 @@ __device__ void union_rows(const Union &U, const Ex8P &P, int tid, int count) {
 __host__ __device__ constexpr int row_stride(int k) { return k + 16; }  // e4m3 rows of x, h: 16 bytes apart in the banks
 
 // ---- gate_up: dynamic shared memory: ring | x rows | their scales | sums | union
-constexpr int kGuWarps = 16, kGuThreads = 32 * (kGuWarps + 2);
-struct GuLay {
-  int stage, ns;  // bytes of a stage (8 rows), stages (even: an item is two)
-  size_t xs, sx, red, un, total;
-};
-__host__ __device__ inline GuLay gu_layout(int H, int t, int K) {
+constexpr int kTeams = 4, kTeam = 4, kGuWarps = kTeams * kTeam, kGuThreads = 32 * (kGuWarps + 2);
+GuLay gu_layout(int H, int t, int K) {
   GuLay l{};
   l.stage = 8 * H;
-  const size_t xs = (size_t)t * row_stride(H), sx = ((size_t)t * (H / 128) * 4 + 15) / 16 * 16, red = 2 * kGuWarps * 512;
+  const size_t xs = (size_t)t * row_stride(H), sx = ((size_t)t * (H / 128) * 4 + 15) / 16 * 16, red = 2 * kGuWarps * 512;  // two of each team
   const size_t rest = xs + sx + red + union_bytes(t * K);
   const size_t room = kSmemCap > rest ? (kSmemCap - rest) / l.stage : 0;
-  l.ns = (int)(room < kMaxStages ? room : kMaxStages) & ~1;
+  const int fit = (int)(room < kMaxStages ? room : kMaxStages);
+  l.teams = fit >= 8 ? 4 : (fit >= 4 ? 2 : 1);
+  l.ns = fit / (2 * l.teams) * (2 * l.teams);
   l.xs = (size_t)l.ns * l.stage, l.sx = l.xs + xs, l.red = l.sx + sx, l.un = l.red + red;
   l.total = (size_t)l.ns * l.stage + rest;
   return l;
@@ -192,21 +202,25 @@ __host__ __device__ inline GuLay gu_layout(int H, int t, int K) {
 template <bool BF16>
 __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_constant__ Ex8P P) {
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], red_full[2], red_empty[2];
-  const GuLay L = gu_layout(P.H, P.t, P.K);
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], red_full[kTeams][2], red_empty[kTeams][2];
+  const GuLay L = P.gl;
   uint8_t *xs = sm + L.xs;
   float *sx = reinterpret_cast<float *>(sm + L.sx);
   float4 *red = reinterpret_cast<float4 *>(sm + L.red);
   const Union U = union_at(sm + L.un, P.t * P.K);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int H = P.H, I = P.I, nk = H / 128, nct = I / 8;
+  // first item of CTA b: a CTA's items follow one another, so that it reads
+  // few experts' pages (with every 152nd item each copy was another page, and
+  // the misses in the address translation bound the kernel)
+  auto share = [&](int items, unsigned b) { return (int)((int64_t)items * b / gridDim.x); };
   pdl_launch_next();
 
   if (warp == kGuWarps) {
     // ---- the union, then the producer: gate rows, up rows of every item
     if (lane == 0) {
-      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], kGuWarps);
-      for (int b = 0; b < 2; b++) mbar_init(&red_full[b], kGuWarps), mbar_init(&red_empty[b], 1);
+      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], kTeam);
+      for (int b = 0; b < 2 * kTeams; b++) mbar_init(&red_full[0][b], kTeam), mbar_init(&red_empty[0][b], 1);
       fence_mbar_init();
       if (blockIdx.x == 0) *P.status = 0;
     }
@@ -216,8 +230,8 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
       int f = 0, s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      const int items = *U.n * nct;
-      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const int items = *U.n * nct, end = share(items, blockIdx.x + 1);
+      for (int it = share(items, blockIdx.x); it < end && ok; it++) {
         const int u = it / nct, ct = it - u * nct;
         const uint8_t *src = P.gu + ((size_t)U.ex[u] * 2 * I + ct * 8) * H;
         for (int h = 0; h < 2; h++) {
@@ -238,10 +252,10 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
     // ---- sums: lane (c, q) adds the warps' parts of channel c, columns 2q
     // and 2q + 1, in the order of the warps
     tc05::named_sync(3, kGuThreads);
-    const int items = *U.n * nct;
-    int turn = 0;
+    const int items = *U.n * nct, end = share(items, blockIdx.x + 1);
+    int team = 0, turn = 0;
     uint32_t ph = 0;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it = share(items, blockIdx.x); it < end; it++) {
       const int u = it / nct, ct = it - u * nct;
       // the columns' entries: a row's first with this expert
       int e0 = -1, e1 = -1;
@@ -251,17 +265,19 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
         if (r == 2 * q) e0 = e;
         if (r == 2 * q + 1) e1 = e;
       }
-      if (!warp_wait(&red_full[turn], ph, P)) break;
+      if (!warp_wait(&red_full[team][turn], ph, P)) break;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kGuWarps; w++) {
-        const float4 p = red[(turn * kGuWarps + w) * 32 + lane];
+      for (int w = 0; w < kTeam; w++) {
+        const float4 p = red[((team * 2 + turn) * kTeam + w) * 32 + lane];
         v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&red_empty[turn]);
-      turn ^= 1;
-      if (turn == 0) ph ^= 1;
+      if (lane == 0) mbar_arrive(&red_empty[team][turn]);
+      if (++team == L.teams) {
+        team = 0, turn ^= 1;
+        if (turn == 0) ph ^= 1;
+      }
       const size_t c = (size_t)ct * 8 + g;
       if (e0 >= 0) P.h32[(size_t)e0 * I + c] = v.x / (1.f + expf(-v.x)) * v.z;
       if (e1 >= 0) P.h32[(size_t)e1 * I + c] = v.y / (1.f + expf(-v.y)) * v.w;
@@ -293,66 +309,90 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
   }
   tc05::named_sync(3, kGuThreads);
   tc05::named_sync(1, 32 * kGuWarps);
-  const int items = *U.n * nct, step_u = (int)gridDim.x / nct, step_c = (int)gridDim.x - step_u * nct;
+  const int team = warp / kTeam, tw = warp - team * kTeam;  // the warp within its team
+  if (team >= L.teams) return;
+  const int all = *U.n * nct, items = share(all, blockIdx.x + 1), step = L.teams, step_u = step / nct,
+            step_c = step - step_u * nct;
   const bool have = g < P.t, have0 = 2 * q < P.t, have1 = 2 * q + 1 < P.t;
   const uint8_t *col = xs + (size_t)(have ? g : 0) * row_stride(H) + q * 32;
   const float *sx0 = sx + (have0 ? 2 * q : 0) * nk, *sx1 = sx + (have1 ? 2 * q + 1 : 0) * nk;
   const size_t up_s = (size_t)(I / 128) * nk;  // from a gate scale to its up scale
-  int u = (int)blockIdx.x / nct, ct = (int)blockIdx.x - u * nct;
-  // the weight scales of the warp's first k block, loaded an item ahead
+  int it = share(all, blockIdx.x) + team;
+  int u = it / nct, ct = it - u * nct;
+  // the weight scales of the warp's first four k blocks, a byte each, loaded
+  // an item ahead
   uint32_t ng = 0, nu = 0;
   auto prefetch = [&](int uu, int cc) {
-    const uint8_t *sg = P.gus + ((size_t)U.ex[uu] * (2 * I / 128) + cc / 16) * nk + warp;
-    ng = sg[0], nu = sg[up_s];
+    const uint8_t *sg = P.gus + ((size_t)U.ex[uu] * (2 * I / 128) + cc / 16) * nk + tw;
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      a[i] = tw + kTeam * i < nk ? sg[kTeam * i] : 0u;
+      b[i] = tw + kTeam * i < nk ? sg[up_s + kTeam * i] : 0u;
+    }
+    ng = a[0] | a[1] << 8 | a[2] << 16 | a[3] << 24, nu = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
   };
-  if ((int)blockIdx.x < items && warp < nk) prefetch(u, ct);
-  int s = 0, turn = 0;
+  if (it < items) prefetch(u, ct);
+  int s = 2 * team, turn = 0;
   uint32_t ph = 0, rph = 0;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+  for (; it < items; it += step) {
     const int u0 = u, ct0 = ct;
     uint32_t wg = ng, wu = nu;
     u += step_u, ct += step_c;
     if (ct >= nct) ct -= nct, u++;
-    if (it + (int)gridDim.x < items && warp < nk) prefetch(u, ct);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!warp_wait(&full[s], ph, P) || !warp_wait(&full[s + 1], ph, P)) break;
+    if (it + step < items) prefetch(u, ct);
     const uint8_t *gr = sm + (size_t)s * L.stage, *ur = gr + L.stage;
-    for (int kb = warp; kb < nk; kb += kGuWarps) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_block(d, gr + kb * 128, ur + kb * 128, H, g, q, col + kb * 128, have);
-      if (kb >= kGuWarps) {
-        const uint8_t *sg = P.gus + ((size_t)U.ex[u0] * (2 * I / 128) + ct0 / 16) * nk + kb;
-        wg = sg[0], wu = sg[up_s];
+    for (int kb = tw; kb < nk; kb += 2 * kTeam) {
+      // two blocks; past the end the second is the first again, unscaled
+      const bool two = kb + kTeam < nk;
+      const int k2 = two ? kb + kTeam : kb;
+      Block x, y;
+      load_block(x, gr + kb * 128, ur + kb * 128, H, g, q, col + kb * 128, have);
+      load_block(y, gr + k2 * 128, ur + k2 * 128, H, g, q, col + k2 * 128, have);
+      float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_blocks(d, x, e, y);
+      if (kb >= 4 * kTeam) {
+        const uint8_t *sg = P.gus + ((size_t)U.ex[u0] * (2 * I / 128) + ct0 / 16) * nk;
+        wg = sg[kb] | (uint32_t)sg[k2] << 8, wu = sg[up_s + kb] | (uint32_t)sg[up_s + k2] << 8;
       }
-      const float fg = e8m0_f(wg), fu = e8m0_f(wu), x0 = have0 ? sx0[kb] : 0.f, x1 = have1 ? sx1[kb] : 0.f;
+      const float fg = e8m0_f(wg & 255u), fu = e8m0_f(wu & 255u), x0 = have0 ? sx0[kb] : 0.f, x1 = have1 ? sx1[kb] : 0.f;
       acc.x += d[0] * x0 * fg, acc.y += d[1] * x1 * fg, acc.z += d[2] * x0 * fu, acc.w += d[3] * x1 * fu;
+      if (two) {
+        const float hg = e8m0_f(wg >> 8 & 255u), hu = e8m0_f(wu >> 8 & 255u);
+        const float y0 = have0 ? sx0[k2] : 0.f, y1 = have1 ? sx1[k2] : 0.f;
+        acc.x += e[0] * y0 * hg, acc.y += e[1] * y1 * hg, acc.z += e[2] * y0 * hu, acc.w += e[3] * y1 * hu;
+      }
+      wg >>= 16, wu >>= 16;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]), mbar_arrive(&empty[s + 1]);
-    s += 2;
-    if (s == L.ns) s = 0, ph ^= 1;
-    if (!warp_wait(&red_empty[turn], rph ^ 1, P)) break;
-    red[(turn * kGuWarps + warp) * 32 + lane] = acc;
+    s += 2 * L.teams;
+    if (s >= L.ns) s -= L.ns, ph ^= 1;
+    if (!warp_wait(&red_empty[team][turn], rph ^ 1, P)) break;
+    red[((team * 2 + turn) * kTeam + tw) * 32 + lane] = acc;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&red_full[turn]);
+    if (lane == 0) mbar_arrive(&red_full[team][turn]);
     turn ^= 1;
     if (turn == 0) rph ^= 1;
   }
 }
 
 // ---- down: dynamic shared memory: ring | h rows | their scales | weight scales | union | sums
-struct DnLay {
-  int stage, ns;
-  size_t hs, sh, sd, un, red, total;
-};
-__host__ __device__ inline DnLay dn_layout(int I, int n) {
+DnLay dn_layout(int I, int n) {
   DnLay l{};
   const int nk = I / 128;
   l.stage = 16 * I;
   const size_t hs = (size_t)n * row_stride(I), sh = ((size_t)n * nk * 4 + 15) / 16 * 16, red = kDownWarps * 16 * 9 * 4;
   const size_t un = union_bytes(n) / 16 * 16, rest = hs + 2 * sh + un + red;
   const size_t room = kSmemCap > rest ? (kSmemCap - rest) / l.stage : 0;
-  l.ns = (int)(room < kMaxStages ? room : kMaxStages);
+  const int fit = (int)(room < kMaxStages ? room : kMaxStages), np = (nk + 1) / 2;
+  for (int ns = fit; ns >= 1 && 2 * ns >= fit; ns--) {
+    int w = kDownWarps;
+    while (ns * np % w) w--;
+    if (w > l.warps) l.warps = w, l.ns = ns;
+  }
   l.hs = (size_t)l.ns * l.stage, l.sh = l.hs + hs, l.sd = l.sh + sh, l.un = l.sd + sh, l.red = l.un + un;
   l.total = (size_t)l.ns * l.stage + rest;
   return l;
@@ -363,7 +403,7 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
   const int n = P.t * P.K;
-  const DnLay L = dn_layout(P.I, n);
+  const DnLay L = P.dl;
   uint8_t *hs = sm + L.hs;
   float *sh = reinterpret_cast<float *>(sm + L.sh), *sd = reinterpret_cast<float *>(sm + L.sd);
   float *red = reinterpret_cast<float *>(sm + L.red);
@@ -373,7 +413,7 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
   if (warp == kDownWarps) {
     // ---- the union, then the producer: this CTA's rows of every expert
     if (lane == 0) {
-      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], (uint32_t)nk);
+      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], (uint32_t)(nk + 1) / 2);
       fence_mbar_init();
     }
     union_warp(U, P);
@@ -426,30 +466,40 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
   }
   tc05::named_sync(1, 32 * kDownWarps);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const int step_u = kDownWarps / nk, step_k = kDownWarps - step_u * nk;
-  int u = warp / nk, kb = warp - u * nk, s = u % L.ns;
-  uint32_t ph = (uint32_t)((u / L.ns) & 1);
-  for (int it = warp; it < items; it += kDownWarps) {
+  const int np = (nk + 1) / 2, pairs = *U.n * np, step_u = L.warps / np, step_p = L.warps - step_u * np;
+  int u = warp / np, pr = warp - u * np, s = u;
+  uint32_t ph = 0;
+  while (s >= L.ns) s -= L.ns, ph ^= 1;
+  for (int it = warp; it < pairs && warp < L.warps; it += L.warps) {
+    // two blocks; past the end the second is the first again, unscaled
+    const int kb = 2 * pr, k2 = kb + 1 < nk ? kb + 1 : kb;
     const int e = U.ent[u][g], e0 = U.ent[u][2 * q], e1 = U.ent[u][2 * q + 1];
+    const uint8_t *col = hs + (size_t)max(e, 0) * row_stride(I) + q * 32;
     if (!warp_wait(&full[s], ph, P)) break;
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint8_t *wr = sm + (size_t)s * L.stage + kb * 128;
-    mma_block(d, wr, wr + 8 * I, I, g, q, hs + (size_t)max(e, 0) * row_stride(I) + kb * 128 + q * 32, e >= 0);
-    // a column whose row did not choose the expert adds nothing, whatever
-    // the product is (a NaN weight times zero)
-    if (e0 >= 0) {
-      const float sc = sh[e0 * nk + kb] * sd[it] * U.w[u][2 * q];
-      acc[0] += d[0] * sc, acc[2] += d[2] * sc;
-    }
-    if (e1 >= 0) {
-      const float sc = sh[e1 * nk + kb] * sd[it] * U.w[u][2 * q + 1];
-      acc[1] += d[1] * sc, acc[3] += d[3] * sc;
-    }
+    const uint8_t *wr = sm + (size_t)s * L.stage;
+    Block x, y;
+    load_block(x, wr + kb * 128, wr + 8 * I + kb * 128, I, g, q, col + kb * 128, e >= 0);
+    load_block(y, wr + k2 * 128, wr + 8 * I + k2 * 128, I, g, q, col + k2 * 128, e >= 0);
+    float d[4] = {0.f, 0.f, 0.f, 0.f}, f[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_blocks(d, x, f, y);
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
+    // a column whose row did not choose the expert adds nothing, whatever
+    // the product is (a NaN weight times zero)
+    const float w1 = sd[u * nk + kb], w2 = k2 > kb ? sd[u * nk + k2] : 0.f;
+    if (e0 >= 0) {
+      const float w = U.w[u][2 * q], p1 = sh[e0 * nk + kb] * w1 * w, p2 = sh[e0 * nk + k2] * w2 * w;
+      acc[0] += d[0] * p1, acc[2] += d[2] * p1;
+      if (k2 > kb) acc[0] += f[0] * p2, acc[2] += f[2] * p2;
+    }
+    if (e1 >= 0) {
+      const float w = U.w[u][2 * q + 1], p1 = sh[e1 * nk + kb] * w1 * w, p2 = sh[e1 * nk + k2] * w2 * w;
+      acc[1] += d[1] * p1, acc[3] += d[3] * p1;
+      if (k2 > kb) acc[1] += f[1] * p2, acc[3] += f[3] * p2;
+    }
     int du = step_u;
-    kb += step_k;
-    if (kb >= nk) kb -= nk, du++;
+    pr += step_p;
+    if (pr >= np) pr -= np, du++;
     u += du, s += du;
     while (s >= L.ns) s -= L.ns, ph ^= 1;
   }
@@ -642,7 +692,7 @@ cudaError_t launch_pdl(F f, dim3 grid, unsigned block, size_t smem, cudaStream_t
 
 bool ex8_small(int H, int I, int t, int K) {
   // an item is two of gate_up's stages
-  return t <= kEx8SmallRows && gu_layout(H, t, K).ns >= 4 && dn_layout(I, t * K).ns >= 3;
+  return t <= kEx8SmallRows && gu_layout(H, t, K).ns >= 2 && dn_layout(I, t * K).ns >= 2;
 }
 
 Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size) {
@@ -661,9 +711,9 @@ Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size) {
   return s;
 }
 
-cudaError_t launch_ex8_small(const Ex8P &p, int n_sms, cudaStream_t st) {
-  const GuLay l = gu_layout(p.H, p.t, p.K);
-  const DnLay d = dn_layout(p.I, p.t * p.K);
+cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st) {
+  const GuLay l = p.gl = gu_layout(p.H, p.t, p.K);
+  const DnLay d = p.dl = dn_layout(p.I, p.t * p.K);
   auto f = p.x_bf16 ? ex8_gate_up<true> : ex8_gate_up<false>;
   auto h = p.out_bf16 ? ex8_down<true> : ex8_down<false>;
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.total);

@@ -162,7 +162,24 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
 namespace moe {
 
 // ---- the routed experts' step (experts8.cu)
+// shared-memory layouts of the few-row kernels, made on the host
+struct GuLay {
+  // bytes of a stage (8 rows), stages, teams.  An item is two stages; the
+  // items' places in the ring are a multiple of the teams, so that a place is
+  // one team's and that team waits for every phase of its barriers (one that
+  // skipped a phase could not tell it from the phase before the last)
+  int stage, ns, teams;
+  size_t xs, sx, red, un, total;
+};
+struct DnLay {
+  // bytes of a stage (16 rows), stages, warps at work: a divisor of the items
+  // of a round of the ring, so that a stage's items are always the same warps'
+  int stage, ns, warps;
+  size_t hs, sh, sd, un, red, total;
+};
 struct Ex8P {
+  GuLay gl;
+  DnLay dl;
   unsigned long long timeout_ns;
   int H, E, I, t, K;
   const uint8_t *gu, *gus, *dn, *dns;
@@ -188,7 +205,7 @@ struct Ex8Sizes {
 constexpr int kEx8SmallRows = 8;  // rows of the few-row path: one column each of an m16n8 tile
 bool ex8_small(int H, int I, int t, int K);
 Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size);
-cudaError_t launch_ex8_small(const Ex8P &p, int n_sms, cudaStream_t st);
+cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_ex8_combine(const Ex8P &p, int n_sms, cudaStream_t st);
 

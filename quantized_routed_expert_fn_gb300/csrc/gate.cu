@@ -41,10 +41,15 @@ __device__ __forceinline__ float load_logit(const GateP &P, int row, int e) {
   if (P.bf16) return __uint_as_float((uint32_t)static_cast<const uint16_t *>(P.logits)[i] << 16);
   return static_cast<const float *>(P.logits)[i];
 }
-// How far a 32-bit selection score may be from the definition's: scores are
-// at most 1, their exponential, sum and quotient are good to 2^-21 together,
-// the sum with the bias to 2^-24 of itself.
-__device__ __forceinline__ float tol_of(float sel) { return 9.5367431640625e-7f * (1.f + fabsf(sel)); }
+// How far a 32-bit selection score may be from the definition's, by the fast
+// exponential (2 + 1.16 |x| ulp) and quotient (2 ulp).  Sigmoid: the score
+// moves by p (1 - p) of the exponential's error, 0.6 ulp of 1 at most, and by
+// the quotient's 2: below 2^-21 together.  Softmax: p |x| < 0.4 and the sum's
+// error, at most that of the mean |x| < ln 1024, weigh in: below 2^-20.  The
+// sum with the bias adds 2^-24 of itself.
+__device__ __forceinline__ float tol_of(float sel, bool sigmoid) {
+  return (sigmoid ? 4.76837158203125e-7f : 9.5367431640625e-7f) + 1.1920928955078125e-7f * fabsf(sel);
+}
 
 // unsigned key in the order of d (0 is left for what is masked)
 __device__ __forceinline__ uint64_t okey64(double d) {
@@ -199,8 +204,10 @@ __device__ __forceinline__ void load_row(const GateP &P, int row, int e0, float 
 template <int C, bool VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_constant__ GateP P) {
   extern __shared__ uint64_t key64[];  // [kGateWarps][E]: rows decided in 64 bits
+  __shared__ uint2 picks[kGateWarps][32];  // the choices of a row: key, id
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = P.E, K = P.K, e0 = lane * C;
+  const unsigned below = (1u << lane) - 1u;
   const bool biased = P.bias != nullptr;
   const bool pair_groups = P.ng > 1 && P.group_top == 2;
   // scores: needed for the bias, the sums of a group, and the full softmax's weights
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
   const int lpg = P.ng > 1 && P.gs % C == 0 && 32 % (P.gs / C) == 0 ? P.gs / C : 0;  // lanes of a group
   float bias[C];
 #pragma unroll
-  for (int i = 0; i < C; i++) bias[i] = biased && e0 + i < E ? P.bias[e0 + i] : 0.f;
+  for (int i = 0; i < C; i++) bias[i] = biased && e0 + i < E ? fmaxf(P.bias[e0 + i], -kInf) : 0.f;  // NaN: -inf
 
   const int step = gridDim.x * kGateWarps;
   float next[C];
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     for (int i = 0; i < C; i++) {
       float v = l[i];
       if (biased) v = score_of(v) + bias[i];
-      key[i] = l[i] > -kInf && bias[i] > -kInf ? okey(v) : 0u;
+      key[i] = l[i] > -kInf && v > -kInf ? okey(v) : 0u;
     }
     // the lane's best two
     uint32_t b1 = 0, b2 = 0;
@@ -307,13 +314,13 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         const uint32_t hi = __reduce_max_sync(FULLM, mine < P.ng && !kept && top1 ? okey(score) : 0u);
         if (lo != 0xffffffffu && hi) {
           const float a = of_key(lo), b = of_key(hi);
-          if (a - b <= 2.f * (tol_of(a) + tol_of(b))) {
+          if (a - b <= 2.f * (tol_of(a, P.sigmoid) + tol_of(b, P.sigmoid))) {
             bool close = false;
             for (int j = 0; j < P.ng; j++) {
               const float o = __shfl_sync(FULLM, score, j * lanes);
               const uint32_t o1 = __shfl_sync(FULLM, top1, j * lanes), o2 = __shfl_sync(FULLM, top2, j * lanes);
               const int ok = __shfl_sync(FULLM, kept ? 1 : 0, j * lanes);
-              if (kept && !ok && top1 && o1 && score - o <= 2.f * (tol_of(o) + tol_of(score)))
+              if (kept && !ok && top1 && o1 && score - o <= 2.f * (tol_of(o, P.sigmoid) + tol_of(score, P.sigmoid)))
                 close |= biased || o1 != top1 || o2 != top2;
             }
             near = __any_sync(FULLM, close);
@@ -343,13 +350,15 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
     uint32_t mykey = 0, taken = 0;
     bool second = true;  // (b2, i2) is the best after (b1, i1)
     if (!near) {
-      for (int r = 0; r < K; r++) {
+      int r = 0;
+      for (; r < K; r++) {
         const uint32_t mx = __reduce_max_sync(FULLM, b1);
         if (mx == 0) break;
-        const int src = __ffs(__ballot_sync(FULLM, b1 == mx)) - 1;
-        const int id = __shfl_sync(FULLM, e0 + i1, src);
-        if (lane == r) mine = id, mykey = mx;
-        if (lane == src) {
+        // the first lane that has it: the lowest id
+        const bool has = b1 == mx;
+        const unsigned who = __ballot_sync(FULLM, has);
+        if (has && (who & below) == 0) {
+          picks[warp][r] = make_uint2(mx, (uint32_t)(e0 + i1));
           taken |= 1u << i1;
           if (second) {
             b1 = b2, i1 = i2, second = false;
@@ -362,7 +371,10 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
             }
           }
         }
+        __syncwarp();
       }
+      if (lane < r) mykey = picks[warp][lane].x, mine = (int)picks[warp][lane].y;
+      __syncwarp();
     }
     float lg = -kInf;
     if (biased) {
@@ -372,17 +384,17 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         // last of them: two that are the same numbers are in order by their ids
         const float b = mine >= 0 ? P.bias[mine] : 0.f, sel = of_key(mykey);
         const float ps = __shfl_up_sync(FULLM, sel, 1), pl = __shfl_up_sync(FULLM, lg, 1), pb = __shfl_up_sync(FULLM, b, 1);
-        bool c = lane > 0 && mine >= 0 && ps - sel <= tol_of(ps) + tol_of(sel) && !(pl == lg && pb == b);
+        bool c = lane > 0 && mine >= 0 && ps - sel <= tol_of(ps, P.sigmoid) + tol_of(sel, P.sigmoid) && !(pl == lg && pb == b);
         const float ls = __shfl_sync(FULLM, sel, K - 1), ll = __shfl_sync(FULLM, lg, K - 1), lb = __shfl_sync(FULLM, b, K - 1);
         const bool full = __shfl_sync(FULLM, mine, K - 1) >= 0;  // (fewer than K: nothing is left)
         const float v1 = of_key(b1);
         unsigned reach = 0;  // what was left within reach of the last
-        if (__any_sync(FULLM, full && b1 && ls - v1 <= tol_of(ls) + tol_of(v1))) {
+        if (__any_sync(FULLM, full && b1 && ls - v1 <= tol_of(ls, P.sigmoid) + tol_of(v1, P.sigmoid))) {
 #pragma unroll
           for (int i = 0; i < C; i++)
             if (key[i] && !((taken >> i) & 1u)) {
               const float v = of_key(key[i]);
-              if (ls - v <= tol_of(ls) + tol_of(v)) {
+              if (ls - v <= tol_of(ls, P.sigmoid) + tol_of(v, P.sigmoid)) {
                 reach |= 1u << i;
                 c |= !(l[i] == ll && bias[i] == lb);
               }

@@ -392,6 +392,8 @@ EX = [  # t, H, I, E, k, x type, out type
     (9, 256, 128, 8, 2, "f32", "f32"), (12, 384, 256, 64, 3, "f32", "bf16"), (40, 256, 256, 3, 2, "bf16", "bf16"),
     (150, 128, 128, 2, 1, "f32", "f32"), (2, 1152, 1152, 6, 2, "f32", "f32"), (8, 640, 128, 20, 8, "bf16", "bf16"),
     (7, 1408, 896, 9, 3, "f32", "bf16"), (8, 128, 512, 64, 32, "f32", "f32"),
+    (2, 4096, 256, 40, 16, "f32", "f32"), (1, 6144, 128, 12, 12, "bf16", "f32"), (8, 512, 1024, 70, 9, "f32", "bf16"),
+    (3, 256, 2048, 24, 8, "f32", "f32"),
 ]
 
 
