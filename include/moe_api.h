@@ -298,7 +298,7 @@ typedef struct {
  *   logits   [t] rows of n_experts values of logit_dtype, ld elements apart
  *   bias     [n_experts] float32, or NULL
  *   topk_idx [t][top_k] uint32, topk_w [t][top_k] float32
- * t may be 0.  Needs no workspace; has no device-side failures. */
+ * t 0..2^30.  Needs no workspace; has no device-side failures. */
 int moe_gate(const moe_gate_cfg *cfg, const void *logits, int logit_dtype, int64_t ld, const float *bias, int t,
              uint32_t *topk_idx, float *topk_w, moe_stream_t stream);
 
@@ -309,14 +309,16 @@ int moe_gate(const moe_gate_cfg *cfg, const void *logits, int logit_dtype, int64
  * [ceil(rows / 128)] rows, lds apart.  A block's exponent is the least with
  * max |x| <= 448 * 2^e over its finite values (0 for a block of zeros, never
  * below -127); values are rounded to nearest, ties to even.  Infinities and
- * NaN become NaN (0x7f) and do not move the scale. */
+ * NaN become NaN (0x7f) and do not move the scale.  rows and cols up to 2^30
+ * (block_rows 128: 65535 blocks of rows). */
 int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int block_rows, uint8_t *q, int64_t ldq,
                uint8_t *s, int64_t lds, moe_stream_t stream);
 
 /* out[r][j] = sum over k of a[r][k] b[j][k], scaled: the block-scaled 8-bit
  * matrix product, accumulated in fp32 and rounded once to out_dtype.
  *   a    e4m3 [t] rows of k, lda bytes apart; 16-byte aligned, lda % 16 == 0
- *   sa   E8M0 [t] rows of ceil(k / 128), lds bytes apart; 4-byte aligned, lds % 4 == 0
+ *   sa   E8M0 [t] rows of ceil(k / 128), lds bytes apart; 4-byte aligned, lds % 4 == 0,
+ *        all t * lds bytes readable
  *   b    e4m3 [max(n_groups, 1)][n][k], 16-byte aligned; sb E8M0 [..][ceil(n / 128)][ceil(k / 128)]
  *   out  [t] rows of n, ldo elements apart; must not overlap the inputs
  *   offs NULL (one weight matrix for every row, n_groups 0), or device int32
@@ -326,7 +328,8 @@ int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int 
  *        not ascend or leave 0..t are reported (MOE_EDEVICE) and nothing is
  *        written.
  *   flags 0 (MOE_TEST_WITHHOLD: failure-detection test, grouped form only)
- * k % 16 == 0; n_groups <= 1024; t may be 0. */
+ * k % 16 == 0, up to 2^24; n_groups <= 1024; t 0..2^30.  The waits inside are
+ * bounded as everywhere (MOE_TIMEOUT_MS, here at least 1 ms): MOE_ETIMEOUT. */
 int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t, const uint8_t *b, const uint8_t *sb,
             int n, int k, void *out, int out_dtype, int64_t ldo, const int32_t *offs, int n_groups, uint32_t flags,
             int *dev_status, moe_stream_t stream);
@@ -345,12 +348,13 @@ typedef struct {
  *   x8 = quant8(x);  (g, u) = mm8 with gate_up;  h8 = quant8(silu(g) * u);
  *   out[r] = sum over j of topk_w[r][j] * (mm8 of h8 with down of expert topk_idx[r][j])
  * in fp32 between the roundings to 8 bits; for more than a few rows the
- * weighted expert outputs are held in out's type before they are summed (in
- * the order of j).  Ids >= n_experts (0xffffffff, or another rank's experts
+ * experts' outputs are held in out's type before they are weighted and summed
+ * (in the order of j).  Ids >= n_experts (0xffffffff, or another rank's experts
  * after the caller subtracted its first id) contribute nothing; a row without
  * experts gives zeros; an expert twice in a row counts twice.
  *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype, must not overlap x
- *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned
+ *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned;
+ *        calls whose executions overlap need one each
  * top_k 1..32; t 0..1048576 with t * top_k < 2^31 / 2. */
 int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const uint32_t *topk_idx,
                  const float *topk_w, int top_k, void *out, int out_dtype, void *work, size_t work_bytes,

@@ -12,6 +12,7 @@ using moe::fail;
 using moe::overlap;
 
 constexpr int kMaxRows = 1 << 20;
+constexpr int kMaxCount = 1 << 30;  // row and column indices step within 32 bits
 
 int dtype_size(int d) { return d == MOE_F32 ? 4 : (d == MOE_BF16 ? 2 : 0); }
 
@@ -63,15 +64,17 @@ int moe_gate(const moe_gate_cfg *c, const void *logits, int logit_dtype, int64_t
     return fail(MOE_ESHAPE, "top_k %u outside 1..min(32, %u experts of the chosen groups)", c->top_k, avail);
   const int size = dtype_size(logit_dtype);
   if (!size) return fail(MOE_EINVAL, "unknown logit_dtype %d", logit_dtype);
-  if (t < 0) return fail(MOE_EINVAL, "t %d is negative", t);
+  if (t < 0 || t > kMaxCount) return fail(MOE_EINVAL, "t %d outside 0..2^30", t);
   if (t == 0) return MOE_OK;
   if (!logits || !topk_idx || !topk_w) return fail(MOE_EINVAL, "logits, topk_idx and topk_w are required");
   if (ld < (int64_t)c->n_experts) return fail(MOE_ESHAPE, "ld %lld below n_experts", (long long)ld);
   if (((uintptr_t)logits % size) || (((uintptr_t)topk_idx | (uintptr_t)topk_w | (uintptr_t)bias) & 3u))
     return fail(MOE_EALIGN, "misaligned pointer");
   const size_t nl = span(t, c->n_experts, ld, size), no = (size_t)t * c->top_k * 4;
-  if (overlap(logits, nl, topk_idx, no) || overlap(logits, nl, topk_w, no) || overlap(topk_idx, no, topk_w, no))
-    return fail(MOE_EINVAL, "the outputs overlap the logits or one another");
+  const size_t nb = bias ? (size_t)c->n_experts * 4 : 0;
+  if (overlap(logits, nl, topk_idx, no) || overlap(logits, nl, topk_w, no) || overlap(topk_idx, no, topk_w, no) ||
+      (bias && (overlap(bias, nb, topk_idx, no) || overlap(bias, nb, topk_w, no))))
+    return fail(MOE_EINVAL, "the outputs overlap the inputs or one another");
   moe::GateP p{};
   p.logits = logits, p.bf16 = logit_dtype == MOE_BF16, p.ld = ld, p.bias = bias;
   p.t = t, p.E = (int)c->n_experts, p.K = (int)c->top_k;
@@ -92,7 +95,8 @@ int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int 
   const int size = dtype_size(x_dtype);
   if (!size) return fail(MOE_EINVAL, "unknown x_dtype %d", x_dtype);
   if (block_rows != 1 && block_rows != 128) return fail(MOE_ESHAPE, "block_rows %d is neither 1 nor 128", block_rows);
-  if (rows < 0 || cols < 1) return fail(MOE_ESHAPE, "rows %d / cols %d", rows, cols);
+  if (rows < 0 || rows > kMaxCount || cols < 1 || cols > kMaxCount)
+    return fail(MOE_ESHAPE, "rows %d outside 0..2^30 or cols %d outside 1..2^30", rows, cols);
   if (rows == 0) return MOE_OK;
   const int64_t cb = ((int64_t)cols + 127) / 128, rb = ((int64_t)rows + block_rows - 1) / block_rows;
   if (!x || !q || !s) return fail(MOE_EINVAL, "x, q and s are required");
@@ -119,7 +123,7 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
   const int size = dtype_size(out_dtype);
   if (!size) return fail(MOE_EINVAL, "unknown out_dtype %d", out_dtype);
   if (flags & ~(uint32_t)MOE_TEST_WITHHOLD) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
-  if (t < 0 || n < 1 || k < 1) return fail(MOE_ESHAPE, "t %d, n %d, k %d", t, n, k);
+  if (t < 0 || t > kMaxCount || n < 1 || k < 1) return fail(MOE_ESHAPE, "t %d, n %d, k %d", t, n, k);
   if (k % 16) return fail(MOE_ESHAPE, "k %d must be a multiple of 16", k);
   if (k > 1 << 24) return fail(MOE_ESHAPE, "k %d above 2^24", k);
   if (!offs != !n_groups || n_groups < 0 || n_groups > 1024)
@@ -211,6 +215,9 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
     return fail(MOE_EINVAL, "out overlaps the ids or weights");
   const moe::Ex8Sizes z = moe::ex8_sizes(H, E, I, t, top_k, os);
   if (work_bytes < z.total) return fail(MOE_ENOSPACE, "work holds %zu bytes, %zu needed", work_bytes, z.total);
+  if (overlap(work, z.total, x, (size_t)t * H * xs) || overlap(work, z.total, out, no) ||
+      overlap(work, z.total, topk_idx, ni) || overlap(work, z.total, topk_w, ni))
+    return fail(MOE_EINVAL, "work overlaps x, out, the ids or the weights");
   moe::Ex8P p{};
   p.H = H, p.E = E, p.I = I, p.t = t, p.K = top_k;
   p.gu = L->gate_up, p.gus = L->gate_up_s, p.dn = L->down, p.dns = L->down_s;
@@ -228,6 +235,7 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   if (moe::ex8_small(H, I, t, top_k)) {
     p.h32 = (float *)take(z.h32);
     p.timeout_ns = moe::timeout_ns();
+    if (p.timeout_ns < 1000000) p.timeout_ns = 1000000;  // as in moe_mm8
     e = moe::launch_ex8_small(p, n_sms, st);
     return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   }

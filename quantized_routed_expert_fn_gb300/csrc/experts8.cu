@@ -716,8 +716,9 @@ cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st) {
   const DnLay d = p.dl = dn_layout(p.I, p.t * p.K);
   auto f = p.x_bf16 ? ex8_gate_up<true> : ex8_gate_up<false>;
   auto h = p.out_bf16 ? ex8_down<true> : ex8_down<false>;
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.total);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(h, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)d.total);
+  // the most any launch asks for (another host thread may launch them too)
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemCap);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(h, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemCap);
   if (e != cudaSuccess) return e;
   const int items = p.t * p.K * (p.I / 8);
   f<<<(unsigned)(items < n_sms ? items : n_sms), kGuThreads, l.total, st>>>(p);

@@ -618,7 +618,10 @@ cudaError_t launch_tc(Mm8P &p, int grid, bool pdl, cudaStream_t st) {
     ok = ok && make_map8(&p.tm_a[i], p.a, p.k, p.t, p.lda, (uint32_t)((i + 1) * LY::unit), KB);
   if (!ok) return cudaErrorNotSupported;
   const int smem = LY::offRing + p.stages * p.stage + 1024;
-  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the most any launch asks for: another host thread's launch of the same
+  // kernel may stand between this and the launch below
+  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       LY::offRing + LY::room + 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[2];
   int n = 0;

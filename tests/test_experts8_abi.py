@@ -32,6 +32,7 @@ def _gate(m, t=4, dtype=0, ld=64, logits=A, idx=B, w=C, bias=None, **over):
     (dict(n_groups=32, top_groups=1, top_k=3), -2), (dict(dtype=2), -1), (dict(t=-1), -1), (dict(ld=63), -2),
     (dict(logits=None), -1), (dict(idx=None), -1), (dict(w=None), -1), (dict(logits=A + 2), -3), (dict(idx=B + 2), -3),
     (dict(bias=D + 1), -3), (dict(idx=A), -1), (dict(w=B), -1),
+    (dict(bias=B), -1), (dict(t=(1 << 30) + 1), -1),
 ])
 def test_gate_refusals(m, over, code):
     assert _gate(m, **over) == code, m.last_error()
@@ -51,7 +52,7 @@ def _quant(m, x=A, dtype=0, ldx=256, rows=4, cols=256, br=1, q=O, ldq=256, s=S, 
     (dict(dtype=7), -1), (dict(br=64), -2), (dict(rows=-1), -2), (dict(cols=0), -2), (dict(x=None), -1),
     (dict(q=None), -1), (dict(s=None), -1), (dict(ldx=255), -2), (dict(ldq=255), -2), (dict(lds=1), -2),
     (dict(x=A + 2), -3), (dict(q=A), -1), (dict(s=A + 16), -1), (dict(s=O), -1),
-    (dict(rows=128 * 65535 + 1, br=128, ldx=256), -2),
+    (dict(rows=128 * 65535 + 1, br=128, ldx=256), -2), (dict(rows=(1 << 30) + 1), -2), (dict(cols=(1 << 30) + 1), -2),
 ])
 def test_quant8_refusals(m, over, code):
     assert _quant(m, **over) == code, m.last_error()
@@ -68,6 +69,7 @@ def _mm8(m, a=A, lda=256, sa=B, lds=4, t=64, b=C, sb=D, n=128, k=256, out=O, dt=
     (dict(lda=240), -2), (dict(lds=0), -2), (dict(ldo=127), -2), (dict(a=A + 8), -3), (dict(lda=264), -3),
     (dict(b=C + 4), -3), (dict(sa=B + 1), -3), (dict(lds=6), -3), (dict(out=O + 2), -3), (dict(offs=W + 2, g=2), -3),
     (dict(out=A + 64), -1), (dict(out=C), -1), (dict(out=D - 16), -1), (dict(n=1 << 22, g=1024, offs=W, ldo=1 << 22), -2),
+    (dict(t=(1 << 30) + 1), -2),
 ])
 def test_mm8_refusals(m, over, code):
     assert _mm8(m, **over) == code, m.last_error()
@@ -95,6 +97,7 @@ def test_experts8_refuses_bad_layers(m, layer, code):
     (dict(x=None), -1), (dict(idx=None), -1), (dict(w=None), -1), (dict(out=None), -1), (dict(work=None), -1),
     (dict(st=None), -1), (dict(x=O + 4), -3), (dict(out=O + (1 << 20) + 8), -3), (dict(idx=W + 1), -3),
     (dict(work=S + 16), -3), (dict(wb=16), -7), (dict(out=O + 64), -1), (dict(out=W), -1),
+    (dict(work=O), -1), (dict(x=S), -1),
 ])
 def test_experts8_refuses_bad_calls(m, over, code):
     assert _ex(m, **over) == code, m.last_error()

@@ -563,6 +563,49 @@ def test_other_stream_and_repeated_calls(moe):
         assert torch.equal(o, outs[0])
 
 
+def test_calls_from_two_threads_and_streams(moe):
+    """Calls of different sizes from two host threads on their own streams, with their own workspaces, at once."""
+    import threading
+    g = np.random.default_rng(6)
+    e, h, i, k = 12, 512, 256, 3
+    L = moe.Layer8(*[cuda(v) for v in make_experts(g, e, h, i)])
+    work = []
+    for t in (3, 40, 130, 700):
+        x = cuda(g.normal(size=(t, h)).astype(np.float32))
+        idx = cuda(np.stack([g.choice(e, size=k, replace=False) for _ in range(t)]).astype(np.int32))
+        w = cuda(g.random(size=(t, k)).astype(np.float32))
+        a, sa, b, sb = operands(g, t, 300, 768)
+        work.append(dict(x=x, idx=idx, w=w, a=cuda(a), sa=padded(sa, 8, 255), b=cuda(b), sb=cuda(sb)))
+    torch.cuda.synchronize()
+
+    def run(out, order):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for n in order:
+                d, t = work[n], work[n]["x"].shape[0]
+                ws = moe.alloc_workspace(moe.experts8_workspace(L, t, k))
+                o, p = torch.empty(t, h, device="cuda"), torch.empty(t, 300, device="cuda")
+                st = torch.zeros(2, dtype=torch.int32, device="cuda")
+                moe.experts8(L, d["x"], d["idx"], d["w"], o, ws, st[:1])
+                moe.mm8(d["a"], d["sa"], d["b"], d["sb"], p, st[1:])
+                out.append((n, o, p, st, ws))
+        s.synchronize()
+
+    ref = []
+    run(ref, range(4))
+    got = [[], []]
+    threads = [threading.Thread(target=run, args=(got[0], [0, 3, 1, 2] * 10)),
+               threading.Thread(target=run, args=(got[1], [2, 0, 3, 1] * 10))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert [len(v) for v in got] == [40, 40]
+    for n, o, p, st, _ in got[0] + got[1]:
+        assert st.tolist() == [0, 0]
+        assert torch.equal(o, ref[n][1]) and torch.equal(p, ref[n][2])
+
+
 def test_binding_refusals(moe):
     z = lambda *s, d=torch.uint8: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
     st = z(1, d=torch.int32)
