@@ -254,8 +254,8 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   d.n = H, d.k = I, d.nk = I / 128, d.nb = H / 128;
   d.out = p.y, d.ldo = H, d.hs = nullptr;
   const int yk = p.out_bf16 ? moe::kOutBf16 : moe::kOutF32;
-  e = moe::launch_ex8_group(p, n_sms, st);
-  if (e == cudaSuccess) e = moe::launch_mm8_tc(u, moe::kOutSilu8, n_sms, false, st);
+  e = moe::launch_ex8_group(p, st);
+  if (e == cudaSuccess) e = moe::launch_mm8_tc(u, moe::kOutSilu8, n_sms, true, st);
   if (e == cudaSuccess) e = moe::launch_mm8_tc(d, yk, n_sms, true, st);
   if (e == cudaSuccess) e = moe::launch_ex8_combine(p, n_sms, st);
   if (e != cudaSuccess) return fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));

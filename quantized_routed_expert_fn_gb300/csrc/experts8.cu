@@ -526,53 +526,12 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
 
 // ------------------------------------------------------------ many rows
 
-constexpr int kCountEntries = 1024;
+constexpr int kCountThreads = 1024, kCountEntries = 4 * kCountThreads;  // of a block
 
-// Place of every entry within its expert's rows.  A block counts its entries
-// in shared memory and takes a run of places per expert; which places an
-// entry gets depends on the order of the blocks, its results do not.  The
-// last block to finish scans the counts.
-__global__ void __launch_bounds__(256) ex8_count(const __grid_constant__ Ex8P P) {
-  extern __shared__ int hist[];  // [E]
-  __shared__ int last, part[9];
-  const int tid = threadIdx.x, lane = tid & 31, n = P.t * P.K, E = P.E;
-  if (blockIdx.x == 0 && tid == 0) *P.status = 0;
-  for (int e = tid; e < E; e += 256) hist[e] = 0;
-  __syncthreads();
-  uint32_t ex[4];
-  int rank[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int j = blockIdx.x * kCountEntries + i * 256 + tid;
-    ex[i] = j < n ? P.idx[j] : 0xffffffffu;
-    rank[i] = ex[i] < (uint32_t)E ? atomicAdd(&hist[ex[i]], 1) : 0;
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += 256) {
-    const int c = hist[e];
-    hist[e] = c ? atomicAdd(&P.counts[e], c) : 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int j = blockIdx.x * kCountEntries + i * 256 + tid;
-    if (j < n) P.place[j] = ex[i] < (uint32_t)E ? hist[ex[i]] + rank[i] : -1;
-  }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(&P.counts[E], 1) == (int)gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // four experts a thread: exclusive scan of the counts
-  int c[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int e = 4 * tid + i;
-    c[i] = e < E ? __ldcg(&P.counts[e]) : 0;
-    sum += c[i];
-  }
-  int x = sum;
+// Exclusive scan of the E counts into offs, by one block (E <= kCountThreads).
+__device__ void scan_counts(const Ex8P &P, int c, int *part) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  int x = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(FULLM, x, o);
@@ -580,21 +539,72 @@ __global__ void __launch_bounds__(256) ex8_count(const __grid_constant__ Ex8P P)
   }
   if (lane == 31) part[tid >> 5] = x;
   __syncthreads();
-  int base = x - sum;
-  for (int w = 0; w < (tid >> 5); w++) base += part[w];
+  if (tid < 32) {
+    int p = part[tid];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULLM, p, o);
+      if (lane >= o) p += y;
+    }
+    part[tid] = p;
+  }
+  __syncthreads();
+  const int base = x - c + (tid >= 32 ? part[(tid >> 5) - 1] : 0);
+  if (tid < P.E) P.offs[tid] = base;
+  if (tid == kCountThreads - 1) P.offs[P.E] = base + c;
+}
+
+// Place of every entry within its expert's rows.  A block counts its entries
+// in shared memory; one block alone is done then, several take runs of places
+// from global counters (zeroed before), and the last to finish scans them.
+// Which places an entry gets depends on the order of the atomics, its results
+// do not.
+__global__ void __launch_bounds__(kCountThreads) ex8_count(const __grid_constant__ Ex8P P) {
+  pdl_launch_next();
+  extern __shared__ int hist[];  // [E]
+  __shared__ int last, part[32];
+  const int tid = threadIdx.x, n = P.t * P.K, E = P.E;
+  if (blockIdx.x == 0 && tid == 0) *P.status = 0;
+  uint32_t ex[4];
+  int rank[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int e = 4 * tid + i;
-    if (e <= E) P.offs[e] = base;
-    base += c[i];
+    const int j = blockIdx.x * kCountEntries + i * kCountThreads + tid;
+    ex[i] = j < n ? P.idx[j] : 0xffffffffu;
   }
-  if (E == 1024 && tid == 255) P.offs[E] = base;
+  if (tid < E) hist[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; i++) rank[i] = ex[i] < (uint32_t)E ? atomicAdd(&hist[ex[i]], 1) : 0;
+  __syncthreads();
+  const int mine = tid < E ? hist[tid] : 0;
+  if (gridDim.x > 1) {
+    if (tid < E) hist[tid] = mine ? atomicAdd(&P.counts[tid], mine) : 0;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int j = blockIdx.x * kCountEntries + i * kCountThreads + tid;
+    if (j < n) P.place[j] = ex[i] < (uint32_t)E ? (gridDim.x > 1 ? hist[ex[i]] : 0) + rank[i] : -1;
+  }
+  if (gridDim.x == 1) {
+    scan_counts(P, mine, part);
+    return;
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(&P.counts[E], 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  scan_counts(P, tid < E ? __ldcg(&P.counts[tid]) : 0, part);
 }
 
 // x rows -> e4m3, written to the places of their entries: a warp per row,
 // 16 values a lane (eight lanes a block), 16-byte stores.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) ex8_scatter(const __grid_constant__ Ex8P P) {
+  pdl_launch_next();
   const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= P.t) return;
   const int K = P.K, H = P.H;
@@ -610,7 +620,8 @@ __global__ void __launch_bounds__(kThreads) ex8_scatter(const __grid_constant__ 
       for (int j = 0; j < 8; j++) x[j] = lo[j], x[8 + j] = hi[j];
     }
   };
-  load(v[0], lane * 16);
+  load(v[0], lane * 16);  // x is older than the previous kernel, the places are its
+  pdl_wait_prev();
   int at = -1;
   if (lane < K) {
     const int j = row * K + lane, pl = P.place[j];
@@ -637,7 +648,10 @@ __global__ void __launch_bounds__(kThreads) ex8_scatter(const __grid_constant__ 
 
 // out[row] = sum over the row's entries, in order, of weight * y: a warp per
 // row and 256 columns, eight a lane.
-template <bool BF16>
+// U entries' loads are in flight at once: one or two where many warps hide
+// the latency (five took 54 us instead of 35 at 4096 x 10 rows of 2048, for
+// want of warps), eight where there are few.
+template <bool BF16, int U>
 __global__ void __launch_bounds__(256) ex8_combine(const __grid_constant__ Ex8P P) {
   pdl_wait_prev();
   const int lane = threadIdx.x & 31, K = P.K, H = P.H, segs = (H + 255) / 256;
@@ -647,15 +661,37 @@ __global__ void __launch_bounds__(256) ex8_combine(const __grid_constant__ Ex8P 
     const int at = lane < K ? P.place[(size_t)row * K + lane] : -1;
     const float wt = lane < K ? P.w[(size_t)row * K + lane] : 0.f;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if constexpr (U > 1) {
+      for (int j0 = 0; j0 < K; j0 += U) {
+        float v[U][8], w[U];
+  #pragma unroll
+        for (int j = 0; j < U; j++) {
+          const int a = __shfl_sync(FULLM, at, (j0 + j) & 31);
+          w[j] = __shfl_sync(FULLM, wt, (j0 + j) & 31);
+          const bool on = j0 + j < K && a >= 0 && c < H;
+          if (on) load_x8<BF16>(P.y, (int64_t)a * H + c, v[j]);
+          if (!on) {
+            w[j] = 0.f;
+  #pragma unroll
+            for (int k = 0; k < 8; k++) v[j][k] = 0.f;
+          }
+        }
+  #pragma unroll
+        for (int j = 0; j < U; j++)
+  #pragma unroll
+          for (int k = 0; k < 8; k++) s[k] += w[j] * v[j][k];
+      }
+    } else {
 #pragma unroll 2
-    for (int j = 0; j < K; j++) {
-      const int a = __shfl_sync(FULLM, at, j);
-      const float w = __shfl_sync(FULLM, wt, j);
-      if (a < 0 || c >= H) continue;
-      float v[8];
-      load_x8<BF16>(P.y, (int64_t)a * H + c, v);
+      for (int j = 0; j < K; j++) {
+        const int a = __shfl_sync(FULLM, at, j);
+        const float w = __shfl_sync(FULLM, wt, j);
+        if (a < 0 || c >= H) continue;
+        float v[8];
+        load_x8<BF16>(P.y, (int64_t)a * H + c, v);
 #pragma unroll
-      for (int k = 0; k < 8; k++) s[k] += w * v[k];
+        for (int k = 0; k < 8; k++) s[k] += w * v[k];
+      }
     }
     if (c >= H) continue;
     if (BF16) {
@@ -726,22 +762,25 @@ cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st) {
   return launch_pdl(h, dim3((unsigned)(p.H / 16)), 32 * kDownWarps + 32, d.total, st, p);
 }
 
-cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st) {
-  (void)n_sms;
-  cudaError_t e = cudaMemsetAsync(p.counts, 0, (size_t)(p.E + 1) * 4, st);
+cudaError_t launch_ex8_group(const Ex8P &p, cudaStream_t st) {
+  const int n = p.t * p.K, blocks = (n + kCountEntries - 1) / kCountEntries;
+  if (blocks > 1) {
+    cudaError_t e = cudaMemsetAsync(p.counts, 0, (size_t)(p.E + 1) * 4, st);
+    if (e != cudaSuccess) return e;
+  }
+  ex8_count<<<(unsigned)blocks, kCountThreads, (size_t)p.E * 4, st>>>(p);
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int n = p.t * p.K;
-  ex8_count<<<(unsigned)((n + kCountEntries - 1) / kCountEntries), 256, (size_t)p.E * 4, st>>>(p);
-  const unsigned grid = (unsigned)((p.t + kWarps - 1) / kWarps);
-  if (p.x_bf16) ex8_scatter<true><<<grid, kThreads, 0, st>>>(p);
-  else ex8_scatter<false><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(p.x_bf16 ? ex8_scatter<true> : ex8_scatter<false>, dim3((unsigned)((p.t + kWarps - 1) / kWarps)), kThreads,
+                    0, st, p);
 }
 
 cudaError_t launch_ex8_combine(const Ex8P &p, int n_sms, cudaStream_t st) {
   const int64_t need = ((int64_t)p.t * ((p.H + 255) / 256) + 7) / 8, cap = (int64_t)n_sms * 8;
-  return launch_pdl(p.out_bf16 ? ex8_combine<true> : ex8_combine<false>, dim3((unsigned)(need < cap ? need : cap)), 256, 0,
-                    st, p);
+  const bool few = need <= 2 * n_sms;
+  auto f = p.out_bf16 ? (few ? ex8_combine<true, 8> : ex8_combine<true, 1>)
+                      : (few ? ex8_combine<false, 8> : ex8_combine<false, 1>);
+  return launch_pdl(f, dim3((unsigned)(need < cap ? need : cap)), 256, 0, st, p);
 }
 
 }  // namespace moe

@@ -206,7 +206,7 @@ constexpr int kEx8SmallRows = 8;  // rows of the few-row path: one column each o
 bool ex8_small(int H, int I, int t, int K);
 Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size);
 cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st);
-cudaError_t launch_ex8_group(const Ex8P &p, int n_sms, cudaStream_t st);
+cudaError_t launch_ex8_group(const Ex8P &p, cudaStream_t st);
 cudaError_t launch_ex8_combine(const Ex8P &p, int n_sms, cudaStream_t st);
 
 }  // namespace moe
