@@ -16,11 +16,18 @@
 //            quantises h while its weights arrive; sums meet in a fixed order
 // An item's chain of wait, loads, MMAs and arrival takes a warp some 1000
 // cycles, in which HBM brings 23 KB to an SM: so several items are worked on
-// at once, and two k blocks' MMAs are interleaved.
+// at once, and two k blocks' MMAs are interleaved.  That rate and the
+// launches bound these kernels, not HBM.  One row, 8 of 128 experts, 2048 x
+// 768: 12 us for the 25 MB of gate_up, 10 for the 13 MB of down, 16 together,
+// the second's start hidden; four rows, 39 of 512 experts, 2048 x 512: 21 and
+// 20, 37 together.
+//
 // Many rows: the entries are grouped by expert (count, scan), x is quantised
 // once per row and written to its entries' places, mm8_tc computes h8 and
 // the outputs y, and a last kernel sums a row's weighted outputs in the
-// order of its entries.
+// order of its entries.  4096 rows, 10 of 512 experts by Zipf(1.1), 2048 x
+// 512, alone: count 7, scatter 20 (101 MB), gate_up 209 (1.16 GB read, 5.5
+// TB/s), down 149 (558 MB read, 168 written), sum 36 us (184 MB).
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
