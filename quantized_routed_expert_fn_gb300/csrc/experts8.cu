@@ -365,11 +365,12 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
         wg = sg[kb] | (uint32_t)sg[k2] << 8, wu = sg[up_s + kb] | (uint32_t)sg[up_s + k2] << 8;
       }
       const float fg = e8m0_f(wg & 255u), fu = e8m0_f(wu & 255u), x0 = have0 ? sx0[kb] : 0.f, x1 = have1 ? sx1[kb] : 0.f;
-      acc.x += d[0] * x0 * fg, acc.y += d[1] * x1 * fg, acc.z += d[2] * x0 * fu, acc.w += d[3] * x1 * fu;
+      // the two powers of two first: scales far from 1 may cancel
+      acc.x += d[0] * (x0 * fg), acc.y += d[1] * (x1 * fg), acc.z += d[2] * (x0 * fu), acc.w += d[3] * (x1 * fu);
       if (two) {
         const float hg = e8m0_f(wg >> 8 & 255u), hu = e8m0_f(wu >> 8 & 255u);
         const float y0 = have0 ? sx0[k2] : 0.f, y1 = have1 ? sx1[k2] : 0.f;
-        acc.x += e[0] * y0 * hg, acc.y += e[1] * y1 * hg, acc.z += e[2] * y0 * hu, acc.w += e[3] * y1 * hu;
+        acc.x += e[0] * (y0 * hg), acc.y += e[1] * (y1 * hg), acc.z += e[2] * (y0 * hu), acc.w += e[3] * (y1 * hu);
       }
       wg >>= 16, wu >>= 16;
     }

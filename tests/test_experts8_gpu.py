@@ -301,6 +301,18 @@ def test_mm8_nan_and_wide_scales_stay_in_their_rows(moe, t):
     assert (np.abs(got - r)[~nan] <= tol[~nan] * 1.001).all()
 
 
+@pytest.mark.parametrize("shift", [114, -118])
+@pytest.mark.parametrize("t", [3, 20, 70])
+def test_mm8_scales_that_cancel(moe, t, shift):
+    """Row scales times 2^shift and weight scales times 2^-shift: the same numbers, bit for bit."""
+    g = np.random.default_rng(t)
+    a, sa, b, sb = operands(g, t, 140, 384)
+    sa = sa + 4  # 122 to 126
+    want, _ = run_mm8(moe, a, sa, b, sb, "f32")
+    got, _ = run_mm8(moe, a, (sa.astype(int) + shift).astype(np.uint8), b, (sb.astype(int) - shift).astype(np.uint8), "f32")
+    assert np.isfinite(want).all() and np.array_equal(got, want)
+
+
 GROUPS = [  # rows of each group, rows before, rows behind, n, k
     ([5], 0, 0, 128, 128), ([0, 3, 0, 0, 200, 1, 224, 225, 16, 0], 0, 13, 130, 272), ([1] * 40, 2, 0, 96, 2048),
     ([0, 0, 0], 0, 9, 64, 128), ([300, 17], 5, 40, 256, 512), ([2, 0] * 512, 0, 3, 16, 144), ([33, 31, 32, 47, 48, 49], 0, 0, 384, 1024),
@@ -443,6 +455,21 @@ def test_experts8_group_sizes_around_a_tile(moe):
     for _ in range(5):
         bad = (~(np.abs(run_experts(moe, ws, x, idx, w, "f32") - ref) <= allow)).any(1)
         assert not bad.any(), np.bincount(idx[bad, 0], minlength=e)
+
+
+@pytest.mark.parametrize("shift", [118, -100])
+@pytest.mark.parametrize("t", [4, 30])
+def test_experts8_scales_that_cancel(moe, t, shift):
+    """x times 2^shift through gate_up scales times 2^-shift: the same numbers, bit for bit."""
+    g = np.random.default_rng(t)
+    gu, gus, dn, dns = make_experts(g, 6, 256, 128)
+    gus = gus + 10  # 123, 124
+    x = g.normal(size=(t, 256)).astype(np.float32)
+    idx, w = np.stack([g.choice(6, size=2, replace=False) for _ in range(t)]), g.random(size=(t, 2)).astype(np.float32)
+    want = run_experts(moe, (gu, gus, dn, dns), cuda(x), idx, w, "f32")
+    x2, gus2 = (x * np.float32(2.0) ** shift).astype(np.float32), (gus.astype(int) - shift).astype(np.uint8)
+    got = run_experts(moe, (gu, gus2, dn, dns), cuda(x2), idx, w, "f32")
+    assert np.isfinite(want).all() and np.array_equal(got, want)
 
 
 @pytest.mark.parametrize("t", [5, 70])
