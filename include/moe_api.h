@@ -352,7 +352,8 @@ typedef struct {
  * (in the order of j).  Ids >= n_experts (0xffffffff, or another rank's experts
  * after the caller subtracted its first id) contribute nothing; a row without
  * experts gives zeros; an expert twice in a row counts twice.
- *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype, must not overlap x
+ *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype; out and work must not
+ *        overlap the inputs, the layer or one another
  *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned;
  *        calls whose executions overlap need one each
  * top_k 1..32; t 0..1048576 with t * top_k < 2^31 / 2. */

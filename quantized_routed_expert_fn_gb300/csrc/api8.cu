@@ -218,6 +218,14 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   if (overlap(work, z.total, x, (size_t)t * H * xs) || overlap(work, z.total, out, no) ||
       overlap(work, z.total, topk_idx, ni) || overlap(work, z.total, topk_w, ni))
     return fail(MOE_EINVAL, "work overlaps x, out, the ids or the weights");
+  const size_t ne = (size_t)E * H * I;  // bytes of down; gate_up has twice as many
+  const struct {
+    const void *p;
+    size_t n;
+  } parts[4] = {{L->gate_up, 2 * ne}, {L->gate_up_s, 2 * ne >> 14}, {L->down, ne}, {L->down_s, ne >> 14}};
+  for (const auto &w : parts)
+    if (overlap(w.p, w.n, out, no) || overlap(w.p, w.n, work, z.total))
+      return fail(MOE_EINVAL, "out or work overlaps the layer's weights or scales");
   moe::Ex8P p{};
   p.H = H, p.E = E, p.I = I, p.t = t, p.K = top_k;
   p.gu = L->gate_up, p.gus = L->gate_up_s, p.dn = L->down, p.dns = L->down_s;

@@ -98,6 +98,9 @@ def test_experts8_refuses_bad_layers(m, layer, code):
     (dict(st=None), -1), (dict(x=O + 4), -3), (dict(out=O + (1 << 20) + 8), -3), (dict(idx=W + 1), -3),
     (dict(work=S + 16), -3), (dict(wb=16), -7), (dict(out=O + 64), -1), (dict(out=W), -1),
     (dict(work=O), -1), (dict(x=S), -1),
+    # out or work in the layer's weights (8 x 256 x 256 and 8 x 256 x 128 bytes) or scales (32 and 16 bytes)
+    (dict(out=A + (1 << 19) - 64), -1), (dict(out=B + 16), -1), (dict(out=C + (1 << 18) - 64), -1), (dict(out=D), -1),
+    (dict(work=A + 4096), -1), (dict(work=C), -1), (dict(work=D), -1),
 ])
 def test_experts8_refuses_bad_calls(m, over, code):
     assert _ex(m, **over) == code, m.last_error()
