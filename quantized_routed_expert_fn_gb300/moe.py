@@ -368,8 +368,7 @@ def _stream_on(stream, dev: int) -> int:
 
 def _ld(t) -> int:
     """Row stride; of a single row, whose stride means nothing, its length."""
-    s, n = t.stride(0), t.shape[1]
-    return s if s > n or t.shape[0] > 1 else n
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 @functools.lru_cache(maxsize=64)
@@ -416,6 +415,8 @@ def mm8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, ou
     """moe_mm8: a e4m3 [t][k] with sa E8M0 [t][ceil(k / 128)] (its rows a multiple of 4 bytes apart, the last
     one held whole) times b e4m3 [n][k] with sb [ceil(n / 128)][ceil(k / 128)] -> out float32 / bfloat16 [t][n].
     With offs int32 [G + 1]: b [G][n][k], sb [G][..][..], group g has the rows offs[g] .. offs[g + 1] - 1."""
+    if offs is not None and (offs.dim() != 1 or offs.shape[0] < 2):
+        _bad(ESHAPE, "offs is a vector of the groups' G + 1 row offsets")
     groups = 0 if offs is None else offs.shape[0] - 1
     if a.dim() != 2 or b.dim() != (3 if groups else 2):
         _bad(ESHAPE, "a is [t][k]; b is [n][k], with offs [G][n][k]")
@@ -467,6 +468,8 @@ def experts8(layer: Layer8, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: tor
              work: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     """moe_experts8: x float32 / bfloat16 [t][hidden] through the experts topk_idx int32 [t][k] (ids outside
     0 .. E - 1 contribute nothing) with weights topk_w -> out float32 / bfloat16 [t][hidden]."""
+    if topk_idx.dim() != 2:
+        _bad(ESHAPE, "topk_idx is a matrix")
     t, k = topk_idx.shape
     dev = _device(x, "x")
     shape = (t, layer.hidden)

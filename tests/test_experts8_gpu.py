@@ -633,6 +633,24 @@ def test_calls_from_two_threads_and_streams(moe):
         assert torch.equal(o, ref[n][1]) and torch.equal(p, ref[n][2])
 
 
+def test_a_single_row_of_any_stride(moe):
+    """The stride of one row means nothing: a row of a transposed or odd view is taken."""
+    g = np.random.default_rng(1)
+    a, sa, b, sb = operands(g, 1, 40, 272)
+    ref, mag = ref8.mm8(a, sa, b, sb)
+    at = cuda(np.concatenate([a, a], 1)).as_strided((1, 272), (287, 1))
+    st = cuda(np.concatenate([sa, sa], 1)).as_strided((1, 3), (4, 1))
+    o = torch.zeros(1, 40, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.mm8(at, st, cuda(b), cuda(sb), o, status)
+    check_mm8(f64(o), ref, mag, 272, "f32")
+    x = torch.randn(1, 300, device="cuda")
+    want = run_quant(moe, x, 1)
+    q, s = torch.zeros(1, 300, dtype=torch.uint8, device="cuda"), torch.zeros(1, 3, dtype=torch.uint8, device="cuda")
+    moe.quant8(x.expand(5, 300)[:1], q.as_strided((1, 300), (1, 1)), s)
+    assert np.array_equal(q.cpu().numpy(), want[0]) and np.array_equal(s.cpu().numpy(), want[1])
+
+
 def test_binding_refusals(moe):
     z = lambda *s, d=torch.uint8: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
     st = z(1, d=torch.int32)
@@ -650,5 +668,12 @@ def test_binding_refusals(moe):
         moe.gate(z(4, 8, d=torch.float32), z(4, 2, d=torch.int32), z(4, 2, d=torch.float32), score="tanh")
     with pytest.raises(moe.MoeError):
         moe.quant8(z(4, 8, d=torch.float16), z(4, 8), z(4, 1))
+    for offs in (z(1, d=torch.int32), z(1, 2, d=torch.int32), z(0, d=torch.int32)):
+        with pytest.raises(moe.MoeError):
+            moe.mm8(z(4, 128), z(4, 4)[:, :1], z(1, 64, 128), z(1, 1, 1), z(4, 64, d=torch.float32), st, offs=offs)
+    L = moe.Layer8(z(2, 256, 128), z(2, 2, 1), z(2, 128, 128), z(2, 1, 1))
+    with pytest.raises(moe.MoeError):
+        moe.experts8(L, z(4, 128, d=torch.float32), z(8, d=torch.int32), z(8, d=torch.float32), z(4, 128, d=torch.float32),
+                     moe.alloc_workspace(1 << 20), st)
     with pytest.raises(moe.MoeError):
         moe.Layer8(z(2, 256, 100), z(2, 2, 1), z(2, 100, 128), z(2, 1, 1))
