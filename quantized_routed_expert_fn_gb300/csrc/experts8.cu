@@ -47,10 +47,12 @@ __device__ __forceinline__ void pdl_wait_prev() { asm volatile("griddepcontrol.w
 // bytes apart) times eight rows of x or h.  Lane (g, q) = (lane / 4, lane %
 // 4) takes the bytes 32q .. 32q + 31 of weight rows g and g + 8 and of row g
 // of x (`col`): the k order inside a block is permuted alike on both sides.
-// (Weight rows are a multiple of 128 bytes apart, so two rows of a load meet
-// in a bank; the MMAs take longer than that.  Converting the weights to f16
-// by hand, by the conversion instruction or by integer operations, was 10 to
-// 25% slower than the 8-bit MMA.)
+// (Rows are a multiple of 128 bytes apart, so two rows of a load meet in a
+// bank.  Loads without such conflicts, odd rows exchanging two pieces after
+// them, took 35.5 us instead of 33.4 for 4 rows through 39 experts, and rows
+// of x and h a piece further apart 33.4: the MMAs take longer than the loads.
+// Converting the weights to f16 by hand, by the conversion instruction or by
+// integer operations, was 10 to 25% slower than the 8-bit MMA.)
 struct Block {
   uint4 a0, a1, a2, a3, b0, b1;
 };
@@ -116,7 +118,7 @@ __device__ __forceinline__ uint2 quant128(const float (&v)[8], uint32_t &e) {
 // ------------------------------------------------------------ few rows
 
 constexpr int kMaxEntries = kEx8SmallRows * 32;
-constexpr int kMaxStages = 24;
+constexpr int kMaxStages = 24;  // at most a lane each
 constexpr int kDownWarps = 16;
 constexpr size_t kSmemCap = 226 * 1024;
 
@@ -128,13 +130,14 @@ struct Union {
   float (*w)[kEx8SmallRows];         // [experts] sum of a row's weights for the expert
   short (*ent)[kEx8SmallRows];       // a row's first entry with that expert, or -1
   uint8_t *own;                      // [n entries] is a row's first entry with its expert
+  uint32_t *seen;                    // a bit an expert
   int *n;
 };
-__host__ __device__ constexpr size_t union_bytes(int n) { return (size_t)n * (4 + 4 + 4 + 4 * 8 + 2 * 8 + 1) + 16 + 15; }
+__host__ __device__ constexpr size_t union_bytes(int n) { return (size_t)n * (4 + 4 + 4 + 4 * 8 + 2 * 8 + 1) + 16 + 128 + 15; }
 __device__ __forceinline__ Union union_at(void *p, int n) {
   Union U;
   U.n = static_cast<int *>(p);
-  U.ids = reinterpret_cast<uint32_t *>(U.n + 4), U.ex = U.ids + n;
+  U.seen = reinterpret_cast<uint32_t *>(U.n + 4), U.ids = U.seen + 32, U.ex = U.ids + n;
   U.wt = reinterpret_cast<float *>(U.ex + n);
   U.w = reinterpret_cast<float(*)[kEx8SmallRows]>(U.wt + n);
   U.ent = reinterpret_cast<short(*)[kEx8SmallRows]>(U.w + n);
@@ -143,7 +146,7 @@ __device__ __forceinline__ Union union_at(void *p, int n) {
 }
 
 // One warp: ids, ex and n.  32 entries at a time: the first of each id among
-// them by a match, those of earlier groups by comparison.
+// them by a match, those of earlier groups by the experts' bits.
 __device__ void union_warp(const Union &U, const Ex8P &P) {
   const int lane = threadIdx.x & 31, n = P.t * P.K;
   uint32_t id[kMaxEntries / 32];
@@ -154,12 +157,14 @@ __device__ void union_warp(const Union &U, const Ex8P &P) {
     wt[i] = 32 * i + lane < n ? P.w[32 * i + lane] : 0.f;
   }
   int cnt = 0;
+  U.seen[lane] = 0;  // E <= 1024
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < kMaxEntries / 32; i++) {
     if (32 * i >= n) break;
     if (32 * i + lane < n) U.ids[32 * i + lane] = id[i], U.wt[32 * i + lane] = wt[i], U.own[32 * i + lane] = 0;
     bool first = __ffs(__match_any_sync(FULLM, id[i])) - 1 == lane && id[i] < (uint32_t)P.E;
-    for (int j = 0; j < cnt; j++) first &= U.ex[j] != id[i];
+    if (first) first = !(atomicOr(&U.seen[id[i] >> 5], 1u << (id[i] & 31)) >> (id[i] & 31) & 1u);
     const unsigned bal = __ballot_sync(FULLM, first);
     if (first) U.ex[cnt + __popc(bal & ((1u << lane) - 1u))] = id[i];
     cnt += __popc(bal);
@@ -186,18 +191,49 @@ __device__ void union_rows(const Union &U, const Ex8P &P, int tid, int count) {
   }
 }
 
-__host__ __device__ constexpr int row_stride(int k) { return k + 16; }  // e4m3 rows of x, h: 16 bytes apart in the banks
+// One warp: n copies of `bytes` each, from src(f), into the ring of ns stages.
+// A lane looks after a stage, so that the copies of free stages are issued
+// together.  For down's many short copies: one thread issuing all of them
+// took 0.24 us a copy, 9 us for the 39 of a CTA, more than HBM.  (gate_up's
+// long ones come at HBM's rate from one thread, in the order of their use;
+// all at once, they arrive together: 33.4 us instead of 32.4 for 4 rows
+// through 39 experts.)
+template <class Src>
+__device__ void produce(uint64_t *full, uint64_t *empty, uint8_t *ring, int ns, int bytes, int n, const Ex8P &P, Src src) {
+  const int lane = threadIdx.x & 31;
+  int f = lane;
+  uint32_t ph = 0;  // of the stage's next copy
+  unsigned long long t0 = 0;
+  bool on = lane < ns && f < n;
+  while (__any_sync(FULLM, on)) {
+    if (on) {
+      if (mbar_test_wait(&empty[lane], ph ^ 1)) {
+        mbar_expect_tx(&full[lane], (uint32_t)bytes);
+        bulk_g2s(ring + (size_t)lane * bytes, src(f), (uint32_t)bytes, &full[lane]);
+        f += ns, ph ^= 1, t0 = 0;
+        on = f < n;
+      } else if (t0 == 0) {
+        t0 = globaltimer();
+      } else if (globaltimer() - t0 > P.timeout_ns) {
+        atomicCAS(P.status, 0, kStatusTimeout);
+        on = false;
+      }
+    }
+  }
+  // the copy still in flight lands before the CTA ends
+  if (lane < ns && f >= ns) thread_wait(&full[lane], ph ^ 1, P);
+}
 
 // ---- gate_up: dynamic shared memory: ring | x rows | their scales | sums | union
 constexpr int kTeams = 4, kTeam = 4, kGuWarps = kTeams * kTeam, kGuThreads = 32 * (kGuWarps + 2);
 GuLay gu_layout(int H, int t, int K) {
   GuLay l{};
   l.stage = 8 * H;
-  const size_t xs = (size_t)t * row_stride(H), sx = ((size_t)t * (H / 128) * 4 + 15) / 16 * 16, red = 2 * kGuWarps * 512;  // two of each team
+  const size_t xs = (size_t)t * H, sx = ((size_t)t * (H / 128) * 4 + 15) / 16 * 16, red = 2 * kGuWarps * 512;  // two of each team
   const size_t rest = xs + sx + red + union_bytes(t * K);
   const size_t room = kSmemCap > rest ? (kSmemCap - rest) / l.stage : 0;
   const int fit = (int)(room < kMaxStages ? room : kMaxStages);
-  l.teams = fit >= 8 ? 4 : (fit >= 4 ? 2 : 1);
+  l.teams = fit >= 2 * kTeams ? kTeams : (fit >= 4 ? 2 : 1);
   l.ns = fit / (2 * l.teams) * (2 * l.teams);
   l.xs = (size_t)l.ns * l.stage, l.sx = l.xs + xs, l.red = l.sx + sx, l.un = l.red + red;
   l.total = (size_t)l.ns * l.stage + rest;
@@ -222,15 +258,14 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
   // the misses in the address translation bound the kernel)
   auto share = [&](int items, unsigned b) { return (int)((int64_t)items * b / gridDim.x); };
   pdl_launch_next();
+  pdl_wait_prev();  // everything before this call; only the launch itself is hidden
 
   if (warp == kGuWarps) {
     // ---- the union, then the producer: gate rows, up rows of every item
-    if (lane == 0) {
-      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], kTeam);
-      for (int b = 0; b < 2 * kTeams; b++) mbar_init(&red_full[0][b], kTeam), mbar_init(&red_empty[0][b], 1);
-      fence_mbar_init();
-      if (blockIdx.x == 0) *P.status = 0;
-    }
+    if (lane < L.ns) mbar_init(&full[lane], 1), mbar_init(&empty[lane], kTeam);
+    if (lane < 2 * kTeams) mbar_init(&red_full[0][lane], kTeam), mbar_init(&red_empty[0][lane], 1);
+    fence_mbar_init();
+    if (lane == 0 && blockIdx.x == 0) *P.status = 0;
     union_warp(U, P);
     tc05::named_arrive(3, kGuThreads);  // the union and the barriers are there
     if (lane == 0) {
@@ -309,7 +344,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
       uint32_t e;
       const uint2 w = quant128(v[i], e);
       if (bb < P.t * nk) {
-        *reinterpret_cast<uint2 *>(xs + (size_t)r * row_stride(H) + (bb - r * nk) * 128 + (lane & 15) * 8) = w;
+        *reinterpret_cast<uint2 *>(xs + (size_t)r * H + (bb - r * nk) * 128 + (lane & 15) * 8) = w;
         if ((lane & 15) == 0) sx[bb] = e8m0_f(e);
       }
     }
@@ -321,7 +356,7 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
   const int all = *U.n * nct, items = share(all, blockIdx.x + 1), step = L.teams, step_u = step / nct,
             step_c = step - step_u * nct;
   const bool have = g < P.t, have0 = 2 * q < P.t, have1 = 2 * q + 1 < P.t;
-  const uint8_t *col = xs + (size_t)(have ? g : 0) * row_stride(H) + q * 32;
+  const uint8_t *col = xs + (size_t)(have ? g : 0) * H + q * 32;
   const float *sx0 = sx + (have0 ? 2 * q : 0) * nk, *sx1 = sx + (have1 ? 2 * q + 1 : 0) * nk;
   const size_t up_s = (size_t)(I / 128) * nk;  // from a gate scale to its up scale
   int it = share(all, blockIdx.x) + team;
@@ -392,7 +427,7 @@ DnLay dn_layout(int I, int n) {
   DnLay l{};
   const int nk = I / 128;
   l.stage = 16 * I;
-  const size_t hs = (size_t)n * row_stride(I), sh = ((size_t)n * nk * 4 + 15) / 16 * 16, red = kDownWarps * 16 * 9 * 4;
+  const size_t hs = (size_t)n * I, sh = ((size_t)n * nk * 4 + 15) / 16 * 16, red = kDownWarps * 16 * 9 * 4;
   const size_t un = union_bytes(n) / 16 * 16, rest = hs + 2 * sh + un + red;
   const size_t room = kSmemCap > rest ? (kSmemCap - rest) / l.stage : 0;
   const int fit = (int)(room < kMaxStages ? room : kMaxStages), np = (nk + 1) / 2;
@@ -420,54 +455,42 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
   const int H = P.H, I = P.I, nk = I / 128, n0 = blockIdx.x * 16;
   if (warp == kDownWarps) {
     // ---- the union, then the producer: this CTA's rows of every expert
-    if (lane == 0) {
-      for (int s = 0; s < L.ns; s++) mbar_init(&full[s], 1), mbar_init(&empty[s], (uint32_t)(nk + 1) / 2);
-      fence_mbar_init();
-    }
+    if (lane < L.ns) mbar_init(&full[lane], 1), mbar_init(&empty[lane], (uint32_t)(nk + 1) / 2);
+    fence_mbar_init();
     union_warp(U, P);
     tc05::named_arrive(3, 32 * kDownWarps + 32);
-    if (lane == 0) {
-      int u = 0;
-      const int nu = *U.n;
-      for (; u < nu; u++) {
-        const int s = u % L.ns;
-        if (!thread_wait(&empty[s], (uint32_t)(((u / L.ns) & 1) ^ 1), P)) break;
-        mbar_expect_tx(&full[s], (uint32_t)L.stage);
-        bulk_g2s(sm + (size_t)s * L.stage, P.dn + ((size_t)U.ex[u] * H + n0) * I, (uint32_t)L.stage, &full[s]);
-      }
-      // copies still in flight land before the CTA ends
-      for (int i = u > L.ns ? u - L.ns : 0; i < u; i++) thread_wait(&full[i % L.ns], (uint32_t)((i / L.ns) & 1), P);
-    }
+    produce(full, empty, sm, L.ns, L.stage, *U.n, P, [&](int u) { return P.dn + ((size_t)U.ex[u] * H + n0) * I; });
     return;
   }
   tc05::named_sync(3, 32 * kDownWarps + 32);
-  union_rows(U, P, tid, 32 * kDownWarps);
   const int items = *U.n * nk;  // (expert, k block), k fastest
-  for (int i = tid; i < items; i += 32 * kDownWarps) {
-    const int u = i / nk, kb = i - u * nk;
-    sd[i] = e8m0_f(P.dns[((size_t)U.ex[u] * (H / 128) + (n0 >> 7)) * nk + kb]);
-  }
+  auto scale = [&](int i) { return P.dns[((size_t)U.ex[i / nk] * (H / 128) + (n0 >> 7)) * nk + i % nk]; };
+  const uint32_t first = tid < items ? scale(tid) : 0u;  // on its way while the tables are made
+  union_rows(U, P, tid, 32 * kDownWarps);
+  if (tid < items) sd[tid] = e8m0_f(first);
+  for (int i = tid + 32 * kDownWarps; i < items; i += 32 * kDownWarps) sd[i] = e8m0_f(scale(i));
   tc05::named_sync(1, 32 * kDownWarps);
   pdl_wait_prev();  // h is the previous kernel's; the weights on their way are not
   // h of every entry that has one (of an expert twice in a row: the first) ->
-  // e4m3, half a warp a block, the loads of four rounds together
-  for (int b = warp * 2; b < n * nk; b += 8 * kDownWarps) {
-    float v[4][8];
+  // e4m3, half a warp a block, the loads of six rounds together
+  constexpr int R = 6;
+  for (int b = warp * 2; b < n * nk; b += 2 * R * kDownWarps) {
+    float v[R][8];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < R; i++) {
       const int bb = b + 2 * kDownWarps * i + (lane >> 4), e = bb / nk;
 #pragma unroll
       for (int j = 0; j < 8; j++) v[i][j] = 0.f;
       if (bb < n * nk && U.own[e]) load_x8<false>(P.h32, (int64_t)bb * 128 + (lane & 15) * 8, v[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < R; i++) {
       const int bb = b + 2 * kDownWarps * i + (lane >> 4), e = bb / nk;
       if (b + 2 * kDownWarps * i >= n * nk) break;  // warp-uniform
       uint32_t x;
       const uint2 w = quant128(v[i], x);
       if (bb < n * nk) {
-        *reinterpret_cast<uint2 *>(hs + (size_t)e * row_stride(I) + (bb - e * nk) * 128 + (lane & 15) * 8) = w;
+        *reinterpret_cast<uint2 *>(hs + (size_t)e * I + (bb - e * nk) * 128 + (lane & 15) * 8) = w;
         if ((lane & 15) == 0) sh[bb] = e8m0_f(x);
       }
     }
@@ -482,7 +505,7 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
     // two blocks; past the end the second is the first again, unscaled
     const int kb = 2 * pr, k2 = kb + 1 < nk ? kb + 1 : kb;
     const int e = U.ent[u][g], e0 = U.ent[u][2 * q], e1 = U.ent[u][2 * q + 1];
-    const uint8_t *col = hs + (size_t)max(e, 0) * row_stride(I) + q * 32;
+    const uint8_t *col = hs + (size_t)max(e, 0) * I + q * 32;
     if (!warp_wait(&full[s], ph, P)) break;
     const uint8_t *wr = sm + (size_t)s * L.stage;
     Block x, y;
@@ -765,8 +788,8 @@ cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaFuncSetAttribute(h, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemCap);
   if (e != cudaSuccess) return e;
   const int items = p.t * p.K * (p.I / 8);
-  f<<<(unsigned)(items < n_sms ? items : n_sms), kGuThreads, l.total, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_pdl(f, dim3((unsigned)(items < n_sms ? items : n_sms)), kGuThreads, l.total, st, p);
+  if (e != cudaSuccess) return e;
   return launch_pdl(h, dim3((unsigned)(p.H / 16)), 32 * kDownWarps + 32, d.total, st, p);
 }
 

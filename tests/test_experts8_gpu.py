@@ -590,6 +590,57 @@ def test_other_stream_and_repeated_calls(moe):
         assert torch.equal(o, outs[0])
 
 
+@pytest.mark.parametrize("t", [2, 30])
+def test_captured_behind_other_work(moe, t):
+    """In a graph: first, behind a copy, behind a fill, behind a kernel, where two streams join, behind itself; and the
+    same calls without a graph.  Each must see what came before it."""
+    g = np.random.default_rng(t)
+    L = moe.Layer8(*[cuda(v) for v in make_experts(g, 6, 256, 128)])
+    src = torch.randn(t, 256, device="cuda")
+    idx = cuda(np.stack([g.choice(6, size=2, replace=False) for _ in range(t)]).astype(np.int32))
+    w = torch.rand(t, 2, device="cuda")
+    work = moe.alloc_workspace(moe.experts8_workspace(L, t, 2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def sequence(outs):
+        call = lambda x, i: moe.experts8(L, x, idx, w, outs[i], work, status)  # noqa: E731
+        x = outs[6]
+        call(src, 0)
+        x.copy_(src)
+        call(x, 1)
+        x.zero_()
+        call(x, 2)
+        torch.add(src, src, out=x)
+        call(x, 3)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x.mul_(0.5)
+        torch.mul(src, 3.0, out=outs[7])
+        torch.cuda.current_stream().wait_stream(side)
+        call(x, 4)
+        call(outs[4], 5)
+
+    new = lambda: [torch.full((t, 256), 5.0, device="cuda") for _ in range(8)]  # noqa: E731
+    plain = new()
+    sequence(plain)
+    torch.cuda.synchronize()
+    outs = new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sequence(outs)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, plain):
+            assert torch.equal(a, b)
+    assert torch.equal(plain[0], plain[1]) and torch.equal(plain[0], plain[4]) and (plain[2] == 0).all()
+    assert not torch.equal(plain[3], plain[0]) and not torch.equal(plain[5], plain[4])
+    assert status.item() == 0
+
+
 def test_calls_from_two_threads_and_streams(moe):
     """Calls of different sizes from two host threads on their own streams, with their own workspaces, at once."""
     import threading
