@@ -41,10 +41,7 @@ cudaError_t launch_quant8_rows(const Quant8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_quant8_blocks(const Quant8P &p, cudaStream_t st);
 
 // ---- products (mm8.cu)
-struct Mm8P {
-  // tokens: boxes of 1, 2, ... times 16 (or 32) rows; weights [G * n][k]:
-  // boxes of 128 rows; 128 bytes of k a block, 128B swizzle
-  CUtensorMap tm_a[7], tm_b;
+struct Mm8Args {
   const uint8_t *a, *sa, *b, *sb;
   int64_t lda, lds;
   int t, n, k, nk, nb;  // nk = ceil(k / 128), nb = ceil(n / 128)
@@ -62,6 +59,11 @@ struct Mm8P {
   int *status;
   unsigned long long timeout_ns;
 };
+struct Mm8P : Mm8Args {
+  // tokens: boxes of 1, 2, ... times 16 (or 32) rows; weights [G * n][k]:
+  // boxes of 128 rows; 128 bytes of k a block, 128B swizzle
+  CUtensorMap tm_a[7], tm_b;
+};
 enum { kOutF32 = 0, kOutBf16 = 1, kOutSilu8 = 2 };
 // Whether the few-row kernel (weights streamed once into mma.sync) takes t
 // rows: its MMAs are slow, so the larger the weights and the more its groups
@@ -72,7 +74,7 @@ enum { kOutF32 = 0, kOutBf16 = 1, kOutSilu8 = 2 };
 inline bool mm8_small(int64_t t, int64_t n, int64_t k) {
   return t <= 8 || (t <= 16 && n * k <= 1 << 24) || (t <= 32 && n * k <= 1 << 23);
 }
-cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st);
+cudaError_t launch_mm8_small(const Mm8Args &p, int out_kind, cudaStream_t st);
 cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st);
 
 #ifdef __CUDACC__

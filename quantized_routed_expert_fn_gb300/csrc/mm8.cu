@@ -12,8 +12,9 @@
 //          specialised, tcgen05 with the tensor cores' own block scaling
 //          (kind::mxf8f6f4), accumulating all of k in TMEM.
 //          8192 x 8192 x 2048: 94 to 98 us, 2.8 to 2.9 PFLOP/s; bound by what
-//          the SMs take in from L2 (14.5 TB/s of requests there).  128 uneven groups, 32668 rows x 1536
-//          x 2048: 122 us, 470 MB read, 15 TB/s at L2.
+//          the SMs take in from L2 (14.5 TB/s of requests there).  128 uneven
+//          groups, 32668 rows x 1536 x 2048: 122 us, 470 MB read, 15 TB/s at
+//          L2.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -54,7 +55,7 @@ constexpr int kSmWarps = 8;
 // takes the blocks w, w + 8, ...; the warps' sums meet in shared memory, in
 // a fixed order.
 template <int NT, class T>
-__global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant__ Mm8P P) {
+__global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant__ Mm8Args P) {
   __shared__ float red[kSmWarps][16][8 * NT + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   if (blockIdx.x == 0 && tid == 0) *P.status = 0;
@@ -653,7 +654,7 @@ cudaError_t launch_tc(Mm8P &p, int grid, bool pdl, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_mm8_small(const Mm8P &p, int out_kind, cudaStream_t st) {
+cudaError_t launch_mm8_small(const Mm8Args &p, int out_kind, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.n + 15) / 16);
   const int nt = (p.t + 7) / 8;
 #define MOE_SMALL(NT)                                                          \

@@ -350,7 +350,7 @@ def _whole(t, name: str, shape: tuple, dtypes, dev: int) -> int:
 def _device(t, name: str) -> int:
     """The call's device: the current one, where the stream and every tensor have to be."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         _bad(EINVAL, f"{name} is on {t.device}, not on the current CUDA device")
     return dev
 
@@ -360,15 +360,19 @@ def _device(t, name: str) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# The same for the current device, once a tensor says that CUDA is there.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_on(stream, dev: int) -> int:
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
     return _stream(stream)
 
 
-def _ld(t) -> int:
+def _ld(t, rows: int, cols: int) -> int:
     """Row stride; of a single row, whose stride means nothing, its length."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if rows > 1 else cols
 
 
 @functools.lru_cache(maxsize=64)
@@ -393,7 +397,8 @@ def gate(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, bia
     wp = _whole(topk_w, "topk_w", (t, k), _F32, dev)
     bp = None if bias is None else _whole(bias, "bias", (e,), _F32, dev)
     cfg = _gate_cfg(e, k, score, n_groups, top_groups, group_top, GATE_RENORM if renorm else 0, scale)
-    _check((_lib or lib()).moe_gate(cfg, lp, _FLOATS[logits.dtype], _ld(logits), bp, t, ip, wp, _stream_on(stream, dev)))
+    _check((_lib or lib()).moe_gate(cfg, lp, _FLOATS[logits.dtype], _ld(logits, t, e), bp, t, ip, wp,
+                                    _stream_on(stream, dev)))
 
 
 def quant8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 1, stream=None) -> None:
@@ -405,9 +410,10 @@ def quant8(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, block_rows: int = 
     dev = _device(x, "x")
     xp = _arg(x, "x", (rows, cols), _FLOATS, dev)
     qp = _arg(q, "q", (rows, cols), _E4M3, dev)
-    sp = _arg(s, "s", (-(-rows // block_rows), -(-cols // 128)), _E8M0, dev)
-    _check((_lib or lib()).moe_quant8(xp, _FLOATS[x.dtype], _ld(x), rows, cols, block_rows, qp, _ld(q), sp, _ld(s),
-                                      _stream_on(stream, dev)))
+    sr, sc = -(-rows // block_rows), -(-cols // 128)
+    sp = _arg(s, "s", (sr, sc), _E8M0, dev)
+    _check((_lib or lib()).moe_quant8(xp, _FLOATS[x.dtype], _ld(x, rows, cols), rows, cols, block_rows, qp,
+                                      _ld(q, rows, cols), sp, _ld(s, sr, sc), _stream_on(stream, dev)))
 
 
 def mm8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, out: torch.Tensor, status: torch.Tensor,
@@ -436,8 +442,8 @@ def mm8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, ou
     if t and not (lds == sa.shape[1] and sa.is_contiguous()):
         if sa.untyped_storage().nbytes() < sa.storage_offset() + t * lds:
             _bad(EINVAL, "sa's last row is not held whole")
-    _check((_lib or lib()).moe_mm8(ap, _ld(a), sap, lds, t, bp, sbp, n, k, op, _FLOATS[out.dtype], _ld(out), fp, groups,
-                                   flags, _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
+    _check((_lib or lib()).moe_mm8(ap, _ld(a, t, k), sap, lds, t, bp, sbp, n, k, op, _FLOATS[out.dtype], _ld(out, t, n),
+                                   fp, groups, flags, _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
 
 
 class Layer8:
