@@ -170,7 +170,7 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
     } else {
       int n_sms = 0;
       if (int r = sm_count(&n_sms)) return r;
-      e = moe::launch_mm8_tc(p, kind, n_sms, false, st);
+      e = moe::launch_mm8_tc(p, kind, n_sms, st);
     }
   }
   if (e != cudaSuccess) return fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
@@ -263,8 +263,8 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   d.out = p.y, d.ldo = H, d.hs = nullptr;
   const int yk = p.out_bf16 ? moe::kOutBf16 : moe::kOutF32;
   e = moe::launch_ex8_group(p, st);
-  if (e == cudaSuccess) e = moe::launch_mm8_tc(u, moe::kOutSilu8, n_sms, true, st);
-  if (e == cudaSuccess) e = moe::launch_mm8_tc(d, yk, n_sms, true, st);
+  if (e == cudaSuccess) e = moe::launch_mm8_tc(u, moe::kOutSilu8, n_sms, st);
+  if (e == cudaSuccess) e = moe::launch_mm8_tc(d, yk, n_sms, st);
   if (e == cudaSuccess) e = moe::launch_ex8_combine(p, n_sms, st);
   if (e != cudaSuccess) return fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return MOE_OK;

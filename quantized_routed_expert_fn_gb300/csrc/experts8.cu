@@ -39,10 +39,6 @@ namespace {
 constexpr unsigned FULLM = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;  // many rows
 
-
-__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // One k block of 128: 16 weight rows (eight from lo, eight from hi on, ld
 // bytes apart) times eight rows of x or h.  Lane (g, q) = (lane / 4, lane %
 // 4) takes the bytes 32q .. 32q + 31 of weight rows g and g + 8 and of row g
@@ -257,8 +253,11 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
   // few experts' pages (with every 152nd item each copy was another page, and
   // the misses in the address translation bound the kernel)
   auto share = [&](int items, unsigned b) { return (int)((int64_t)items * b / gridDim.x); };
+  // everything before this call; only the launch itself is hidden.  The next
+  // kernel may start from here on, not sooner: it reads the ids before it
+  // waits for this one
+  pdl_wait_prev();
   pdl_launch_next();
-  pdl_wait_prev();  // everything before this call; only the launch itself is hidden
 
   if (warp == kGuWarps) {
     // ---- the union, then the producer: gate rows, up rows of every item
@@ -739,21 +738,6 @@ __global__ void __launch_bounds__(256) ex8_combine(const __grid_constant__ Ex8P 
 }
 
 size_t al(size_t n) { return (n + 1023) & ~(size_t)1023; }
-
-template <class F>
-cudaError_t launch_pdl(F f, dim3 grid, unsigned block, size_t smem, cudaStream_t st, const Ex8P &p) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, p);
-}
 
 }  // namespace
 

@@ -75,9 +75,30 @@ inline bool mm8_small(int64_t t, int64_t n, int64_t k) {
   return t <= 8 || (t <= 16 && n * k <= 1 << 24) || (t <= 32 && n * k <= 1 << 23);
 }
 cudaError_t launch_mm8_small(const Mm8Args &p, int out_kind, cudaStream_t st);
-cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st);
+cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, cudaStream_t st);
 
 #ifdef __CUDACC__
+
+// Programmatic dependent launch: the kernel may start while the one before it
+// in the stream ends, and touches memory behind pdl_wait_prev only.  What a
+// kernel does before that wait holds as long as the one before it lets it
+// start (pdl_launch_next) behind its own.
+__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class F, class P>
+cudaError_t launch_pdl(F f, dim3 grid, unsigned block, size_t smem, cudaStream_t st, const P &p) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, p);
+}
 
 // e8m0 byte -> the power of two it stands for
 __device__ __forceinline__ float e8m0_f(uint32_t e) {

@@ -206,6 +206,8 @@ template <int C, bool VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_constant__ GateP P) {
   extern __shared__ uint64_t key64[];  // [kGateWarps][E]: rows decided in 64 bits
   __shared__ uint2 picks[kGateWarps][32];  // the choices of a row: key, id
+  pdl_wait_prev();
+  pdl_launch_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = P.E, K = P.K, e0 = lane * C;
   const unsigned below = (1u << lane) - 1u;
@@ -477,9 +479,7 @@ cudaError_t launch(const GateP &p, int n_sms, cudaStream_t st) {
   const bool vec = p.E % C == 0 && (p.ld * size) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0;
   const int64_t need = ((int64_t)p.t + kGateWarps - 1) / kGateWarps, cap = (int64_t)n_sms * 64;
   const unsigned grid = (unsigned)(need < cap ? need : cap);
-  if (vec) gate_kernel<C, true><<<grid, 32 * kGateWarps, smem, st>>>(p);
-  else gate_kernel<C, false><<<grid, 32 * kGateWarps, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(vec ? gate_kernel<C, true> : gate_kernel<C, false>, dim3(grid), 32 * kGateWarps, smem, st, p);
 }
 
 }  // namespace

@@ -27,9 +27,6 @@ namespace {
 
 constexpr unsigned FULLM = 0xffffffffu;
 
-__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait_prev() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 template <class T>
 __device__ __forceinline__ void store_out(T *p, float v);
 template <>
@@ -55,9 +52,11 @@ constexpr int kSmWarps = 8;
 // takes the blocks w, w + 8, ...; the warps' sums meet in shared memory, in
 // a fixed order.
 template <int NT, class T>
-__global__ void __launch_bounds__(32 * kSmWarps) mm8_small(const __grid_constant__ Mm8Args P) {
+__global__ void __launch_bounds__(32 * kSmWarps) mm8_few_rows(const __grid_constant__ Mm8Args P) {
   __shared__ float red[kSmWarps][16][8 * NT + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  pdl_wait_prev();
+  pdl_launch_next();
   if (blockIdx.x == 0 && tid == 0) *P.status = 0;
   const int n0 = blockIdx.x * 16;
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -613,7 +612,7 @@ bool use_pairs(const Mm8P &p, int out_kind) { return weight_tiles(p, out_kind) >
 // The launch of one form: the ring for the tile width p.wmax, the tensor
 // maps, the kernel.
 template <int MB, int KIND, int CG, int KB>
-cudaError_t launch_tc(Mm8P &p, int grid, bool pdl, cudaStream_t st) {
+cudaError_t launch_tc(Mm8P &p, int grid, cudaStream_t st) {
   using LY = TcLay<MB, CG>;
   const int rows = (p.wmax / CG + LY::unit - 1) / LY::unit * LY::unit;
   p.tok = rows * 128;
@@ -637,11 +636,9 @@ cudaError_t launch_tc(Mm8P &p, int grid, bool pdl, cudaStream_t st) {
     at[n].val.clusterDim.x = 2, at[n].val.clusterDim.y = 1, at[n].val.clusterDim.z = 1;
     n++;
   }
-  if (pdl) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n].val.programmaticStreamSerializationAllowed = 1;
-    n++;
-  }
+  at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[n].val.programmaticStreamSerializationAllowed = 1;
+  n++;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kTcThreads);
@@ -657,18 +654,13 @@ cudaError_t launch_tc(Mm8P &p, int grid, bool pdl, cudaStream_t st) {
 cudaError_t launch_mm8_small(const Mm8Args &p, int out_kind, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.n + 15) / 16);
   const int nt = (p.t + 7) / 8;
-#define MOE_SMALL(NT)                                                          \
-  if (out_kind == kOutF32) mm8_small<NT, float><<<grid, 32 * kSmWarps, 0, st>>>(p); \
-  else mm8_small<NT, uint16_t><<<grid, 32 * kSmWarps, 0, st>>>(p);
-  if (nt <= 1) { MOE_SMALL(1) }
-  else if (nt <= 2) { MOE_SMALL(2) }
-  else { MOE_SMALL(4) }
-#undef MOE_SMALL
-  return cudaGetLastError();
+  auto f = nt <= 1 ? mm8_few_rows<1, float> : (nt <= 2 ? mm8_few_rows<2, float> : mm8_few_rows<4, float>);
+  if (out_kind == kOutBf16) f = nt <= 1 ? mm8_few_rows<1, uint16_t> : (nt <= 2 ? mm8_few_rows<2, uint16_t> : mm8_few_rows<4, uint16_t>);
+  return launch_pdl(f, dim3(grid), 32 * kSmWarps, 0, st, p);
 }
 
 template <int MB, int KIND>
-cudaError_t launch_tc_form(Mm8P p, int n_sms, bool pdl, cudaStream_t st) {
+cudaError_t launch_tc_form(Mm8P p, int n_sms, cudaStream_t st) {
   const bool pairs = use_pairs(p, KIND);
   p.wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ldo * (KIND == kOutF32 ? 4 : 2))) & 15) == 0;
   p.wmax = pairs ? TcLay<MB, 2>::N : TcLay<MB, 1>::N;
@@ -690,16 +682,16 @@ cudaError_t launch_tc_form(Mm8P p, int n_sms, bool pdl, cudaStream_t st) {
   const int64_t tt = (p.t + p.wmax - 1) / p.wmax + (p.offs ? p.G : 0);
   const int64_t tiles = tt * ((weight_tiles(p, KIND) + cg - 1) / cg);
   const int grid = (int)(tiles < n_sms / cg ? tiles : n_sms / cg) * cg;
-  if (!pairs) return launch_tc<MB, KIND, 1, 1>(p, grid, pdl, st);
+  if (!pairs) return launch_tc<MB, KIND, 1, 1>(p, grid, st);
   if constexpr (MB == 1)
-    if (p.k % 256 == 0) return launch_tc<MB, KIND, 2, 2>(p, grid, pdl, st);
-  return launch_tc<MB, KIND, 2, 1>(p, grid, pdl, st);
+    if (p.k % 256 == 0) return launch_tc<MB, KIND, 2, 2>(p, grid, st);
+  return launch_tc<MB, KIND, 2, 1>(p, grid, st);
 }
 
-cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, bool pdl, cudaStream_t st) {
-  if (out_kind == kOutF32) return launch_tc_form<1, kOutF32>(p, n_sms, pdl, st);
-  if (out_kind == kOutBf16) return launch_tc_form<1, kOutBf16>(p, n_sms, pdl, st);
-  return launch_tc_form<2, kOutSilu8>(p, n_sms, pdl, st);
+cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, cudaStream_t st) {
+  if (out_kind == kOutF32) return launch_tc_form<1, kOutF32>(p, n_sms, st);
+  if (out_kind == kOutBf16) return launch_tc_form<1, kOutBf16>(p, n_sms, st);
+  return launch_tc_form<2, kOutSilu8>(p, n_sms, st);
 }
 
 }  // namespace moe

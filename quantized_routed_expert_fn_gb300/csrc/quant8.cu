@@ -62,6 +62,8 @@ __device__ __forceinline__ void store8(uint8_t *q, int n, uint32_t lo, uint32_t 
 // 80 instructions a block are what bounds this kernel beside HBM.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows(const __grid_constant__ Quant8P P) {
+  pdl_wait_prev();
+  pdl_launch_next();
   const int cb = (P.cols + 127) / 128, sub = threadIdx.x & 15;
   const int step = gridDim.x * 16, step_r = step / cb, step_b = step - step_r * cb;
   const int i0 = blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -94,6 +96,8 @@ __global__ void __launch_bounds__(256) quant_rows(const __grid_constant__ Quant8
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) quant_blocks(const __grid_constant__ Quant8P P) {
   __shared__ uint32_t red[8];
+  pdl_wait_prev();
+  pdl_launch_next();
   const int sub = threadIdx.x & 15, r0 = blockIdx.y * 128 + (threadIdx.x >> 4), c = blockIdx.x * 128 + sub * 8;
   float v[8][8];
   uint32_t a = 0;
@@ -137,27 +141,16 @@ cudaError_t launch_quant8_rows(const Quant8P &p, int n_sms, cudaStream_t st) {
   const int64_t rounds = (need + cap - 1) / cap;
   const unsigned grid = (unsigned)((need + rounds - 1) / rounds);
   const bool v = vec_ok(p);
-  if (p.bf16) {
-    if (v) quant_rows<true, true><<<grid, 256, 0, st>>>(p);
-    else quant_rows<true, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (v) quant_rows<false, true><<<grid, 256, 0, st>>>(p);
-    else quant_rows<false, false><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  auto f = p.bf16 ? (v ? quant_rows<true, true> : quant_rows<true, false>) : (v ? quant_rows<false, true> : quant_rows<false, false>);
+  return launch_pdl(f, dim3(grid), 256, 0, st, p);
 }
 
 cudaError_t launch_quant8_blocks(const Quant8P &p, cudaStream_t st) {
   const dim3 grid((unsigned)((p.cols + 127) / 128), (unsigned)((p.rows + 127) / 128));
   const bool v = vec_ok(p);
-  if (p.bf16) {
-    if (v) quant_blocks<true, true><<<grid, 256, 0, st>>>(p);
-    else quant_blocks<true, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (v) quant_blocks<false, true><<<grid, 256, 0, st>>>(p);
-    else quant_blocks<false, false><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  auto f = p.bf16 ? (v ? quant_blocks<true, true> : quant_blocks<true, false>)
+                  : (v ? quant_blocks<false, true> : quant_blocks<false, false>);
+  return launch_pdl(f, grid, 256, 0, st, p);
 }
 
 }  // namespace moe

@@ -641,6 +641,48 @@ def test_captured_behind_other_work(moe, t):
     assert status.item() == 0
 
 
+def test_calls_behind_one_another_without_a_wait(moe):
+    """A chain in which each call reads what the one before it writes, and one that overwrites what the one before it
+    reads, over and over: as with a synchronisation after every call."""
+    g = np.random.default_rng(17)
+    t, h, i, e, k = 4, 256, 128, 6, 2
+    L = moe.Layer8(*[cuda(v) for v in make_experts(g, e, h, i)])
+    router = cuda(ref8.round_e4m3(g.normal(size=(e, h)) * 50))
+    rs = torch.full((1, h // 128), 118, dtype=torch.uint8, device="cuda")
+    xs = [torch.randn(t, h, device="cuda") for _ in range(3)]
+
+    def chain(wait):
+        z = lambda *s, d=torch.float32: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+        x, q, s, lg = z(t, h), z(t, h, d=torch.uint8), z(t, 4, d=torch.uint8)[:, : h // 128], z(t, e)
+        idx, w, st, out = z(t, k, d=torch.int32), z(t, k), z(1, d=torch.int32), []
+        work = moe.alloc_workspace(moe.experts8_workspace(L, t, k))
+        y = z(t, h)
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        for n in range(60):
+            x.copy_(xs[n % 3])
+            done()
+            for _ in range(2):
+                moe.quant8(x, q, s)
+                done()
+                moe.mm8(q, s, router, rs, lg, st)
+                done()
+                moe.gate(lg, idx, w, renorm=True)
+                done()
+                moe.experts8(L, x, idx, w, y, work, st)
+                done()
+                x.copy_(y)
+                done()
+            out.append((idx.clone(), y.clone()))
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        return out
+
+    want, got = chain(True), chain(False)
+    for (i0, y0), (i1, y1) in zip(want, got):
+        assert torch.equal(i0, i1) and torch.equal(y0, y1)
+    assert not torch.equal(want[0][1], want[1][1])
+
+
 def test_calls_from_two_threads_and_streams(moe):
     """Calls of different sizes from two host threads on their own streams, with their own workspaces, at once."""
     import threading
