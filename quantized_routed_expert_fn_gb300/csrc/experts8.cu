@@ -590,7 +590,8 @@ __device__ void scan_counts(const Ex8P &P, int c, int *part) {
 // Which places an entry gets depends on the order of the atomics, its results
 // do not.
 __global__ void __launch_bounds__(kCountThreads) ex8_count(const __grid_constant__ Ex8P P) {
-  pdl_launch_next();
+  pdl_wait_prev();
+  pdl_launch_next();  // behind the wait: the next kernel reads x before its own
   extern __shared__ int hist[];  // [E]
   __shared__ int last, part[32];
   const int tid = threadIdx.x, n = P.t * P.K, E = P.E;
@@ -780,11 +781,10 @@ cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st) {
 cudaError_t launch_ex8_group(const Ex8P &p, cudaStream_t st) {
   const int n = p.t * p.K, blocks = (n + kCountEntries - 1) / kCountEntries;
   if (blocks > 1) {
-    cudaError_t e = cudaMemsetAsync(p.counts, 0, (size_t)(p.E + 1) * 4, st);
+    const cudaError_t e = cudaMemsetAsync(p.counts, 0, (size_t)(p.E + 1) * 4, st);
     if (e != cudaSuccess) return e;
   }
-  ex8_count<<<(unsigned)blocks, kCountThreads, (size_t)p.E * 4, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(ex8_count, dim3((unsigned)blocks), kCountThreads, (size_t)p.E * 4, st, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(p.x_bf16 ? ex8_scatter<true> : ex8_scatter<false>, dim3((unsigned)((p.t + kWarps - 1) / kWarps)), kThreads,
                     0, st, p);

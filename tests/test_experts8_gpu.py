@@ -641,11 +641,12 @@ def test_captured_behind_other_work(moe, t):
     assert status.item() == 0
 
 
-def test_calls_behind_one_another_without_a_wait(moe):
+@pytest.mark.parametrize("t", [4, 24, 2500])
+def test_calls_behind_one_another_without_a_wait(moe, t):
     """A chain in which each call reads what the one before it writes, and one that overwrites what the one before it
     reads, over and over: as with a synchronisation after every call."""
     g = np.random.default_rng(17)
-    t, h, i, e, k = 4, 256, 128, 6, 2
+    h, i, e, k = 256, 128, 6, 2
     L = moe.Layer8(*[cuda(v) for v in make_experts(g, e, h, i)])
     router = cuda(ref8.round_e4m3(g.normal(size=(e, h)) * 50))
     rs = torch.full((1, h // 128), 118, dtype=torch.uint8, device="cuda")
@@ -658,7 +659,7 @@ def test_calls_behind_one_another_without_a_wait(moe):
         work = moe.alloc_workspace(moe.experts8_workspace(L, t, k))
         y = z(t, h)
         done = torch.cuda.synchronize if wait else (lambda: None)
-        for n in range(60):
+        for n in range(30):
             x.copy_(xs[n % 3])
             done()
             for _ in range(2):
