@@ -16,11 +16,12 @@
 //            quantises h while its weights arrive; sums meet in a fixed order
 // An item's chain of wait, loads, MMAs and arrival takes a warp some 1000
 // cycles, in which HBM brings 23 KB to an SM: so several items are worked on
-// at once, and two k blocks' MMAs are interleaved.  That rate and the
-// launches bound these kernels, not HBM.  One row, 8 of 128 experts, 2048 x
-// 768: 12 us for the 25 MB of gate_up, 10 for the 13 MB of down, 16 together,
-// the second's start hidden; four rows, 39 of 512 experts, 2048 x 512: 21 and
-// 20, 37 together.
+// at once, and two k blocks' MMAs are interleaved.
+// One row, 8 of 128 experts, 2048 x 768, 38 MB: 13.2 us back to back; four
+// rows, 39 of 512 experts, 2048 x 512, 123 MB: 30.  By time stamps in the
+// latter: union 1.1, gate_up's sums until 17 (13 without MMAs and loads: HBM),
+// down's start, union and tables until 20, gate_up's end seen at 21, h ready
+// at 24 (80 KB loaded and quantised by every CTA), products and sums until 31.
 //
 // Many rows: the entries are grouped by expert (count, scan), x is quantised
 // once per row and written to its entries' places, mm8_tc computes h8 and

@@ -6,7 +6,7 @@
 //          straight into the fragments of mma.sync (no shared memory), the
 //          few rows come from L1; a CTA takes 16 weight rows and splits k
 //          over its warps.
-//          1 x 2048 x 2048: 5.6 us alone, of which the 4.2 MB are 0.6: launch
+//          1 x 2048 x 2048: 5.1 us in a graph, of which the 4.2 MB are 0.6: launch
 //          and one HBM latency bound it.
 //   tc     any number of rows, dense or grouped: persistent, warp
 //          specialised, tcgen05 with the tensor cores' own block scaling
