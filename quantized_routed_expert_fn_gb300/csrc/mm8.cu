@@ -183,8 +183,8 @@ struct TcLay {
   static constexpr int unit = 16 * CG == 32 ? 16 : 32;           // token boxes: multiples of this many rows
   // front: silu: h bytes [N][128], maxima [4][N]; else 32 x 32 values a warp
   static constexpr int epi = MB == 2 ? N * 128 + 4 * N * 4 : 4 * 4096;
-  static constexpr int offTab = (epi + 15) & ~15;                // int [G + 1] first row, [G + 1] first token tile
-  static constexpr int offBars = (offTab + 2 * (kMaxGroups + 1) * 4 + 15) & ~15;
+  static constexpr int offTab = (epi + 15) & ~15;                // int [G + 1] first row, first token tile, [G] tile width
+  static constexpr int offBars = (offTab + 3 * (kMaxGroups + 1) * 4 + 15) & ~15;
   static constexpr int offRing = (offBars + (int)sizeof(TcBars) + 1023) / 1024 * 1024;
   static constexpr int room = 226 * 1024 - offRing;              // for the ring, the base rounded up
 };
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
   const int S = P.stages;
   uint8_t *ring = sm + LY::offRing;
   TcBars &B = *reinterpret_cast<TcBars *>(sm + LY::offBars);
-  int *s_off = reinterpret_cast<int *>(sm + LY::offTab), *s_tile = s_off + kMaxGroups + 1;
+  int *s_off = reinterpret_cast<int *>(sm + LY::offTab), *s_tile = s_off + kMaxGroups + 1, *s_w = s_tile + kMaxGroups + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = CG == 1 ? 0 : (int)tc05::cluster_rank();
   const int G = P.G > 0 ? P.G : 1, nk = P.nk;
@@ -257,18 +257,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
   else tc05::cluster_sync();
   tc05::fence_after();
   const uint32_t tmem = B.tmem;
-  // group table: first row and first token tile of every group
+  // group table: first row, first token tile and tile width (the rows of a
+  // group are cut into equal tiles) of every group
+  auto width = [](int m, int c) { return ((m + c - 1) / c + LY::step - 1) / LY::step * LY::step; };
   if (P.offs) {
     for (int g = tid; g <= G; g += kTcThreads) s_off[g] = P.offs[g];
     __syncthreads();
     for (int g = tid; g < G; g += kTcThreads)
       if (s_off[g] < 0 || s_off[g] > s_off[g + 1] || s_off[g + 1] > P.t) B.bad = 1;
     __syncthreads();
+    for (int g = tid; g < G; g += kTcThreads) {
+      const int m = s_off[g + 1] - s_off[g], c = B.bad ? 0 : (m + P.wmax - 1) / P.wmax;
+      s_tile[g] = c, s_w[g] = c ? width(m, c) : 0;
+    }
+    __syncthreads();
     if (warp == 0) {
       int base = 0;
       for (int g0 = 0; g0 < G; g0 += 32) {
-        const int g = g0 + lane;
-        const int c = g < G && !B.bad ? (s_off[g + 1] - s_off[g] + P.wmax - 1) / P.wmax : 0;
+        const int g = g0 + lane, c = g < G ? s_tile[g] : 0;
         int x = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
   } else if (tid == 0) {
     s_off[0] = 0, s_off[1] = P.t;
     s_tile[0] = 0, s_tile[1] = (P.t + P.wmax - 1) / P.wmax;
+    s_w[0] = width(P.t, s_tile[1]);
   }
   __syncthreads();
   // the status of the call: one CTA's to set (a wait gives up long after)
@@ -293,23 +300,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
   const int ntiles = s_tile[G] * nmp, cl = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
   const int my_tiles = cl < ntiles ? (ntiles - 1 - cl) / ncl + 1 : 0;
   // tile i: the weight tiles of a token tile follow one another (their token
-  // rows stay in L2); the rows of a group are cut into equal tiles
-  auto tile_of = [&](int lt) {
-    const int i = cl + lt * ncl, tt = i / nmp;
-    int lo = 0, hi = G;  // the last group whose first token tile is <= tt
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_tile[mid] <= tt) lo = mid; else hi = mid;
+  // rows stay in L2).  A role walks its tiles by next_tile: without divisions,
+  // and the warps (not the one thread that issues MMAs) look for the group 32
+  // entries at a time, as the copies of the next tile wait for this.
+  int tt = cl / nmp, mp = cl - tt * nmp;
+  const int step_t = ncl / nmp, step_m = ncl - step_t * nmp;
+  auto next_tile = [&](auto by_warp) {
+    int lo = 0;  // the last group whose first token tile is <= tt
+    if constexpr (decltype(by_warp)::value) {
+      lo = 32 * (__popc(__ballot_sync(FULLM, 32 * lane < G && s_tile[32 * lane] <= tt)) - 1);
+      lo += __popc(__ballot_sync(FULLM, lo + lane < G && s_tile[lo + lane] <= tt)) - 1;
+    } else {
+      for (int hi = G; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tile[mid] <= tt) lo = mid; else hi = mid;
+      }
     }
-    const int m = s_off[lo + 1] - s_off[lo], c = s_tile[lo + 1] - s_tile[lo];
-    const int w = ((m + c - 1) / c + LY::step - 1) / LY::step * LY::step, r0 = (tt - s_tile[lo]) * w;
+    const int m = s_off[lo + 1] - s_off[lo], w = s_w[lo], r0 = (tt - s_tile[lo]) * w;
     Tile T;
-    T.g = lo, T.mt = (i - tt * nmp) * CG + rank;
+    T.g = lo, T.mt = mp * CG + rank;
     T.n0 = s_off[lo] + r0;
     T.nlen = max(0, min(w, m - r0));
     T.N = max(LY::step, (T.nlen + LY::step - 1) / LY::step * LY::step);
+    tt += step_t, mp += step_m;
+    if (mp >= nmp) mp -= nmp, tt++;
     return T;
   };
+  using ByWarp = std::true_type;
+  using ByThread = std::false_type;
   auto weight_row = [&](const Tile &T, int m) { return T.g * P.n + (MB == 2 ? m * (P.n / 2) : 0) + T.mt * 128; };
   // arrive on a barrier of the even CTA (this CTA's, without a pair)
   auto arrive_even = [&](uint64_t *bar) {
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       uint32_t ph = 0, slp = 0;
       bool ok = true;
       Tile Tn;
-      if (my_tiles > 0) Tn = tile_of(0);
+      if (my_tiles > 0) Tn = next_tile(ByThread());
       const uint32_t base = smem_u32(ring);
       for (int lt = 0; lt < my_tiles && ok; lt++) {
         const Tile T = Tn;
@@ -371,7 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
           if constexpr (CG == 1) tc05::commit(&B.empty[s]);
           else tc05::commit_pair(&B.empty[s]);
           if (++s == S) s = 0, ph ^= 1;
-          if (k0 == 0 && lt + 1 < my_tiles) Tn = tile_of(lt + 1);  // while the MMAs run
+          if (k0 == 0 && lt + 1 < my_tiles) Tn = next_tile(ByThread());  // while the MMAs run
         }
         if (ok) {
           if constexpr (CG == 1) tc05::commit(&B.acc_full[b]);
@@ -390,7 +408,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
     uint32_t ph = 0;
     bool ok = true;
     for (int lt = 0; lt < my_tiles && ok; lt++) {
-      const Tile T = tile_of(lt);
+      const Tile T = next_tile(ByWarp());
       // this CTA's token rows of the tile: one box of as many rows (64 + 32 +
       // 16 in three boxes cost 7% at 8192 x 8192 x 2048).  One lane issues
       // the copies: their operands are uniform registers, and lanes with
@@ -439,10 +457,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       }
     };
     Tile T, Tn;
-    if (my_tiles > 0) Tn = tile_of(0), fetch(Tn, 0);
+    if (my_tiles > 0) Tn = next_tile(ByWarp()), fetch(Tn, 0);
     for (int lt = 0; lt < my_tiles && ok; lt++) {
       T = Tn;
-      if (lt + 1 < my_tiles) Tn = tile_of(lt + 1);
+      if (lt + 1 < my_tiles) Tn = next_tile(ByWarp());
       for (int kb = 0; kb < nk; kb += 4, f++) {
         if ((kb & 31) == 0)
 #pragma unroll
@@ -485,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
       if (lane == 0) arrive_even(&B.acc_empty[b]);
     };
     for (int lt = 0; lt < my_tiles; lt++) {
-      const Tile T = tile_of(lt);
+      const Tile T = next_tile(ByWarp());
       const int b = lt & 1;
       // the four epilogue warps stop together (they share named barriers)
       if (!tc05::named_and(2, 128, tc_warp_wait<CG>(&B.acc_full[b], (uint32_t)((lt >> 1) & 1), P))) break;
