@@ -27,8 +27,8 @@
 // once per row and written to its entries' places, mm8_tc computes h8 and
 // the outputs y, and a last kernel sums a row's weighted outputs in the
 // order of its entries.  4096 rows, 10 of 512 experts by Zipf(1.1), 2048 x
-// 512, alone: count 7, scatter 20 (101 MB), gate_up 209 (1.16 GB read, 5.5
-// TB/s), down 149 (558 MB read, 168 written), sum 36 us (184 MB).
+// 512, alone: count 7, scatter 19 (101 MB), gate_up 205 (1.16 GB from HBM, 5.7
+// TB/s; L2 15.5), down 135 (558 MB read, 168 written), sum 36 us (184 MB).
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
