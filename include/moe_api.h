@@ -347,11 +347,11 @@ typedef struct {
  * moe_route's or a caller's):
  *   x8 = quant8(x);  (g, u) = mm8 with gate_up;  h8 = quant8(silu(g) * u);
  *   out[r] = sum over j of topk_w[r][j] * (mm8 of h8 with down of expert topk_idx[r][j])
- * in fp32 between the roundings to 8 bits; for more than a few rows the
- * experts' outputs are held in out's type before they are weighted and summed
- * (in the order of j).  Ids >= n_experts (0xffffffff, or another rank's experts
- * after the caller subtracted its first id) contribute nothing; a row without
- * experts gives zeros; an expert twice in a row counts twice.
+ * in fp32 between the roundings to 8 bits and up to the sum (for more than a
+ * few rows in the order of j), which is rounded once to out's type.  Ids >=
+ * n_experts (0xffffffff, or another rank's experts after the caller subtracted
+ * its first id) contribute nothing; a row without experts gives zeros; an
+ * expert twice in a row counts twice.
  *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype; out and work must not
  *        overlap the inputs, the layer or one another
  *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned;

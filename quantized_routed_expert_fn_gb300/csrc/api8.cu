@@ -179,8 +179,7 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
 
 size_t moe_experts8_workspace(const moe_layer8 *L, int t, int top_k) {
   if (check_layer8(L, t, top_k) != MOE_OK) return 0;
-  // out in float32 needs the most
-  const size_t n = moe::ex8_sizes((int)L->hidden, (int)L->n_experts, (int)L->inter, t, top_k, 4).total;
+  const size_t n = moe::ex8_sizes((int)L->hidden, (int)L->n_experts, (int)L->inter, t, top_k).total;
   return n ? n : 256;
 }
 
@@ -213,7 +212,7 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   if (overlap(x, (size_t)t * H * xs, out, no)) return fail(MOE_EINVAL, "out overlaps x");
   if (overlap(topk_idx, ni, out, no) || overlap(topk_w, ni, out, no))
     return fail(MOE_EINVAL, "out overlaps the ids or weights");
-  const moe::Ex8Sizes z = moe::ex8_sizes(H, E, I, t, top_k, os);
+  const moe::Ex8Sizes z = moe::ex8_sizes(H, E, I, t, top_k);
   if (work_bytes < z.total) return fail(MOE_ENOSPACE, "work holds %zu bytes, %zu needed", work_bytes, z.total);
   if (overlap(work, z.total, x, (size_t)t * H * xs) || overlap(work, z.total, out, no) ||
       overlap(work, z.total, topk_idx, ni) || overlap(work, z.total, topk_w, ni))
@@ -249,7 +248,7 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   }
   p.h8 = take(z.h8), p.h8s = take(z.h8s), p.x8 = take(z.x8), p.x8s = take(z.x8s);
   p.counts = (int *)take(z.counts), p.offs = (int *)take(z.offs), p.place = (int *)take(z.place);
-  p.y = take(z.y);
+  p.y = (float *)take(z.y);
   moe::Mm8P u, d;
   memset(&u, 0, sizeof u);
   u.a = p.x8, u.lda = H, u.sa = p.x8s, u.lds = p.ldh, u.b = p.gu, u.sb = p.gus;
@@ -261,10 +260,9 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   d.a = p.h8, d.lda = I, d.sa = p.h8s, d.lds = p.ldi, d.b = p.dn, d.sb = p.dns;
   d.n = H, d.k = I, d.nk = I / 128, d.nb = H / 128;
   d.out = p.y, d.ldo = H, d.hs = nullptr;
-  const int yk = p.out_bf16 ? moe::kOutBf16 : moe::kOutF32;
   e = moe::launch_ex8_group(p, st);
   if (e == cudaSuccess) e = moe::launch_mm8_tc(u, moe::kOutSilu8, n_sms, st);
-  if (e == cudaSuccess) e = moe::launch_mm8_tc(d, yk, n_sms, st);
+  if (e == cudaSuccess) e = moe::launch_mm8_tc(d, moe::kOutF32, n_sms, st);
   if (e == cudaSuccess) e = moe::launch_ex8_combine(p, n_sms, st);
   if (e != cudaSuccess) return fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
   return MOE_OK;

@@ -220,14 +220,14 @@ struct Ex8P {
   int *counts;          // [E] entries per expert, then one ticket
   int *offs;            // [E + 1]
   int *place;           // [t * K] place of an entry within its expert, -1: none
-  void *y;              // [t * K][H] weighted outputs in out's type
+  float *y;             // [t * K][H] the entries' outputs, not weighted yet
 };
 struct Ex8Sizes {
   size_t h32, h8, h8s, x8, x8s, counts, offs, place, y, total;
 };
 constexpr int kEx8SmallRows = 8;  // rows of the few-row path: one column each of an m16n8 tile
 bool ex8_small(int H, int I, int t, int K);
-Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K, int out_size);
+Ex8Sizes ex8_sizes(int H, int E, int I, int t, int K);
 cudaError_t launch_ex8_small(Ex8P &p, int n_sms, cudaStream_t st);
 cudaError_t launch_ex8_group(const Ex8P &p, cudaStream_t st);
 cudaError_t launch_ex8_combine(const Ex8P &p, int n_sms, cudaStream_t st);

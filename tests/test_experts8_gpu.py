@@ -771,3 +771,18 @@ def test_binding_refusals(moe):
                      moe.alloc_workspace(1 << 20), st)
     with pytest.raises(moe.MoeError):
         moe.Layer8(z(2, 256, 100), z(2, 2, 1), z(2, 100, 128), z(2, 1, 1))
+
+
+# ------------------------------------------------------------ experts8: terms in 32 bits whatever the number of rows
+
+@pytest.mark.parametrize("t,h,i,e,k", [(3, 256, 128, 8, 4), (8, 384, 256, 12, 4), (9, 256, 128, 8, 4), (40, 384, 256, 12, 6),
+                                       (300, 256, 128, 16, 8), (1500, 640, 128, 30, 5)])
+def test_experts8_rounds_the_sum_once(moe, t, h, i, e, k):
+    """A bf16 output is the 32-bit one rounded once: the experts' terms are in 32 bits for few rows and for many."""
+    g = np.random.default_rng(t)
+    ws = make_experts(g, e, h, i)
+    x = cuda(g.normal(size=(t, h)).astype(np.float32))
+    idx, w = np.stack([g.choice(e, size=k, replace=False) for _ in range(t)]), g.random(size=(t, k)).astype(np.float32)
+    whole = run_experts(moe, ws, x, idx, w, "f32")
+    got = run_experts(moe, ws, x, idx, w, "bf16")
+    assert np.array_equal(got, f64(torch.from_numpy(whole).float().bfloat16()))
