@@ -294,13 +294,29 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
         top1 = t1, top2 = t2;
       }
       if (P.group_top == 1) top2 = 0u;
-      float score = -kInf;
+      // The group's score, and how far it may be from the definition's: the
+      // errors of its terms (a bias of each sign may cancel in the sum, the
+      // roundings it brought do not) and the sum's own rounding.  A term that
+      // is infinite makes the score exact; a sum past the 32-bit range is left
+      // to 64.
+      float score = -kInf, gtol = 0.f;
+      bool over = false;
       if (top1) {
         score = of_key(top1);
         if (pair_groups) {
           if (!biased) score = score_of(score);
-          if (top2) score += biased ? of_key(top2) : score_of(of_key(top2));
+          gtol = tol_of(score, P.sigmoid);
+          if (top2) {
+            const float s1 = score, s2 = biased ? of_key(top2) : score_of(of_key(top2));
+            gtol += tol_of(s2, P.sigmoid);
+            score += s2;
+            over = fabsf(score) == kInf && s1 < kInf;
+          }
+          gtol += 1.1920928955078125e-7f * fabsf(score);
+        } else {
+          gtol = tol_of(score, P.sigmoid);
         }
+        if (score == kInf && !over) gtol = 0.f;
       }
       const int lanes = lpg ? lpg : 1;
       int rank = 0;
@@ -311,19 +327,20 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const __grid_cons
       const bool kept = mine < P.ng && rank < P.top_groups;
       if (biased || pair_groups) {
         // the lowest kept and the highest dropped score; where they are
-        // within the error of each other, every such pair that is not the
-        // same numbers makes the row a near one
+        // within the largest error of each other, every such pair within its
+        // own that is not the same numbers makes the row a near one
         const uint32_t lo = __reduce_min_sync(FULLM, kept && top1 ? okey(score) : 0xffffffffu);
         const uint32_t hi = __reduce_max_sync(FULLM, mine < P.ng && !kept && top1 ? okey(score) : 0u);
-        if (lo != 0xffffffffu && hi) {
-          const float a = of_key(lo), b = of_key(hi);
-          if (a - b <= 2.f * (tol_of(a, P.sigmoid) + tol_of(b, P.sigmoid))) {
+        const float tmax = __uint_as_float(__reduce_max_sync(FULLM, mine < P.ng ? __float_as_uint(gtol) : 0u));
+        near = __any_sync(FULLM, mine < P.ng && over);
+        if (!near && lo != 0xffffffffu && hi) {
+          if (!(of_key(lo) - of_key(hi) > 2.f * tmax)) {
             bool close = false;
             for (int j = 0; j < P.ng; j++) {
-              const float o = __shfl_sync(FULLM, score, j * lanes);
+              const float o = __shfl_sync(FULLM, score, j * lanes), ot = __shfl_sync(FULLM, gtol, j * lanes);
               const uint32_t o1 = __shfl_sync(FULLM, top1, j * lanes), o2 = __shfl_sync(FULLM, top2, j * lanes);
               const int ok = __shfl_sync(FULLM, kept ? 1 : 0, j * lanes);
-              if (kept && !ok && top1 && o1 && score - o <= 2.f * (tol_of(o, P.sigmoid) + tol_of(score, P.sigmoid)))
+              if (kept && !ok && top1 && o1 && !(score - o > gtol + ot))
                 close |= biased || o1 != top1 || o2 != top2;
             }
             near = __any_sync(FULLM, close);

@@ -786,3 +786,39 @@ def test_experts8_rounds_the_sum_once(moe, t, h, i, e, k):
     whole = run_experts(moe, ws, x, idx, w, "f32")
     got = run_experts(moe, ws, x, idx, w, "bf16")
     assert np.array_equal(got, f64(torch.from_numpy(whole).float().bfloat16()))
+
+
+# ------------------------------------------------------------ gate: bounds and ranges at their edges
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [2, 4, 8, 5])
+@pytest.mark.parametrize("big", [16.0, 100.0, 1e4])
+def test_gate_large_biases_that_cancel_in_a_group(moe, big, size, score):
+    """A group's best two have biases big and -big (a forced expert beside one switched off): their scores carry the
+    rounding of numbers as large as big, their sum is about 1.  Groups' sums some 1e-6 apart: the order is 64-bit
+    arithmetic's."""
+    g = np.random.default_rng(int(big) + size)
+    groups, t = 8, 300
+    bias = np.full((groups, size), -np.inf, np.float32)
+    bias[:, 0], bias[:, 1] = big, -big
+    bias[:, 2:] = np.where(g.random((groups, size - 2)) < 0.5, -np.inf, -3 * big)
+    bias = g.permuted(bias, axis=1).reshape(-1)
+    lg = (g.normal(size=(t, 1)) * 0.3 + g.normal(size=(t, groups * size)) * np.exp(g.normal(size=(t, 1))) * 1e-5).astype(np.float32)
+    for top_groups, k in ((1, 1), (3, 4)):
+        check_gate(moe, cuda(lg), k, cuda(bias), score=score, n_groups=groups, top_groups=top_groups, group_top=2, renorm=True)
+
+
+def test_gate_group_sums_by_hand(moe):
+    """Two groups of two, biases 1000 and -1000: sums 1.00004 and 1.00002 in 64 bits, 1.0 and 1.000061 in 32."""
+    p = np.array([[0.50002, 0.50002, 0.50004, 0.49998]])
+    bias = cuda(np.array([1000, -1000, 1000, -1000], np.float32))
+    idx, _ = check_gate(moe, cuda(np.log(p / (1 - p)).astype(np.float32)), 1, bias, score="sigmoid", n_groups=2, group_top=2)
+    assert idx.tolist() == [[0]]
+
+
+@pytest.mark.parametrize("top_groups", [1, 2, 3, 4])
+def test_gate_group_sums_past_32_bits(moe, top_groups):
+    """Biases whose sums leave the 32-bit range on either side, beside a group that is masked throughout."""
+    bias = np.array([-np.inf, -np.inf, -3e38, -3e38, 3e38, 2e38, 3e38, 3e38, -3e38, -2e38], np.float32)
+    lg = np.random.default_rng(2).normal(size=(20, 10)).astype(np.float32)
+    check_gate(moe, cuda(lg), 2 * top_groups, cuda(bias), score="sigmoid", n_groups=5, top_groups=top_groups, group_top=2)
