@@ -315,7 +315,9 @@ int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int 
                uint8_t *s, int64_t lds, moe_stream_t stream);
 
 /* out[r][j] = sum over k of a[r][k] b[j][k], scaled: the block-scaled 8-bit
- * matrix product, accumulated in fp32 and rounded once to out_dtype.
+ * matrix product, accumulated in fp32 and rounded once to out_dtype.  The two
+ * scales of a block may be of any size, whatever their product: what leaves
+ * the fp32 range is a partial sum or the result.
  *   a    e4m3 [t] rows of k, lda bytes apart; 16-byte aligned, lda % 16 == 0
  *   sa   E8M0 [t] rows of ceil(k / 128), lds bytes apart; 4-byte aligned, lds % 4 == 0,
  *        all t * lds bytes readable

@@ -73,6 +73,24 @@ __device__ __forceinline__ void mma_blocks(float (&d)[4], const Block &x, float 
   mma_e4m3(e, y.a2.z, y.a3.z, y.a2.w, y.a3.w, y.b1.z, y.b1.w);
 }
 
+// acc += d scaled: columns 2q (x0) and 2q + 1 (x1), gate rows (fg), up rows (fu)
+__device__ __forceinline__ void add_scaled(float4 &acc, const float (&d)[4], float x0, float x1, float fg, float fu) {
+  const float p[4] = {x0 * fg, x1 * fg, x0 * fu, x1 * fu};
+  if (scales_hold(p)) {
+    acc.x += d[0] * p[0], acc.y += d[1] * p[1], acc.z += d[2] * p[2], acc.w += d[3] * p[3];
+  } else {
+    acc.x += by_scales(d[0], x0, fg), acc.y += by_scales(d[1], x1, fg);
+    acc.z += by_scales(d[2], x0, fu), acc.w += by_scales(d[3], x1, fu);
+  }
+}
+// acc += w * (d scaled by a and b), two sums: a weight meets the scaled
+// product, as in the definition
+__device__ __forceinline__ void add_weighted(float &acc0, float &acc1, float d0, float d1, float a, float b, float w) {
+  const float p[1] = {a * b};
+  if (scales_hold(p)) acc0 += d0 * p[0] * w, acc1 += d1 * p[0] * w;
+  else acc0 += d0 * a * b * w, acc1 += d1 * a * b * w;
+}
+
 // bounded wait on an mbarrier phase, of a thread and of a warp; false (and
 // the status) once the limit passes
 __device__ bool thread_wait(uint64_t *bar, uint32_t par, const Ex8P &P) {
@@ -399,13 +417,12 @@ __global__ void __launch_bounds__(kGuThreads, 1) ex8_gate_up(const __grid_consta
         const uint8_t *sg = P.gus + ((size_t)U.ex[u0] * (2 * I / 128) + ct0 / 16) * nk;
         wg = sg[kb] | (uint32_t)sg[k2] << 8, wu = sg[up_s + kb] | (uint32_t)sg[up_s + k2] << 8;
       }
-      const float fg = e8m0_f(wg & 255u), fu = e8m0_f(wu & 255u), x0 = have0 ? sx0[kb] : 0.f, x1 = have1 ? sx1[kb] : 0.f;
-      // the two powers of two first: scales far from 1 may cancel
-      acc.x += d[0] * (x0 * fg), acc.y += d[1] * (x1 * fg), acc.z += d[2] * (x0 * fu), acc.w += d[3] * (x1 * fu);
+      const float fg = e8m0_f(wg & 255u), fu = e8m0_f(wu & 255u), x0 = have0 ? sx0[kb] : 1.f, x1 = have1 ? sx1[kb] : 1.f;
+      add_scaled(acc, d, x0, x1, fg, fu);
       if (two) {
         const float hg = e8m0_f(wg >> 8 & 255u), hu = e8m0_f(wu >> 8 & 255u);
-        const float y0 = have0 ? sx0[k2] : 0.f, y1 = have1 ? sx1[k2] : 0.f;
-        acc.x += e[0] * (y0 * hg), acc.y += e[1] * (y1 * hg), acc.z += e[2] * (y0 * hu), acc.w += e[3] * (y1 * hu);
+        const float y0 = have0 ? sx0[k2] : 1.f, y1 = have1 ? sx1[k2] : 1.f;
+        add_scaled(acc, e, y0, y1, hg, hu);
       }
       wg >>= 16, wu >>= 16;
     }
@@ -519,14 +536,12 @@ __global__ void __launch_bounds__(32 * kDownWarps + 32, 1) ex8_down(const __grid
     // the product is (a NaN weight times zero)
     const float w1 = sd[u * nk + kb], w2 = k2 > kb ? sd[u * nk + k2] : 0.f;
     if (e0 >= 0) {
-      const float w = U.w[u][2 * q], p1 = sh[e0 * nk + kb] * w1 * w, p2 = sh[e0 * nk + k2] * w2 * w;
-      acc[0] += d[0] * p1, acc[2] += d[2] * p1;
-      if (k2 > kb) acc[0] += f[0] * p2, acc[2] += f[2] * p2;
+      add_weighted(acc[0], acc[2], d[0], d[2], sh[e0 * nk + kb], w1, U.w[u][2 * q]);
+      if (k2 > kb) add_weighted(acc[0], acc[2], f[0], f[2], sh[e0 * nk + k2], w2, U.w[u][2 * q]);
     }
     if (e1 >= 0) {
-      const float w = U.w[u][2 * q + 1], p1 = sh[e1 * nk + kb] * w1 * w, p2 = sh[e1 * nk + k2] * w2 * w;
-      acc[1] += d[1] * p1, acc[3] += d[3] * p1;
-      if (k2 > kb) acc[1] += f[1] * p2, acc[3] += f[3] * p2;
+      add_weighted(acc[1], acc[3], d[1], d[3], sh[e1 * nk + kb], w1, U.w[u][2 * q + 1]);
+      if (k2 > kb) add_weighted(acc[1], acc[3], f[1], f[3], sh[e1 * nk + k2], w2, U.w[u][2 * q + 1]);
     }
     int du = step_u;
     pr += step_p;

@@ -105,6 +105,23 @@ __device__ __forceinline__ float e8m0_f(uint32_t e) {
   return __uint_as_float(e == 0 ? 0x00400000u : (e == 255u ? 0x7fc00000u : e << 23));
 }
 
+// Two scales a and b of a product d (powers of two) are multiplied first, as
+// scales far from 1 may cancel.  Where that is infinite or below the normal
+// numbers, both are above 1 or both below: then d * a * b, one after the
+// other, leaves the 32-bit range only where the result does, and zeros stay
+// zeros (by_scales).  scales_hold: none of the N products is of that kind.
+template <int N>
+__device__ __forceinline__ bool scales_hold(const float (&p)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; i++) m = max(m, __float_as_uint(p[i]) - 0x00800000u);
+  return m < 0x7f000000u;
+}
+__device__ __forceinline__ float by_scales(float d, float a, float b) {
+  const float p[1] = {a * b};
+  return scales_hold(p) ? d * p[0] : d * a * b;
+}
+
 // Scale byte of a block whose largest finite magnitude has the bits `a`:
 // the least e with |x| <= 448 * 2^(e - 127) = 1.75 * 2^(e - 119); 127 for a
 // block of zeros, 0 at least.

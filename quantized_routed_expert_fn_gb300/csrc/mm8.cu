@@ -87,18 +87,21 @@ __global__ void __launch_bounds__(32 * kSmWarps) mm8_few_rows(const __grid_const
       const uint4 b0 = r < P.t && k0 < P.k ? *reinterpret_cast<const uint4 *>(xr + k0) : zero;
       const uint4 b1 = r < P.t && k1 < P.k ? *reinterpret_cast<const uint4 *>(xr + k1) : zero;
       const int c = 8 * j + 2 * q;
-      // the two powers of two first: scales far from 1 may cancel
-      const float s0 = c < P.t ? e8m0_f(P.sa[(size_t)c * P.lds + kb]) * fb : 0.f;
-      const float s1 = c + 1 < P.t ? e8m0_f(P.sa[(size_t)(c + 1) * P.lds + kb]) * fb : 0.f;
+      const float s0 = c < P.t ? e8m0_f(P.sa[(size_t)c * P.lds + kb]) : 1.f;
+      const float s1 = c + 1 < P.t ? e8m0_f(P.sa[(size_t)(c + 1) * P.lds + kb]) : 1.f;
       float d[4] = {0.f, 0.f, 0.f, 0.f};
       mma_e4m3(d, x[0][0].x, x[0][1].x, x[0][0].y, x[0][1].y, b0.x, b0.y);
       mma_e4m3(d, x[0][0].z, x[0][1].z, x[0][0].w, x[0][1].w, b0.z, b0.w);
       mma_e4m3(d, x[1][0].x, x[1][1].x, x[1][0].y, x[1][1].y, b1.x, b1.y);
       mma_e4m3(d, x[1][0].z, x[1][1].z, x[1][0].w, x[1][1].w, b1.z, b1.w);
-      acc[j][0] += d[0] * s0;
-      acc[j][1] += d[1] * s1;
-      acc[j][2] += d[2] * s0;
-      acc[j][3] += d[3] * s1;
+      const float p[2] = {s0 * fb, s1 * fb};
+      if (scales_hold(p)) {
+        acc[j][0] += d[0] * p[0], acc[j][1] += d[1] * p[1];
+        acc[j][2] += d[2] * p[0], acc[j][3] += d[3] * p[1];
+      } else {
+        acc[j][0] += by_scales(d[0], s0, fb), acc[j][1] += by_scales(d[1], s1, fb);
+        acc[j][2] += by_scales(d[2], s0, fb), acc[j][3] += by_scales(d[3], s1, fb);
+      }
     }
   };
 #pragma unroll

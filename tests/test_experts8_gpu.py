@@ -822,3 +822,45 @@ def test_gate_group_sums_past_32_bits(moe, top_groups):
     bias = np.array([-np.inf, -np.inf, -3e38, -3e38, 3e38, 2e38, 3e38, 3e38, -3e38, -2e38], np.float32)
     lg = np.random.default_rng(2).normal(size=(20, 10)).astype(np.float32)
     check_gate(moe, cuda(lg), 2 * top_groups, cuda(bias), score="sigmoid", n_groups=5, top_groups=top_groups, group_top=2)
+
+
+# ------------------------------------------------------------ scales: the whole range of their sum
+
+@pytest.mark.parametrize("ea,eb", [(65, 64), (126, 3), (3, 126), (-75, -75), (-123, -27), (-27, -123)])
+@pytest.mark.parametrize("t", [3, 8, 13, 20, 70])
+def test_mm8_scales_that_add_up_past_32_bits(moe, t, ea, eb):
+    """Scales 2^ea and 2^eb whose product no 32-bit number holds (or only a rounded one), of operands that bring the
+    result back: the same numbers times a power of two, bit for bit, and zeros stay zeros."""
+    g = np.random.default_rng(t)
+    a, sa, b, sb = operands(g, t, 140, 256, whole=True)  # values -2 .. 2, every sum exact
+    a[0] = 0
+    ref, _ = ref8.mm8(a, sa, b, sb)
+    f = 2.0 ** (-7 if ea + eb > 0 else 7)
+    a, b = ref8.round_e4m3(ref8.E4M3[a] * f), ref8.round_e4m3(ref8.E4M3[b] * f)
+    sa, sb = np.minimum(sa, 127), np.minimum(sb, 127)
+    ref, _ = ref8.mm8(a, sa, b, sb)
+    ref = ref * 2.0 ** (ea + eb)
+    assert np.abs(ref).max() < 2.0 ** 128 and np.array_equal(ref, ref.astype(np.float32))
+    got, status = run_mm8(moe, a, (sa.astype(int) + ea).astype(np.uint8), b, (sb.astype(int) + eb).astype(np.uint8), "f32")
+    assert status == 0 and np.array_equal(got, ref)
+
+
+@pytest.mark.parametrize("t", [4, 30])
+def test_experts8_blocks_of_zeros_under_large_scales(moe, t):
+    """A block of weights that are zero adds nothing, whatever its scale and however large x or h is there."""
+    g = np.random.default_rng(t)
+    gu, gus, dn, dns = make_experts(g, 6, 256, 256)
+    x = g.normal(size=(t, 256)).astype(np.float32)
+    x[:, :128] *= np.float32(2.0) ** 118
+    gu[:, :, :128], dn[:, :, :128] = 0, 0
+    gus[:, :, 0], dns[:, :, 0] = 127, 127
+    gus[:, 0, 1], gus[:, 2, 1] = 113 + 59, 113 + 59  # the first 128 channels of h: some 2^110
+    idx, w = np.stack([g.choice(6, size=2, replace=False) for _ in range(t)]), g.random(size=(t, 2)).astype(np.float32)
+    want = run_experts(moe, (gu, gus, dn, dns), cuda(x), idx, w, "f32")
+    assert np.isfinite(want).all() and (want != 0).any()
+    for big in (150, 254):
+        gus2, dns2 = gus.copy(), dns.copy()
+        gus2[:, :, 0] = big
+        assert np.array_equal(run_experts(moe, (gu, gus2, dn, dns), cuda(x), idx, w, "f32"), want)
+        dns2[:, :, 0] = big
+        assert np.array_equal(run_experts(moe, (gu, gus, dn, dns2), cuda(x), idx, w, "f32"), want)
