@@ -357,7 +357,8 @@ typedef struct {
  *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype; out and work must not
  *        overlap the inputs, the layer or one another
  *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned;
- *        calls whose executions overlap need one each
+ *        one for t rows serves every call of fewer rows with this layer and top_k (the function
+ *        does not fall with t); calls whose executions overlap need one each
  * top_k 1..32; t 0..1048576 with t * top_k < 2^31 / 2. */
 int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const uint32_t *topk_idx,
                  const float *topk_w, int top_k, void *out, int out_dtype, void *work, size_t work_bytes,

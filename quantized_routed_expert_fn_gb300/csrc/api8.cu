@@ -1,4 +1,5 @@
 // api8.cu -- C ABI of the 8-bit experts: argument checks and launches.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -179,8 +180,12 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
 
 size_t moe_experts8_workspace(const moe_layer8 *L, int t, int top_k) {
   if (check_layer8(L, t, top_k) != MOE_OK) return 0;
-  const size_t n = moe::ex8_sizes((int)L->hidden, (int)L->n_experts, (int)L->inter, t, top_k).total;
-  return n ? n : 256;
+  // few rows have buffers of their own, which may need more than many rows':
+  // the most that t rows or fewer need
+  size_t n = 256;
+  for (int r = t; r >= 0; r = r > moe::kEx8SmallRows ? moe::kEx8SmallRows : r - 1)
+    n = std::max(n, moe::ex8_sizes((int)L->hidden, (int)L->n_experts, (int)L->inter, r, top_k).total);
+  return n;
 }
 
 int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const uint32_t *topk_idx,

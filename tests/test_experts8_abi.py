@@ -116,6 +116,14 @@ def test_experts8_workspace(m):
     assert ctypes.sizeof(m.MoeLayer8) == 48
 
 
+@pytest.mark.parametrize("k", [1, 8, 32])
+@pytest.mark.parametrize("h,i", [(256, 768), (1024, 2048), (128, 16384), (2048, 512), (16384, 128), (4096, 2048)])
+def test_experts8_workspace_does_not_fall_with_rows(m, h, i, k):
+    """A workspace for the largest batch serves every smaller one (few rows have buffers of their own)."""
+    ws = [m.lib().moe_experts8_workspace(_layer(m, hidden=h, inter=i), t, k) for t in list(range(40)) + [100, 4096]]
+    assert ws[0] > 0 and all(a <= b for a, b in zip(ws, ws[1:]))
+
+
 def test_python_binding_refuses_host_tensors(m):
     torch = pytest.importorskip("torch")
     x = torch.zeros(2, 128)

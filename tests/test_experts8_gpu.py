@@ -864,3 +864,19 @@ def test_experts8_blocks_of_zeros_under_large_scales(moe, t):
         assert np.array_equal(run_experts(moe, (gu, gus2, dn, dns), cuda(x), idx, w, "f32"), want)
         dns2[:, :, 0] = big
         assert np.array_equal(run_experts(moe, (gu, gus, dn, dns2), cuda(x), idx, w, "f32"), want)
+
+
+def test_experts8_one_workspace_for_every_smaller_batch(moe):
+    """A workspace for the largest batch serves all smaller ones, where h is wider than x too."""
+    g = np.random.default_rng(3)
+    e, h, i, k = 10, 256, 768, 8
+    L = moe.Layer8(*[cuda(v) for v in make_experts(g, e, h, i)])
+    work = moe.alloc_workspace(moe.experts8_workspace(L, 9, k))
+    x = cuda(g.normal(size=(9, h)).astype(np.float32))
+    idx = cuda(np.stack([g.choice(e, size=k, replace=False) for _ in range(9)]).astype(np.int32))
+    w = cuda(g.random(size=(9, k)).astype(np.float32))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for t in range(9, 0, -1):
+        o = torch.empty(t, h, device="cuda")
+        moe.experts8(L, x[:t], idx[:t], w[:t], o, work, status)
+        assert status.item() == 0 and torch.isfinite(o).all()
