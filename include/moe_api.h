@@ -282,10 +282,12 @@ enum { MOE_GATE_RENORM = 1 /* weights divided by their sum over the chosen exper
  * order.  Ties go to the lowest id everywhere.  Weights are the p of the
  * chosen experts (never the bias), with MOE_GATE_RENORM divided by their sum,
  * times `scale`.  An expert whose logit or bias is -inf or NaN is masked: it
- * is never chosen and counts in no sum; slots left without an expert get the
- * id 0xffffffff and weight 0 (a fully masked row: all of them).  Comparisons
- * hold as in 64-bit arithmetic: rows whose order 32 bits cannot tell are
- * decided again in 64. */
+ * is never chosen and counts in no group's score.  The softmax runs over every
+ * expert whose logit is not -inf or NaN, those that their bias masks among
+ * them: the bias steers the choice and moves no p.  Slots left without an
+ * expert get the id 0xffffffff and weight 0 (a fully masked row: all of them).
+ * Comparisons hold as in 64-bit arithmetic: rows whose order 32 bits cannot
+ * tell are decided again in 64. */
 typedef struct {
   uint32_t n_experts, top_k; /* n_experts <= 1024, top_k <= min(32, experts of top_groups groups) */
   uint32_t score;            /* MOE_SCORE_* */

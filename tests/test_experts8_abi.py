@@ -157,3 +157,12 @@ def test_reference_gate_by_hand():
     assert idx.tolist() == [[0, 1]] and np.allclose(w, [[0.5, 1 / (1 + np.exp(-1.0))]])
     idx, w = ref8.gate(lg, 3, groups=2, top_groups=1, group_top=2)
     assert idx.tolist() == [[1, 0, -1]] and w[0, 2] == 0
+
+
+def test_reference_gate_softmax_runs_over_experts_a_bias_masks():
+    """The bias moves no p: an expert that it masks is not chosen, but its logit stays in the softmax."""
+    lg = np.log(np.array([[1.0, 2.0, 3.0, 4.0]]))
+    idx, w = ref8.gate(lg, 2, bias=np.array([0.0, 0.0, 0.0, -np.inf]))
+    assert idx.tolist() == [[2, 1]] and np.allclose(w, [[0.3, 0.2]])
+    idx, w = ref8.gate(np.log(np.array([[1.0, 2.0, 3.0, 1e-300]])) + [[0, 0, 0, -np.inf]], 2)
+    assert idx.tolist() == [[2, 1]] and np.allclose(w, [[0.5, 1 / 3]])

@@ -880,3 +880,18 @@ def test_experts8_one_workspace_for_every_smaller_batch(moe):
         o = torch.empty(t, h, device="cuda")
         moe.experts8(L, x[:t], idx[:t], w[:t], o, work, status)
         assert status.item() == 0 and torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("e,o", [(64, {}), (64, dict(n_groups=8, top_groups=3, group_top=2)), (300, dict(scale=2.0))])
+def test_gate_softmax_runs_over_experts_a_bias_masks(moe, e, o):
+    """A bias of -inf or NaN takes an expert out of the choice and of its group's score; the softmax still runs over
+    every expert with a logit, so that an expert's weight does not depend on which others are switched off."""
+    g = np.random.default_rng(e)
+    lg = g.normal(size=(40, e)).astype(np.float32) * 2
+    lg[:, 7] = -np.inf
+    bias = (g.normal(size=e) * 0.1).astype(np.float32)
+    bias[::5], bias[3::7] = -np.inf, np.nan
+    idx, w = check_gate(moe, cuda(lg), 6, cuda(bias), **o)
+    p = np.exp(lg.astype(np.float64))
+    p /= p.sum(1, keepdims=True)
+    assert np.abs(w / o.get("scale", 1.0) - np.take_along_axis(p, idx.astype(np.int64), 1)).max() <= 2.0 ** -19
