@@ -66,13 +66,27 @@ struct Mm8P : Mm8Args {
 };
 enum { kOutF32 = 0, kOutBf16 = 1, kOutSilu8 = 2 };
 // Whether the few-row kernel (weights streamed once into mma.sync) takes t
-// rows: its MMAs are slow, so the larger the weights and the more its groups
-// of eight rows, the sooner the tensor-core kernel, which starts slower, wins.
-// us at n x k, few-row / tensor-core: 16 rows 2048 x 2048 3.9 / 7.3, 8192 x
-// 2048 8.4 / 8.5, 16384 x 4096 23.7 / 15.9; 32 rows 5.4 / 7.4, 16.4 / 8.7,
-// 49.9 / 16.0; 8 rows 16384 x 4096 17.0 / 16.1.
+// rows.  The tensor-core kernel starts slower and takes k in series over n /
+// 256 CTA pairs, whatever t; the few-row kernel shares k out over a CTA's
+// warps, starts a CTA for every 16 of n, and takes longer with every group of
+// eight rows.  us a call, few-row / tensor-core, in a graph of calls on
+// weights that are not in L2 (bf16 out):
+//   n x k          1 row        8 rows       16 rows      32 rows
+//   2048 x 2048     2.9 / 6.4    3.2 / 6.4    3.9 / 6.4    5.7 / 6.5
+//   4096 x 2048     4.2 / 6.5    4.4 / 6.6    5.3 / 6.6    7.5 / 6.6
+//   8192 x 1024     4.1 / 5.5    4.6 / 5.6    6.1 / 5.6    8.6 / 5.6
+//   4096 x 4096     6.4 / 9.2    6.9 / 9.3    8.8 / 9.3   12.8 / 9.4
+//   8192 x 2048     6.1 / 7.3    6.7 / 7.4    9.0 / 7.4   13.5 / 7.4
+//   8192 x 4096    10.4 / 11.0  11.3 / 11.0  15.9 / 11.0  23.7 / 11.1
+//   4096 x 8192    11.0 / 14.4  11.5 / 14.4  15.1 / 14.4  23.1 / 14.6
+//   8192 x 8192    19.0 / 17.8  19.8 / 17.8  27.9 / 17.8  42.8 / 17.8
+//   16384 x 4096   16.6 / 15.2  17.7 / 15.3  26.6 / 15.3  42.6 / 15.2
+//   4096 x 16384   19.7 / 24.6  20.6 / 24.7  27.6 / 24.7  47.3 / 24.7
+//   16384 x 16384  55.9 / 47.2  57.8 / 47.3   100 / 47.5   169 / 47.4
 inline bool mm8_small(int64_t t, int64_t n, int64_t k) {
-  return t <= 8 || (t <= 16 && n * k <= 1 << 24) || (t <= 32 && n * k <= 1 << 23);
+  if (t <= 8) return n <= 4096 || n * k <= 1 << 25;
+  if (t <= 16) return n * k < 1 << 23 || (n <= 4096 && n * k <= 1 << 24);
+  return t <= 32 && n * k <= 1 << 22;
 }
 cudaError_t launch_mm8_small(const Mm8Args &p, int out_kind, cudaStream_t st);
 cudaError_t launch_mm8_tc(const Mm8P &p, int out_kind, int n_sms, cudaStream_t st);

@@ -2,12 +2,13 @@
 // kb of 128 k of 2^(sa[r][kb] + sb[j / 128][kb] - 254) * (a[r] . b[j] in kb).
 //
 // Two kernels:
-//   small  up to 32 rows: the weights are streamed once from HBM
+//   small  up to 32 rows, by mm8_small: the weights are streamed once from HBM
 //          straight into the fragments of mma.sync (no shared memory), the
 //          few rows come from L1; a CTA takes 16 weight rows and splits k
 //          over its warps.
-//          1 x 2048 x 2048: 5.1 us in a graph, of which the 4.2 MB are 0.6: launch
-//          and one HBM latency bound it.
+//          1 x 2048 x 2048: 2.9 us a call in a graph of calls on weights
+//          from HBM, of which the 4.2 MB are 0.6: launch and one HBM latency
+//          bound it.  8 x 8192 x 4096: 11.3, the bytes 5.0.
 //   tc     any number of rows, dense or grouped: persistent, warp
 //          specialised, tcgen05 with the tensor cores' own block scaling
 //          (kind::mxf8f6f4), accumulating all of k in TMEM.

@@ -895,3 +895,17 @@ def test_gate_softmax_runs_over_experts_a_bias_masks(moe, e, o):
     p = np.exp(lg.astype(np.float64))
     p /= p.sum(1, keepdims=True)
     assert np.abs(w / o.get("scale", 1.0) - np.take_along_axis(p, idx.astype(np.int64), 1)).max() <= 2.0 ** -19
+
+
+# ------------------------------------------------------------ mm8: both sides of the few-row rule at large weights
+
+@pytest.mark.parametrize("t,n,k", [(1, 8192, 4096), (8, 8192, 4096), (1, 8192, 4224), (8, 8320, 4096), (5, 2048, 16512), (16, 8192, 2048), (16, 4096, 4096), (16, 4096, 4224),
+                                   (32, 2048, 2048), (32, 2048, 2064)])
+def test_mm8_few_rows_of_large_weights(moe, t, n, k):
+    g = np.random.default_rng(n + t)
+    a, sa, b, sb = operands(g, t, n, k)
+    got, status = run_mm8(moe, a, sa, b, sb, "f32")
+    assert status == 0
+    for r in (slice(0, 128), slice(n // 2 // 128 * 128, n // 2 // 128 * 128 + 128), slice(n - 128, n)):
+        ref, mag = ref8.mm8(a, sa, b[r], sb[r.start // 128: -(-r.stop // 128)])
+        check_mm8(got[:, r], ref, mag, k, "f32")
