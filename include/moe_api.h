@@ -317,9 +317,10 @@ int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int 
                uint8_t *s, int64_t lds, moe_stream_t stream);
 
 /* out[r][j] = sum over k of a[r][k] b[j][k], scaled: the block-scaled 8-bit
- * matrix product, accumulated in fp32 and rounded once to out_dtype.  The two
- * scales of a block may be of any size, whatever their product: what leaves
- * the fp32 range is a partial sum or the result.
+ * matrix product, accumulated in fp32 (by the tensor cores, whose sums cut off
+ * what lies below 2^-23 of them: 1e-6 of the result at k = 8112) and rounded
+ * once to out_dtype.  The two scales of a block may be of any size, whatever
+ * their product: what leaves the fp32 range is a partial sum or the result.
  *   a    e4m3 [t] rows of k, lda bytes apart; 16-byte aligned, lda % 16 == 0
  *   sa   E8M0 [t] rows of ceil(k / 128), lds bytes apart; 4-byte aligned, lds % 4 == 0,
  *        all t * lds bytes readable
@@ -331,7 +332,8 @@ int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int 
  *        [offs[0], offs[n_groups]) are left as they are.  Offsets that do
  *        not ascend or leave 0..t are reported (MOE_EDEVICE) and nothing is
  *        written.
- *   flags 0 (MOE_TEST_WITHHOLD: failure-detection test, grouped form only)
+ *   flags 0 (MOE_TEST_WITHHOLD: failure-detection test of the tensor-core kernel, which then takes
+ *        dense calls of any number of rows)
  * k % 16 == 0, up to 2^24; n_groups <= 1024; t 0..2^30.  The waits inside are
  * bounded as everywhere (MOE_TIMEOUT_MS, here at least 1 ms): MOE_ETIMEOUT. */
 int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t, const uint8_t *b, const uint8_t *sb,
@@ -361,7 +363,7 @@ typedef struct {
  *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned;
  *        one for t rows serves every call of fewer rows with this layer and top_k (the function
  *        does not fall with t); calls whose executions overlap need one each
- * top_k 1..32; t 0..1048576 with t * top_k < 2^31 / 2. */
+ * top_k 1..32; t 0..1048576. */
 int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const uint32_t *topk_idx,
                  const float *topk_w, int top_k, void *out, int out_dtype, void *work, size_t work_bytes,
                  int *dev_status, moe_stream_t stream);
