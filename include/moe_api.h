@@ -325,7 +325,7 @@ int moe_quant8(const void *x, int x_dtype, int64_t ldx, int rows, int cols, int 
  *   sa   E8M0 [t] rows of ceil(k / 128), lds bytes apart; 4-byte aligned, lds % 4 == 0,
  *        all t * lds bytes readable
  *   b    e4m3 [max(n_groups, 1)][n][k], 16-byte aligned; sb E8M0 [..][ceil(n / 128)][ceil(k / 128)]
- *   out  [t] rows of n, ldo elements apart; must not overlap the inputs
+ *   out  [t] rows of n, ldo elements apart; must not overlap the inputs (nor may dev_status overlap any of them)
  *   offs NULL (one weight matrix for every row, n_groups 0), or device int32
  *        [n_groups + 1], ascending, 0 <= offs[g] <= t: rows offs[g] ..
  *        offs[g+1] - 1 are multiplied with b[g]; rows outside
@@ -359,7 +359,7 @@ typedef struct {
  * its first id) contribute nothing; a row without experts gives zeros; an
  * expert twice in a row counts twice.
  *   x    [t][hidden] x_dtype, 16-byte aligned; out [t][hidden] out_dtype; out and work must not
- *        overlap the inputs, the layer or one another
+ *        overlap the inputs, the layer or one another (nor may dev_status overlap any of them)
  *   work device workspace of at least moe_experts8_workspace(L, t, top_k) bytes, 256-byte aligned;
  *        one for t rows serves every call of fewer rows with this layer and top_k (the function
  *        does not fall with t); calls whose executions overlap need one each

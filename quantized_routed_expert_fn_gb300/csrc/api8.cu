@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "api.cuh"
 #include "fp8.cuh"
@@ -28,6 +29,19 @@ int sm_count(int *n) {
 // bytes from the first to the last element of rows x cols, ld elements apart
 size_t span(int64_t rows, int64_t cols, int64_t ld, int size) {
   return rows < 1 ? 0 : ((size_t)(rows - 1) * ld + cols) * size;
+}
+
+// The device status is a word of its own: the kernels zero it while they read
+// and write the other buffers.
+struct Buf {
+  const void *p;
+  size_t n;
+};
+int check_status(const int *st, std::initializer_list<Buf> bufs) {
+  if ((uintptr_t)st & 3u) return fail(MOE_EALIGN, "dev_status is misaligned");
+  for (const Buf &b : bufs)
+    if (b.p && overlap(st, 4, b.p, b.n)) return fail(MOE_EINVAL, "dev_status lies in another buffer");
+  return MOE_OK;
 }
 
 int check_layer8(const moe_layer8 *L, int t, int top_k) {
@@ -132,6 +146,7 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
   if (G * n > INT32_MAX - 256) return fail(MOE_ESHAPE, "n_groups x n exceeds the 2^31 rows a tensor-map coordinate reaches");
   if (nb * (((int64_t)t + 15) / 16 + G) > INT32_MAX) return fail(MOE_ESHAPE, "too many output tiles");
   if (!dev_status) return fail(MOE_EINVAL, "dev_status is NULL");
+  if (int r = check_status(dev_status, {})) return r;
   if (t > 0) {
     if (!a || !sa || !b || !sb || !out) return fail(MOE_EINVAL, "a, sa, b, sb and out are required");
     if (lda < k || lds < nk || ldo < n) return fail(MOE_ESHAPE, "a row stride is below the row's length");
@@ -145,6 +160,9 @@ int moe_mm8(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t lds, int t
         overlap(out, no, b, (size_t)(G * n) * k) || overlap(out, no, sb, (size_t)(G * nb * nk)) ||
         (offs && overlap(out, no, offs, (size_t)(G + 1) * 4)))
       return fail(MOE_EINVAL, "out overlaps an input");
+    if (int r = check_status(dev_status, {{out, no}, {a, span(t, k, lda, 1)}, {sa, span(t, nk, lds, 1)},
+                                          {b, (size_t)(G * n) * k}, {sb, (size_t)(G * nb * nk)}, {offs, (size_t)(G + 1) * 4}}))
+      return r;
   }
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
@@ -198,6 +216,7 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
   if (((uintptr_t)L->gate_up | (uintptr_t)L->down) & 15u)
     return fail(MOE_EALIGN, "gate_up and down must be 16-byte aligned");
   if (!dev_status) return fail(MOE_EINVAL, "dev_status is NULL");
+  if (int r = check_status(dev_status, {})) return r;
   const int H = (int)L->hidden, E = (int)L->n_experts, I = (int)L->inter;
   if ((int64_t)E * 2 * I > INT32_MAX || (int64_t)E * H > INT32_MAX)
     return fail(MOE_ESHAPE, "weight rows exceed the 2^31 rows a tensor-map coordinate reaches");
@@ -222,13 +241,13 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
       overlap(work, z.total, topk_idx, ni) || overlap(work, z.total, topk_w, ni))
     return fail(MOE_EINVAL, "work overlaps x, out, the ids or the weights");
   const size_t ne = (size_t)E * H * I;  // bytes of down; gate_up has twice as many
-  const struct {
-    const void *p;
-    size_t n;
-  } parts[4] = {{L->gate_up, 2 * ne}, {L->gate_up_s, 2 * ne >> 14}, {L->down, ne}, {L->down_s, ne >> 14}};
-  for (const auto &w : parts)
+  const Buf parts[4] = {{L->gate_up, 2 * ne}, {L->gate_up_s, 2 * ne >> 14}, {L->down, ne}, {L->down_s, ne >> 14}};
+  for (const Buf &w : parts)
     if (overlap(w.p, w.n, out, no) || overlap(w.p, w.n, work, z.total))
       return fail(MOE_EINVAL, "out or work overlaps the layer's weights or scales");
+  if (int r = check_status(dev_status, {{x, (size_t)t * H * xs}, {topk_idx, ni}, {topk_w, ni}, {out, no}, {work, z.total},
+                                        parts[0], parts[1], parts[2], parts[3]}))
+    return r;
   moe::Ex8P p{};
   p.H = H, p.E = E, p.I = I, p.t = t, p.K = top_k;
   p.gu = L->gate_up, p.gus = L->gate_up_s, p.dn = L->down, p.dns = L->down_s;

@@ -116,6 +116,25 @@ def test_experts8_workspace(m):
     assert ctypes.sizeof(m.MoeLayer8) == 48
 
 
+@pytest.mark.parametrize("st,code", [
+    (S + 2, -3), (S - 1, -3), (O, -1), (O + 64 * 128 * 4 - 4, -1), (A + 16, -1), (B + 4, -1), (C + 128, -1), (D, -1), (W + 8, -1),
+])
+def test_mm8_refuses_a_status_in_another_buffer(m, st, code):
+    """A misaligned status, or one within out (64 x 128 floats), a, sa, b, sb or the offsets, is refused on the host."""
+    assert _mm8(m, st=st, offs=W, g=2) == code, m.last_error()
+
+
+@pytest.mark.parametrize("st,code", [
+    (S - 254, -3), (S - 255, -3), (S + 64, -1), (O + 16, -1), (O + (1 << 20) + 4092, -1), (W + 4, -1), (W + 4096 + 28, -1),
+    (A + 1024, -1), (B + 28, -1), (C, -1), (D + 12, -1),
+])
+def test_experts8_refuses_a_status_in_another_buffer(m, st, code):
+    """The same for work, x, out (4 x 256 floats), the ids and weights (4 x 2 words) and the layer's four buffers."""
+    assert _ex(m, st=st) == code, m.last_error()
+    if code == -3:
+        assert _ex(m, st=st, t=0) == code
+
+
 @pytest.mark.parametrize("k", [1, 8, 32])
 @pytest.mark.parametrize("h,i", [(256, 768), (1024, 2048), (128, 16384), (2048, 512), (16384, 128), (4096, 2048)])
 def test_experts8_workspace_does_not_fall_with_rows(m, h, i, k):
