@@ -28,7 +28,8 @@
 // the outputs y, and a last kernel sums a row's weighted outputs in the
 // order of its entries.  4096 rows, 10 of 512 experts by Zipf(1.1), 2048 x
 // 512, alone: count 7, scatter 19 (101 MB), gate_up 205 (1.16 GB from HBM, 5.7
-// TB/s; L2 15.5), down 135 (558 MB read, 168 written), sum 36 us (184 MB).
+// TB/s; L2 15.6), down 154 (559 MB read, 288 of 336 written, 5.5 TB/s), sum 60
+// us (336 MB read, 5.8 TB/s); 446 in a graph.
 #include <cuda_runtime.h>
 
 #include "fp8.cuh"
@@ -699,8 +700,8 @@ __global__ void __launch_bounds__(kThreads) ex8_scatter(const __grid_constant__ 
 // bf16 halved its traffic, 395 us instead of 445 for the 4096 rows above in a
 // graph, and its rounding left 1.4 times the error of the last one).
 // U entries' loads are in flight at once: one or two where many warps hide
-// the latency (five took 54 us instead of 35 at 4096 x 10 rows of 2048, for
-// want of warps), eight where there are few.
+// the latency (five took 54 us instead of 35 at 4096 x 10 rows of 2048, then
+// in bf16, for want of warps), eight where there are few.
 template <bool BF16, int U>
 __global__ void __launch_bounds__(256) ex8_combine(const __grid_constant__ Ex8P P) {
   pdl_wait_prev();
