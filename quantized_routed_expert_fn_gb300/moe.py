@@ -467,6 +467,7 @@ class Layer8:
 
 
 def experts8_workspace(layer: Layer8, t: int, top_k: int) -> int:
+    """Bytes experts8 needs for t rows or fewer of this layer and top_k: one workspace for the largest batch serves all."""
     return int(lib().moe_experts8_workspace(layer.c, t, top_k))
 
 
