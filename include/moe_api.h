@@ -266,7 +266,11 @@ int moe_prefill_group(const moe_layer *L, const float *x, int t, uint32_t *topk_
  * one per 128 x 128 block (the last block of a row or a matrix may be
  * smaller).  A power of two keeps the scaling exact, so a value is rounded
  * once, and is what the tensor cores apply by themselves. */
-enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 };
+enum moe_dtype {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_E4M3 = 2 /* an output of moe_norm and moe_add_norm only */
+};
 
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_GATE_RENORM = 1 /* weights divided by their sum over the chosen experts */ };
@@ -368,6 +372,55 @@ int moe_experts8(const moe_layer8 *L, const void *x, int x_dtype, int t, const u
                  const float *topk_w, int top_k, void *out, int out_dtype, void *work, size_t work_bytes,
                  int *dev_status, moe_stream_t stream);
 size_t moe_experts8_workspace(const moe_layer8 *L, int t, int top_k);
+
+/* ---- around the experts' step: the norms of a block, dense products with
+ * what follows them in their epilogue, the answer's log probabilities.
+ *
+ * Matrices are rows of values, each row contiguous, rows ld elements apart
+ * (a multiple of nothing: rows that start on 16 bytes are faster).  Sums and
+ * statistics are held in fp32; a result is rounded once, to its type. */
+
+/* out[r][i] = x[r][i] / sqrt(mean over i of x[r][i]^2 + eps) * w[i]
+ *   x    [t] rows of h, float32 / bf16 (x_dtype)
+ *   w    [h] float32, or NULL (1)
+ *   out  [t] rows of h: MOE_F32, MOE_BF16, or MOE_E4M3 with scales as
+ *        moe_quant8 gives them (a scale byte per 128 of a row, [t] rows of
+ *        ceil(h / 128), lds apart; NULL for the other types); may be x
+ *        itself (same address, stride and type), else overlaps no input
+ * t 0..2^30, h 1..32768; eps positive.  A row whose sum of squares leaves the
+ * fp32 range is normalised all the same; infinities and NaN give what the
+ * formula gives (e4m3: NaN).  Needs no workspace; has no device-side
+ * failures.  This is the x^ of MOE_PRENORM for any row count, with a weight. */
+int moe_norm(const void *x, int x_dtype, int64_t ldx, const float *w, float eps, int t, int h, void *out, int out_dtype,
+             int64_t ldo, uint8_t *scales, int64_t lds, moe_stream_t stream);
+
+enum {
+  MOE_NORM_POST = 1,        /* the block's output is normalised (eps, w_post) before it is added */
+  MOE_NORM_GATE_SIGMOID = 2 /* gates are 1 / (1 + exp(-gate)) */
+};
+typedef struct {
+  uint32_t flags;
+  float eps, scale, res_scale;
+  const float *w_post; /* [h] or NULL (1); with MOE_NORM_POST */
+  const float *w;      /* [h] or NULL (1); of the norm after the sum */
+  const void *gate;    /* rows of gate_cols values, ldg apart (0: one row for all rows), or NULL (1) */
+  int64_t ldg;
+  int gate_dtype; /* MOE_F32 or MOE_BF16 */
+  int gate_cols;  /* 1 (a gate a row) or h */
+} moe_add_norm_cfg;
+
+/* The end of a block and the start of the next, in one pass:
+ *   v = y, or with MOE_NORM_POST its norm with w_post
+ *   s[r][i] = res_scale * residual[r][i] + scale * gate[r][i] * v[r][i]
+ *   res_out = s;  out = norm of s with w (of the 32-bit s, not of the rounded res_out)
+ *   y, residual, res_out  [t] rows of h, float32 / bf16 each; res_out may be
+ *        residual or y itself (same address, stride and type)
+ *   out  as moe_norm's, or NULL: res_out only; may be y itself, else
+ *        overlaps no other buffer
+ * Sizes and values as moe_norm. */
+int moe_add_norm(const moe_add_norm_cfg *cfg, const void *y, int y_dtype, int64_t ldy, const void *residual,
+                 int res_dtype, int64_t ldr, void *res_out, int res_out_dtype, int64_t ldro, int t, int h, void *out,
+                 int out_dtype, int64_t ldo, uint8_t *scales, int64_t lds, moe_stream_t stream);
 
 /* Workspace bytes moe_forward needs for these layers and nb rows (0 if the
  * arguments are invalid). */

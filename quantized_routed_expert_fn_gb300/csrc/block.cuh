@@ -1,0 +1,44 @@
+// block.cuh -- parameters of the kernels around the experts' step: norms with
+// a block's gate and residual, products with an epilogue, log probabilities.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace moe {
+
+// ---- norms (norm.cu)
+enum { kNormOutF32 = 0, kNormOutBf16 = 1, kNormOutE4m3 = 2, kNormOutNone = 3 };
+struct NormP {
+  int t, h;
+  float eps;
+  const void *y;  // [t][h]: what is normalised, or the block's output
+  int64_t ldy;
+  int y_bf16;
+  // the end of a block (res != nullptr)
+  int post, gate_bf16, gate_sigmoid, gate_cols;  // gate_cols: 1 or h
+  float scale, res_scale;
+  const float *wp;   // [h] or nullptr
+  const void *gate;  // or nullptr; rows ldg apart, 0: one row for all
+  int64_t ldg;
+  const void *res;
+  int64_t ldr;
+  void *ro;
+  int64_t ldro;
+  int res_bf16, ro_bf16;
+  // the norm's output
+  int out_kind;
+  const float *w;  // [h] or nullptr
+  void *out;
+  int64_t ldo;
+  uint8_t *s;  // e4m3: a scale byte per 128 of a row
+  int64_t lds;
+  int T;  // threads of a row
+};
+constexpr int kNormMaxCols = 32768;
+cudaError_t launch_norm(const NormP &p, int n_sms, cudaStream_t st);
+
+}  // namespace moe

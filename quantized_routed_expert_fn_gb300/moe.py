@@ -21,9 +21,10 @@ PRENORM = 2
 LOOKAHEAD = 4
 TEST_WITHHOLD = 0x100
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 GATE_RENORM = 1
+NORM_POST, NORM_GATE_SIGMOID = 1, 2
 
 OK, EINVAL, ESHAPE, EALIGN, ECUDA, ETIMEOUT, EDEVICE, ENOSPACE = 0, -1, -2, -3, -4, -5, -6, -7
 STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EALIGN", -4: "MOE_ECUDA",
@@ -31,8 +32,8 @@ STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EALIGN
 
 EXPORTS = ["moe_route", "moe_forward", "moe_forward_traced", "moe_forward_noalloc", "moe_forward_workspace",
            "moe_prefill", "moe_prefill_timed", "moe_prefill_workspace", "moe_prefill_group", "moe_last_error",
-           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_tier_create", "moe_tier_update", "moe_tier_slot", "moe_tier_get_stats", "moe_tier_addresses",
-           "moe_tier_destroy", "moe_tier_last_error"]
+           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_norm", "moe_add_norm",
+           "moe_tier_create", "moe_tier_update", "moe_tier_slot", "moe_tier_get_stats", "moe_tier_addresses", "moe_tier_destroy", "moe_tier_last_error"]
 PREFILL_KERNELS = 10
 PREFILL_KERNEL_NAMES = ["prep", "router_gemm", "topk", "group_count", "group_scan", "group_fill", "gather",
                         "gate_up_gemm", "down_gemm", "output"]
@@ -73,6 +74,13 @@ class MoeLayer8(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_uint32), ("n_experts", ctypes.c_uint32), ("inter", ctypes.c_uint32),
                 ("gate_up", ctypes.c_void_p), ("gate_up_s", ctypes.c_void_p), ("down", ctypes.c_void_p),
                 ("down_s", ctypes.c_void_p)]
+
+
+class MoeAddNormCfg(ctypes.Structure):
+    _fields_ = [("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("w_post", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_dtype", ctypes.c_int),
+                ("gate_cols", ctypes.c_int)]
 
 
 class MoeError(RuntimeError):
@@ -123,6 +131,12 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.moe_experts8_workspace.argtypes = [ctypes.POINTER(MoeLayer8), i32, i32]
         L.moe_experts8.restype = i32
         L.moe_experts8.argtypes = [ctypes.POINTER(MoeLayer8), vp, i32, i32, vp, vp, i32, vp, i32, vp, sz, vp, vp]
+        f32 = ctypes.c_float
+        L.moe_norm.restype = i32
+        L.moe_norm.argtypes = [vp, i32, i64, vp, f32, i32, i32, vp, i32, i64, vp, i64, vp]
+        L.moe_add_norm.restype = i32
+        L.moe_add_norm.argtypes = [ctypes.POINTER(MoeAddNormCfg), vp, i32, i64, vp, i32, i64, vp, i32, i64, i32, i32, vp, i32,
+                                   i64, vp, i64, vp]
         L.moe_tier_create.restype = i32
         L.moe_tier_create.argtypes = [i32, i32, sz, vp, vp, i32, vp, vp, vp, ctypes.POINTER(vp)]
         L.moe_tier_update.restype = i32
@@ -488,6 +502,60 @@ def experts8(layer: Layer8, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: tor
                                         _whole(topk_w, "topk_w", (t, k), _F32, dev), k,
                                         _whole(out, "out", shape, _FLOATS, dev), _FLOATS[out.dtype], wp, wb,
                                         _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
+
+
+# ---- around the experts' step: norms, products with an epilogue, log probabilities
+
+def _norm_out(out, scales, t: int, h: int, dev: int) -> tuple:
+    """(out, its type, its row stride, scales, their row stride) of a norm."""
+    if scales is None:
+        return _arg(out, "out", (t, h), _FLOATS, dev), _FLOATS[out.dtype], _ld(out, t, h), None, 0
+    sc = -(-h // 128)
+    return (_arg(out, "out", (t, h), _E4M3, dev), E4M3, _ld(out, t, h), _arg(scales, "scales", (t, sc), _E8M0, dev),
+            _ld(scales, t, sc))
+
+
+def norm(x: torch.Tensor, out: torch.Tensor, w=None, eps: float = 1e-6, scales=None, stream=None) -> None:
+    """moe_norm: x float32 / bfloat16 [t][h] -> out = x / sqrt(mean(x^2) + eps) * w in float32 / bfloat16, or with
+    scales (E8M0 [t][ceil(h / 128)]) in e4m3 as quant8 gives it; w float32 [h]; row strides as they are."""
+    if x.dim() != 2:
+        _bad(ESHAPE, "x is a matrix")
+    t, h = x.shape
+    dev = _device(x, "x")
+    xp = _arg(x, "x", (t, h), _FLOATS, dev)
+    wp = None if w is None else _whole(w, "w", (h,), _F32, dev)
+    _check((_lib or lib()).moe_norm(xp, _FLOATS[x.dtype], _ld(x, t, h), wp, eps, t, h, *_norm_out(out, scales, t, h, dev),
+                                    _stream_on(stream, dev)))
+
+
+def add_norm(y: torch.Tensor, residual: torch.Tensor, res_out: torch.Tensor, post: bool = False, w_post=None, gate=None,
+             gate_sigmoid: bool = False, scale: float = 1.0, res_scale: float = 1.0, out=None, w=None, scales=None,
+             eps: float = 1e-6, stream=None) -> None:
+    """moe_add_norm: res_out = res_scale * residual + scale * gate * v, v = y or (post) its norm with w_post; with out,
+    out = the norm of that sum with w, as norm gives it.  y, residual, res_out float32 / bfloat16 [t][h] (res_out may be
+    residual or y); gate float32 / bfloat16 [t or 1][h or 1], with gate_sigmoid through a sigmoid."""
+    if y.dim() != 2:
+        _bad(ESHAPE, "y is a matrix")
+    t, h = y.shape
+    dev = _device(y, "y")
+    yp = _arg(y, "y", (t, h), _FLOATS, dev)
+    rp = _arg(residual, "residual", (t, h), _FLOATS, dev)
+    op = _arg(res_out, "res_out", (t, h), _FLOATS, dev)
+    cfg = MoeAddNormCfg((NORM_POST if post else 0) | (NORM_GATE_SIGMOID if gate_sigmoid else 0), eps, scale, res_scale,
+                        None if w_post is None else _whole(w_post, "w_post", (h,), _F32, dev),
+                        None if w is None else _whole(w, "w", (h,), _F32, dev))
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[0] not in (1, t) or gate.shape[1] not in (1, h):
+            _bad(ESHAPE, f"gate has shape {tuple(gate.shape)}, expected [{t} or 1][{h} or 1]")
+        cfg.gate = _arg(gate, "gate", gate.shape, _FLOATS, dev)
+        cfg.gate_dtype, cfg.gate_cols = _FLOATS[gate.dtype], gate.shape[1]
+        cfg.ldg = gate.stride(0) if gate.shape[0] > 1 else 0
+    if out is None and scales is not None:
+        _bad(EINVAL, "scales without out")
+    to = (None, F32, h, None, 0) if out is None else _norm_out(out, scales, t, h, dev)
+    _check((_lib or lib()).moe_add_norm(cfg, yp, _FLOATS[y.dtype], _ld(y, t, h), rp, _FLOATS[residual.dtype],
+                                        _ld(residual, t, h), op, _FLOATS[res_out.dtype], _ld(res_out, t, h), t, h, *to,
+                                        _stream_on(stream, dev)))
 
 
 class Tier:

@@ -1,0 +1,92 @@
+"""Plain 64-bit implementations of the operators around the experts' step (numpy), with bounds of what 32-bit sums and
+the outputs' roundings may change, for the tests."""
+import math
+
+import numpy as np
+
+import ref8
+
+U = 2.0 ** -24  # half a step of 32-bit numbers, relative
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133}  # a step below the normal numbers
+# a 32-bit sum of squares over a row: up to 64 terms a thread one after another, 5 + 4 exchanges, the mean, the root and
+# the quotient; the root halves the sums' part.  In units of U.
+NORM = 64 / 2 + 9 + 4
+
+
+def sigmoid(x):
+    x = np.asarray(x, np.float64)
+    e = np.exp(-np.abs(x))
+    return np.where(x >= 0, 1, e) / (1 + e)
+
+
+def norm(x, w=None, eps=1e-6):
+    with np.errstate(all="ignore"):
+        y = x / np.sqrt((x * x).mean(1, keepdims=True) + np.float64(np.float32(eps)))
+        return y if w is None else y * w
+
+
+def add_norm(y, res, post=False, w_post=None, gate=None, sig=False, scale=1.0, res_scale=1.0, w=None, eps=1e-6):
+    """(sum, its bound, norm, its bound) before the outputs' roundings."""
+    scale, res_scale = np.float64(np.float32(scale)), np.float64(np.float32(res_scale))
+    v = norm(y, w_post, eps) if post else y
+    if gate is not None:
+        v = v * (sigmoid(gate) if sig else gate)
+    s = res_scale * res + scale * v
+    # norm, weight, sigmoid (exponential 2 steps, sum, quotient), gate, two products and the sum
+    ds = (np.abs(scale * v) * ((NORM + 2 if post else 0) + 10) + np.abs(res_scale * res) * 2 + np.abs(s)) * U
+    out = norm(s, w, eps)
+    inv = norm(np.ones_like(s), None, eps)
+    rms = np.sqrt((s * s).mean(1, keepdims=True) + eps)
+    drms = np.sqrt((ds * ds).mean(1, keepdims=True)) / rms  # relative change of the root by the sums' errors
+    dout = ds / rms * (1 if w is None else np.abs(w)) + np.abs(out) * (drms + (NORM + 2) * U)
+    del inv
+    return s, ds, out, dout
+
+
+def check(got, ref, bound, kind, what=""):
+    """got (64-bit copies of a tensor of type `kind`) within `bound` and half a step of ref; what is not finite alike."""
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    top = 3.4028235677973366e38 if kind == "f32" else 3.3961775292304601e38  # from here on a value rounds to infinity
+    ref = np.where(np.abs(ref) >= top, np.sign(ref) * np.inf, ref)
+    fine = np.isfinite(ref)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), what
+    assert np.array_equal(got[~fine & ~np.isnan(ref)], ref[~fine & ~np.isnan(ref)]), what
+    with np.errstate(invalid="ignore"):
+        room = np.broadcast_to(bound, ref.shape) * (1 + HALF[kind]) + np.abs(ref) * HALF[kind] + TINY[kind]
+        bad = fine & ~(np.abs(got - ref) <= room)
+    assert not bad.any(), (what, np.argwhere(bad)[:4].tolist(), got[bad][:4], ref[bad][:4], np.broadcast_to(room, ref.shape)[bad][:4])
+
+
+def check_e4m3(q, s, ref, bound, what=""):
+    """q, s (bytes) as quant8 gives them for some values within `bound` of ref."""
+    t, h = ref.shape
+    for b in range(s.shape[1]):
+        at = slice(128 * b, min(h, 128 * b + 128))
+        y, d = ref[:, at], np.broadcast_to(bound, ref.shape)[:, at]
+        fine = np.isfinite(y)
+        a = np.where(fine, np.abs(y), 0)
+        lo, hi = np.where(fine, np.maximum(a - d, 0), 0).max(1), np.where(fine, a + d, 0).max(1)
+        hi = np.where(a.max(1) == 0, 0, hi)  # zeros are exact
+        for r in range(t):
+            e = int(s[r, b]) - 127
+            ok = {ref8.scale_exponent(lo[r]), ref8.scale_exponent(hi[r])}
+            assert e in ok, (what, r, b, e, ok)
+            f = 2.0 ** -e
+            with np.errstate(invalid="ignore"):
+                c0, c1 = (ref8.E4M3[ref8.round_e4m3(np.clip(v * f, -448, 448))] for v in (y[r] - d[r], y[r] + d[r]))
+            g = ref8.E4M3[q[r, at]]
+            ok = np.where(fine[r], (g >= c0) & (g <= c1), np.isnan(g))
+            assert ok.all(), (what, r, b, np.argwhere(~ok)[:3].tolist())
+
+
+def act(name, z):
+    if name == "silu":
+        return z * sigmoid(z)
+    if name == "gelu":
+        return z * 0.5 * np.vectorize(math.erfc, otypes=[np.float64])(-z * math.sqrt(0.5))
+    if name == "gelu_tanh":
+        return z * sigmoid(math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3))
+    if name == "relu":
+        return np.where(z > 0, z, 0.0) + np.where(np.isnan(z), z, 0.0)
+    return sigmoid(z) if name == "sigmoid" else z
