@@ -422,6 +422,26 @@ int moe_add_norm(const moe_add_norm_cfg *cfg, const void *y, int y_dtype, int64_
                  int res_dtype, int64_t ldr, void *res_out, int res_out_dtype, int64_t ldro, int t, int h, void *out,
                  int out_dtype, int64_t ldo, uint8_t *scales, int64_t lds, moe_stream_t stream);
 
+/* Log probabilities of given tokens, entropy and top alternatives of rows of
+ * logits l, with p = softmax over the row of scale * l:
+ *   logp[r][i] = ln p of token tokens[r][i];  entropy[r] = -sum p ln p;
+ *   top_idx, top_logp [r]: the top_k largest logits in descending order (ties
+ *   to the lowest id) and their ln p
+ * A logit that is -inf or NaN is masked: its p is 0 (ln p -inf), it is no
+ * alternative.  Infinite logits share p among them.  Ids outside 0..v-1 have
+ * ln p -inf.  Alternatives that are missing have the id 0xffffffff and -inf; a
+ * row without a logit has entropy 0.
+ *   logits  [t] rows of v, float32 / bf16, ld apart
+ *   scale   positive (1 / temperature), 1e6 at most
+ *   tokens  [t][m] int32, logp [t][m] float32; NULL when m is 0 (m up to 1024)
+ *   entropy [t] float32, or NULL
+ *   top_idx [t][top_k] uint32, top_logp [t][top_k] float32; NULL when top_k is 0 (up to min(32, v))
+ * t 0..2^27, v 1..2^24.  ln p carries an absolute error of some 2^-23 beside
+ * its relative one (the sum over the row is held to 32 bits).  Needs no
+ * workspace; has no device-side failures. */
+int moe_logprobs(const void *logits, int logit_dtype, int64_t ld, int t, int v, float scale, const int32_t *tokens, int m,
+                 float *logp, float *entropy, uint32_t *top_idx, float *top_logp, int top_k, moe_stream_t stream);
+
 /* Workspace bytes moe_forward needs for these layers and nb rows (0 if the
  * arguments are invalid). */
 size_t moe_forward_workspace(const moe_layer *layers, int n_layers, int nb);

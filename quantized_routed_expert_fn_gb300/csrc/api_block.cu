@@ -159,4 +159,39 @@ int moe_add_norm(const moe_add_norm_cfg *c, const void *y, int y_dtype, int64_t 
   return launch(p, stream);
 }
 
+int moe_logprobs(const void *logits, int logit_dtype, int64_t ld, int t, int v, float scale, const int32_t *tokens, int m,
+                 float *logp, float *entropy, uint32_t *top_idx, float *top_logp, int top_k, moe_stream_t stream) {
+  const int size = float_size(logit_dtype);
+  if (!size) return fail(MOE_EINVAL, "unknown logit_dtype %d", logit_dtype);
+  if (t < 0 || t > kMaxCount / 8) return fail(MOE_ESHAPE, "t %d outside 0..2^27", t);
+  if (v < 1 || v > 1 << 24) return fail(MOE_ESHAPE, "v %d outside 1..2^24", v);
+  if (!(scale > 0.f) || !(scale <= 1e6f)) return fail(MOE_EINVAL, "scale must be positive, 1e6 at most");
+  if (m < 0 || m > 1024) return fail(MOE_ESHAPE, "m %d outside 0..1024", m);
+  if (top_k < 0 || top_k > 32 || top_k > v) return fail(MOE_ESHAPE, "top_k %d outside 0..min(32, v)", top_k);
+  if (t == 0) return MOE_OK;
+  if (m == 0 && top_k == 0 && !entropy) return fail(MOE_EINVAL, "nothing is asked for");
+  if ((m > 0) != (tokens != nullptr) || (m > 0) != (logp != nullptr))
+    return fail(MOE_EINVAL, "tokens, logp and m go together");
+  if ((top_k > 0) != (top_idx != nullptr) || (top_k > 0) != (top_logp != nullptr))
+    return fail(MOE_EINVAL, "top_idx, top_logp and top_k go together");
+  const Mat ml{logits, t, v, ld, size}, mt{tokens, t, m, m, 4}, mk{top_idx, t, top_k, top_k, 4};
+  const Mat outs[4] = {{logp, t, m, m, 4}, {entropy, t, 1, 1, 4}, mk, {top_logp, t, top_k, top_k, 4}};
+  if (int r = check_mat(ml, "logits")) return r;
+  if (((uintptr_t)tokens | (uintptr_t)logp | (uintptr_t)entropy | (uintptr_t)top_idx | (uintptr_t)top_logp) & 3u)
+    return fail(MOE_EALIGN, "misaligned pointer");
+  for (int i = 0; i < 4; i++) {
+    if (!apart(outs[i], ml) || !apart(outs[i], mt)) return fail(MOE_EINVAL, "an output overlaps the logits or the tokens");
+    for (int j = 0; j < i; j++)
+      if (!apart(outs[i], outs[j])) return fail(MOE_EINVAL, "two outputs overlap");
+  }
+  moe::LogprobsP p{};
+  p.x = logits, p.ld = ld, p.bf16 = logit_dtype == MOE_BF16, p.t = t, p.v = v, p.scale = scale;
+  p.tokens = tokens, p.m = m, p.logp = logp, p.entropy = entropy;
+  p.top_idx = top_idx, p.top_logp = top_logp, p.k = top_k;
+  int n_sms = 0;
+  if (int r = sm_count(&n_sms)) return r;
+  const cudaError_t e = moe::launch_logprobs(p, n_sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+}
+
 }  // extern "C"

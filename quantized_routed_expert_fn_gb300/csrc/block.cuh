@@ -41,4 +41,21 @@ struct NormP {
 constexpr int kNormMaxCols = 32768;
 cudaError_t launch_norm(const NormP &p, int n_sms, cudaStream_t st);
 
+// ---- log probabilities (logprobs.cu)
+struct LogprobsP {
+  const void *x;  // [t][v]
+  int64_t ld;
+  int bf16, t, v;
+  float scale;
+  const int32_t *tokens;  // [t][m]
+  int m;
+  float *logp;     // [t][m]
+  float *entropy;  // [t] or nullptr
+  uint32_t *top_idx;  // [t][k]
+  float *top_logp;
+  int k;
+  int S, seg;  // blocks of a row, values of a block
+};
+cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st);
+
 }  // namespace moe

@@ -32,7 +32,7 @@ STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EALIGN
 
 EXPORTS = ["moe_route", "moe_forward", "moe_forward_traced", "moe_forward_noalloc", "moe_forward_workspace",
            "moe_prefill", "moe_prefill_timed", "moe_prefill_workspace", "moe_prefill_group", "moe_last_error",
-           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_norm", "moe_add_norm",
+           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_norm", "moe_add_norm", "moe_logprobs",
            "moe_tier_create", "moe_tier_update", "moe_tier_slot", "moe_tier_get_stats", "moe_tier_addresses", "moe_tier_destroy", "moe_tier_last_error"]
 PREFILL_KERNELS = 10
 PREFILL_KERNEL_NAMES = ["prep", "router_gemm", "topk", "group_count", "group_scan", "group_fill", "gather",
@@ -137,6 +137,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.moe_add_norm.restype = i32
         L.moe_add_norm.argtypes = [ctypes.POINTER(MoeAddNormCfg), vp, i32, i64, vp, i32, i64, vp, i32, i64, i32, i32, vp, i32,
                                    i64, vp, i64, vp]
+        L.moe_logprobs.restype = i32
+        L.moe_logprobs.argtypes = [vp, i32, i64, i32, i32, f32, vp, i32, vp, vp, vp, vp, i32, vp]
         L.moe_tier_create.restype = i32
         L.moe_tier_create.argtypes = [i32, i32, sz, vp, vp, i32, vp, vp, vp, ctypes.POINTER(vp)]
         L.moe_tier_update.restype = i32
@@ -555,6 +557,32 @@ def add_norm(y: torch.Tensor, residual: torch.Tensor, res_out: torch.Tensor, pos
     to = (None, F32, h, None, 0) if out is None else _norm_out(out, scales, t, h, dev)
     _check((_lib or lib()).moe_add_norm(cfg, yp, _FLOATS[y.dtype], _ld(y, t, h), rp, _FLOATS[residual.dtype],
                                         _ld(residual, t, h), op, _FLOATS[res_out.dtype], _ld(res_out, t, h), t, h, *to,
+                                        _stream_on(stream, dev)))
+
+
+def logprobs(logits: torch.Tensor, tokens=None, logp=None, entropy=None, top_idx=None, top_logp=None, scale: float = 1.0,
+             stream=None) -> None:
+    """moe_logprobs: logits float32 / bfloat16 [t][v] (any row stride), p = softmax(scale * logits) -> logp float32 [t][m]
+    of tokens int32 [t][m], entropy float32 [t], top_idx int32 and top_logp float32 [t][k]; any of the three."""
+    if logits.dim() != 2 or (tokens is None) != (logp is None) or (top_idx is None) != (top_logp is None):
+        _bad(ESHAPE, "logits is a matrix; tokens and logp, top_idx and top_logp go together")
+    t, v = logits.shape
+    dev = _device(logits, "logits")
+    lp = _arg(logits, "logits", (t, v), _FLOATS, dev)
+    m = k = 0
+    tp = op = ip = xp = None
+    if tokens is not None:
+        if tokens.dim() != 2 or not tokens.shape[1]:
+            _bad(ESHAPE, "tokens is [t][m]")
+        m = tokens.shape[1]
+        tp, op = _whole(tokens, "tokens", (t, m), _I32, dev), _whole(logp, "logp", (t, m), _F32, dev)
+    if top_idx is not None:
+        if top_idx.dim() != 2 or not top_idx.shape[1]:
+            _bad(ESHAPE, "top_idx is [t][k]")
+        k = top_idx.shape[1]
+        ip, xp = _whole(top_idx, "top_idx", (t, k), _I32, dev), _whole(top_logp, "top_logp", (t, k), _F32, dev)
+    ep = None if entropy is None else _whole(entropy, "entropy", (t,), _F32, dev)
+    _check((_lib or lib()).moe_logprobs(lp, _FLOATS[logits.dtype], _ld(logits, t, v), t, v, scale, tp, m, op, ep, ip, xp, k,
                                         _stream_on(stream, dev)))
 
 

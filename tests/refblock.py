@@ -90,3 +90,27 @@ def act(name, z):
     if name == "relu":
         return np.where(z > 0, z, 0.0) + np.where(np.isnan(z), z, 0.0)
     return sigmoid(z) if name == "sigmoid" else z
+
+
+def logprobs(x, tokens, k, scale=1.0):
+    """(logp, entropy, top ids, their logp, bound of log Z's error) of rows x in 64 bits."""
+    scale = np.float64(np.float32(scale))
+    t, v = x.shape
+    with np.errstate(all="ignore"):
+        live = x > -np.inf  # false for NaN
+        top = np.where(live.any(1), np.where(live, x, -np.inf).max(1), 0.0)[:, None]
+        d = np.where(live, np.where(x == top, 0.0, scale * (x - top)), -np.inf)
+        e = np.exp(d)
+        z = e.sum(1, keepdims=True)
+        lp = d - np.log(z)
+        lp[~live] = -np.inf
+        p = e / z
+        ent = np.where(live.any(1), -np.where(p > 0, p * lp, 0.0).sum(1), 0.0)
+        spread = np.where(live.any(1), np.where(p > 0, p * np.abs(d), 0.0).sum(1), 0.0)
+    # terms: the exponent's rounding (its size, weighted), the exponential (2^-22), a thread's own sum, the tree
+    dz = (max(64, v // 128) + 40 + 8 * spread / math.log(2)) * U
+    inside = (tokens >= 0) & (tokens < v)
+    given = np.where(inside, np.take_along_axis(lp, np.where(inside, tokens, 0), 1), -np.inf)
+    order = np.argsort(np.where(live, -x, np.inf), axis=1, kind="stable")[:, :k]
+    none = ~np.take_along_axis(live, order, 1)
+    return given, ent, np.where(none, -1, order), np.where(none, -np.inf, np.take_along_axis(lp, order, 1)), dz[:, None]

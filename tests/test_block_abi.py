@@ -101,3 +101,33 @@ def test_reference_activations_by_hand():
     assert np.allclose(refblock.act("gelu", z), [-0.04550026389635842, 0, 2.99595030634], atol=1e-9)
     assert np.allclose(refblock.act("gelu_tanh", z), 0.5 * z * (1 + np.tanh((2 / np.pi) ** 0.5 * (z + 0.044715 * z ** 3))))
     assert np.allclose(refblock.act("relu", z), [0, 0, 3]) and np.allclose(refblock.act("sigmoid", z), 1 / (1 + np.exp(-z)))
+
+
+def _lp(m, x=X, xd=0, ld=1000, t=4, v=1000, scale=1.0, tok=Y, n=2, lp=O, ent=P, idx=W, tl=G, k=8):
+    return m.lib().moe_logprobs(x, xd, ld, t, v, scale, tok, n, lp, ent, idx, tl, k, None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(xd=2), -1), (dict(t=-1), -2), (dict(t=(1 << 27) + 1), -2), (dict(v=0), -2), (dict(v=(1 << 24) + 1, ld=1 << 25), -2),
+    (dict(scale=0.0), -1), (dict(scale=-1.0), -1), (dict(scale=NAN), -1), (dict(scale=INF), -1), (dict(scale=2e6), -1),
+    (dict(n=-1), -2), (dict(n=1025), -2), (dict(k=33), -2), (dict(k=-1), -2), (dict(v=4, k=5), -2), (dict(x=None), -1),
+    (dict(tok=None), -1), (dict(lp=None), -1), (dict(n=0), -1), (dict(idx=None), -1), (dict(tl=None), -1), (dict(k=0), -1),
+    (dict(n=0, tok=None, lp=None, k=0, idx=None, tl=None, ent=None), -1), (dict(ld=999), -2), (dict(x=X + 2), -3), (dict(tok=Y + 2), -3),
+    (dict(ent=P + 1), -3), (dict(lp=X + 64), -1), (dict(ent=Y), -1), (dict(idx=O), -1), (dict(tl=W), -1), (dict(ent=G + 4), -1),
+])
+def test_logprobs_refusals(m, over, code):
+    assert _lp(m, **over) == code, m.last_error()
+
+
+def test_empty_logprobs_need_no_pointers(m):
+    assert _lp(m, t=0, x=None, tok=None, lp=None, idx=None, tl=None) == 0
+
+
+def test_reference_logprobs_by_hand():
+    x = np.log(np.array([[1.0, 2.0, 2.0, 5.0]]))
+    lp, ent, idx, tl, _ = refblock.logprobs(x, np.array([[0, 3, 4, -1]]), 3)
+    assert np.allclose(lp[0, :2], np.log([0.1, 0.5])) and np.isneginf(lp[0, 2:]).all()
+    assert np.allclose(ent, -sum(p * np.log(p) for p in (0.1, 0.2, 0.2, 0.5)))
+    assert idx.tolist() == [[3, 1, 2]] and np.allclose(tl, np.log([[0.5, 0.2, 0.2]]))
+    lp, ent, idx, tl, _ = refblock.logprobs(np.array([[np.nan, -np.inf]]), np.array([[0]]), 2)
+    assert np.isneginf(lp).all() and ent[0] == 0 and idx.tolist() == [[-1, -1]]
