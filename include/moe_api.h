@@ -422,6 +422,46 @@ int moe_add_norm(const moe_add_norm_cfg *cfg, const void *y, int y_dtype, int64_
                  int res_dtype, int64_t ldr, void *res_out, int res_out_dtype, int64_t ldro, int t, int h, void *out,
                  int out_dtype, int64_t ldo, uint8_t *scales, int64_t lds, moe_stream_t stream);
 
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,      /* z / (1 + exp(-z)) */
+  MOE_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  MOE_ACT_RELU = 4,
+  MOE_ACT_SIGMOID = 5
+};
+/* What follows a product in its epilogue; all zero: nothing. */
+typedef struct {
+  uint32_t act;           /* MOE_ACT_* */
+  int res_dtype;          /* of residual: MOE_F32 or MOE_BF16 */
+  const float *bias;      /* [n] (gated: [2n]) or NULL */
+  const float *row_scale; /* [t] or NULL (1): a shared expert's gate */
+  const void *residual;   /* [t] rows of n, ldr apart, or NULL */
+  int64_t ldr;
+} moe_epilogue;
+enum { MOE_MM16_GATED = 1 /* b holds 2n rows: rows 0..n-1 the gate, then up */ };
+
+/* The bf16 matrix product with its epilogue: logits for moe_gate, a shared
+ * expert beside moe_experts8, projections, the vocabulary product.
+ *   z[r][j] = sum over k of a[r][k] b[j][k] + bias[j]
+ *   h = act(z), with MOE_MM16_GATED  h[r][j] = act(z[r][j]) * z[r][n + j]
+ *   out[r][j] = row_scale[r] * h[r][j] + residual[r][j]
+ * in fp32 (the tensor cores' sums cut off what lies below 2^-23 of them) up to
+ * the one rounding to out's type.
+ *   a    bf16 [t] rows of k, lda apart;  b bf16 [n] (gated [2n]) rows of k,
+ *        ldb apart; both and their rows start on 16 bytes (lda, ldb % 8 == 0),
+ *        k itself may be odd
+ *   out  [t] rows of n, MOE_F32 or MOE_BF16; may be the residual itself (same
+ *        address, stride and type), else overlaps no input (nor may dev_status
+ *        overlap anything)
+ *   epi  NULL: the product alone
+ *   flags  MOE_MM16_GATED (MOE_TEST_WITHHOLD: failure-detection test of the
+ *        tensor-core kernel, which then takes any number of rows)
+ * k up to 2^24; t 0..2^30.  The waits inside are bounded as everywhere
+ * (MOE_TIMEOUT_MS, here at least 1 ms): MOE_ETIMEOUT in *dev_status. */
+int moe_mm16(const uint16_t *a, int64_t lda, int t, const uint16_t *b, int64_t ldb, int n, int k, const moe_epilogue *epi,
+             void *out, int out_dtype, int64_t ldo, uint32_t flags, int *dev_status, moe_stream_t stream);
+
 /* Log probabilities of given tokens, entropy and top alternatives of rows of
  * logits l, with p = softmax over the row of scale * l:
  *   logp[r][i] = ln p of token tokens[r][i];  entropy[r] = -sum p ln p;

@@ -13,7 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["decode.cu", "prefill.cu", "mm8.cu", "experts8.cu",
-           "norm.cu", "logprobs.cu", "gate.cu", "quant8.cu", "api.cu", "api8.cu", "api_block.cu", "tier.cu"]
+           "mm16.cu", "norm.cu", "logprobs.cu", "gate.cu", "quant8.cu", "api.cu", "api8.cu", "api_block.cu", "tier.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

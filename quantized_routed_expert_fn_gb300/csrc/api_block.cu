@@ -194,4 +194,65 @@ int moe_logprobs(const void *logits, int logit_dtype, int64_t ld, int t, int v, 
   return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
 }
 
+int moe_mm16(const uint16_t *a, int64_t lda, int t, const uint16_t *b, int64_t ldb, int n, int k, const moe_epilogue *epi,
+             void *out, int out_dtype, int64_t ldo, uint32_t flags, int *dev_status, moe_stream_t stream) {
+  static const moe_epilogue none = {};
+  const moe_epilogue &E = epi ? *epi : none;
+  const int os = float_size(out_dtype);
+  if (!os) return fail(MOE_EINVAL, "unknown out_dtype %d", out_dtype);
+  if (flags & ~(uint32_t)(MOE_MM16_GATED | MOE_TEST_WITHHOLD)) return fail(MOE_EINVAL, "unknown flags 0x%x", flags);
+  if (E.act > MOE_ACT_SIGMOID) return fail(MOE_EINVAL, "unknown act %u", E.act);
+  const bool gated = (flags & MOE_MM16_GATED) != 0;
+  if (t < 0 || t > kMaxCount || n < 1 || k < 1 || k > 1 << 24) return fail(MOE_ESHAPE, "t %d, n %d, k %d", t, n, k);
+  const int64_t wrows = gated ? 2 * (int64_t)n : n;
+  if (wrows > INT32_MAX - 256) return fail(MOE_ESHAPE, "more weight rows than a tensor-map coordinate reaches");
+  if (((int64_t)t / 16 + 1) * (n / 64 + 2) > INT32_MAX) return fail(MOE_ESHAPE, "too many output tiles");
+  int rs = 2;
+  if (E.residual) {
+    rs = float_size(E.res_dtype);
+    if (!rs) return fail(MOE_EINVAL, "unknown res_dtype %d", E.res_dtype);
+  }
+  if (!dev_status) return fail(MOE_EINVAL, "dev_status is NULL");
+  if ((uintptr_t)dev_status & 3u) return fail(MOE_EALIGN, "dev_status is misaligned");
+  cudaStream_t st = (cudaStream_t)stream;
+  if (t == 0) {
+    const cudaError_t e = cudaMemsetAsync(dev_status, 0, 4, st);
+    return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "memset failed: %s", cudaGetErrorString(e));
+  }
+  const Mat ma{a, t, k, lda, 2}, mb{b, wrows, k, ldb, 2}, mo{out, t, n, ldo, os}, mr{E.residual, t, n, E.ldr, rs};
+  const Mat mbias{E.bias, 1, wrows, wrows, 4}, mrs{E.row_scale, 1, t, t, 4}, mst{dev_status, 1, 1, 1, 4};
+  if (int r = check_mat(ma, "a")) return r;
+  if (int r = check_mat(mb, "b")) return r;
+  if (int r = check_mat(mo, "out")) return r;
+  if (E.residual)
+    if (int r = check_mat(mr, "residual")) return r;
+  if ((((uintptr_t)a | (uintptr_t)b) & 15u) || lda % 8 || ldb % 8)
+    return fail(MOE_EALIGN, "a, b and their rows must start on 16 bytes");
+  if (((uintptr_t)E.bias | (uintptr_t)E.row_scale) & 3u) return fail(MOE_EALIGN, "bias or row_scale is misaligned");
+  if (!apart(mo, ma) || !apart(mo, mb) || !apart(mo, mbias) || !apart(mo, mrs)) return fail(MOE_EINVAL, "out overlaps an input");
+  if (!apart_or_same(mo, mr)) return fail(MOE_EINVAL, "out overlaps the residual (it may be the residual itself, in its type)");
+  for (const Mat *m : {&ma, &mb, &mo, &mr, &mbias, &mrs})
+    if (!apart(mst, *m)) return fail(MOE_EINVAL, "dev_status lies in another buffer");
+  moe::Mm16P p;
+  memset(&p, 0, sizeof p);
+  p.a = a, p.lda = lda, p.b = b, p.ldb = ldb, p.t = t, p.n = n, p.k = k, p.gated = gated, p.act = (int)E.act;
+  p.bias = E.bias, p.row_scale = E.row_scale, p.res = E.residual, p.ldr = E.ldr, p.res_bf16 = E.res_dtype == MOE_BF16;
+  p.out = out, p.ldo = ldo, p.out_bf16 = out_dtype == MOE_BF16;
+  auto whole = [](const Mat &m) { return !m.p || (((uintptr_t)m.p | (uintptr_t)(m.ld * m.size)) & (4u * m.size - 1)) == 0; };
+  p.wide = whole(mo) && whole(mr);
+  p.withhold = (flags & MOE_TEST_WITHHOLD) != 0;
+  p.status = dev_status;
+  p.timeout_ns = moe::timeout_ns();
+  if (p.timeout_ns < 1000000) p.timeout_ns = 1000000;  // a wait gives up no sooner than the status is zeroed
+  cudaError_t e;
+  if (moe::mm16_few(t, n, k) && !p.withhold) {
+    e = moe::launch_mm16_few(p, st);
+  } else {
+    int n_sms = 0;
+    if (int r = sm_count(&n_sms)) return r;
+    e = moe::launch_mm16_tc(p, n_sms, st);
+  }
+  return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+}
+
 }  // extern "C"

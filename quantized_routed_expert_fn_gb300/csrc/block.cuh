@@ -58,4 +58,33 @@ struct LogprobsP {
 };
 cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st);
 
+// ---- products with an epilogue (mm16.cu)
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3, kActRelu = 4, kActSigmoid = 5 };
+struct Mm16Args {
+  const uint16_t *a, *b;  // bf16 [t][k]; [n][k], gated [2n][k]
+  int64_t lda, ldb;
+  int t, n, k, gated, act;
+  const float *bias;       // [n] (gated [2n]) or nullptr
+  const float *row_scale;  // [t] or nullptr
+  const void *res;         // [t][n] or nullptr
+  int64_t ldr;
+  int res_bf16, out_bf16;
+  void *out;
+  int64_t ldo;
+  int wide;  // four neighbouring values of out (and residual) are one access
+  int withhold;
+  int *status;
+  unsigned long long timeout_ns;
+  // tensor cores: tokens of a tile, k blocks, weight and token tiles, CTAs
+  // that split k, ring
+  int w, nk, nmt, ntt, split, stage, stages;
+};
+struct Mm16P : Mm16Args {
+  CUtensorMap tm_a, tm_b;
+};
+// Whether the few-row kernel takes t rows.
+inline bool mm16_few(int64_t t, int64_t, int64_t) { return t <= 8; }
+cudaError_t launch_mm16_few(const Mm16Args &p, cudaStream_t st);
+cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st);
+
 }  // namespace moe

@@ -25,6 +25,8 @@ F32, BF16, E4M3 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 GATE_RENORM = 1
 NORM_POST, NORM_GATE_SIGMOID = 1, 2
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4, "sigmoid": 5}
+MM16_GATED = 1
 
 OK, EINVAL, ESHAPE, EALIGN, ECUDA, ETIMEOUT, EDEVICE, ENOSPACE = 0, -1, -2, -3, -4, -5, -6, -7
 STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EALIGN", -4: "MOE_ECUDA",
@@ -32,7 +34,8 @@ STATUS_NAMES = {0: "MOE_OK", -1: "MOE_EINVAL", -2: "MOE_ESHAPE", -3: "MOE_EALIGN
 
 EXPORTS = ["moe_route", "moe_forward", "moe_forward_traced", "moe_forward_noalloc", "moe_forward_workspace",
            "moe_prefill", "moe_prefill_timed", "moe_prefill_workspace", "moe_prefill_group", "moe_last_error",
-           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_norm", "moe_add_norm", "moe_logprobs",
+           "moe_gate", "moe_quant8", "moe_mm8", "moe_experts8", "moe_experts8_workspace", "moe_norm", "moe_add_norm", "moe_mm16",
+           "moe_logprobs",
            "moe_tier_create", "moe_tier_update", "moe_tier_slot", "moe_tier_get_stats", "moe_tier_addresses", "moe_tier_destroy", "moe_tier_last_error"]
 PREFILL_KERNELS = 10
 PREFILL_KERNEL_NAMES = ["prep", "router_gemm", "topk", "group_count", "group_scan", "group_fill", "gather",
@@ -81,6 +84,11 @@ class MoeAddNormCfg(ctypes.Structure):
                 ("res_scale", ctypes.c_float), ("w_post", ctypes.c_void_p), ("w", ctypes.c_void_p),
                 ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_dtype", ctypes.c_int),
                 ("gate_cols", ctypes.c_int)]
+
+
+class MoeEpilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_uint32), ("res_dtype", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("row_scale", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -137,6 +145,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.moe_add_norm.restype = i32
         L.moe_add_norm.argtypes = [ctypes.POINTER(MoeAddNormCfg), vp, i32, i64, vp, i32, i64, vp, i32, i64, i32, i32, vp, i32,
                                    i64, vp, i64, vp]
+        L.moe_mm16.restype = i32
+        L.moe_mm16.argtypes = [vp, i64, i32, vp, i64, i32, i32, ctypes.POINTER(MoeEpilogue), vp, i32, i64, u32, vp, vp]
         L.moe_logprobs.restype = i32
         L.moe_logprobs.argtypes = [vp, i32, i64, i32, i32, f32, vp, i32, vp, vp, vp, vp, i32, vp]
         L.moe_tier_create.restype = i32
@@ -391,6 +401,11 @@ def _ld(t, rows: int, cols: int) -> int:
     return t.stride(0) if rows > 1 else cols
 
 
+def _ld16(t, rows: int, cols: int) -> int:
+    """The same for rows that start on 16 bytes."""
+    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
+
+
 @functools.lru_cache(maxsize=64)
 def _gate_cfg(n_experts, top_k, score, n_groups, top_groups, group_top, flags, scale) -> MoeGateCfg:
     if score not in SCORES:
@@ -558,6 +573,37 @@ def add_norm(y: torch.Tensor, residual: torch.Tensor, res_out: torch.Tensor, pos
     _check((_lib or lib()).moe_add_norm(cfg, yp, _FLOATS[y.dtype], _ld(y, t, h), rp, _FLOATS[residual.dtype],
                                         _ld(residual, t, h), op, _FLOATS[res_out.dtype], _ld(res_out, t, h), t, h, *to,
                                         _stream_on(stream, dev)))
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def mm16(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, status: torch.Tensor, bias=None, act: str = "none",
+         gated: bool = False, row_scale=None, residual=None, flags: int = 0, stream=None) -> None:
+    """moe_mm16: z = a b^T + bias of a bfloat16 [t][k], b bfloat16 [n][k] (gated: [2n][k], the gate's rows first; rows of
+    both start on 16 bytes) -> out float32 / bfloat16 [t][n] = row_scale * act(z) + residual, gated row_scale * act(z[:, :n])
+    * z[:, n:] + residual; bias float32 [n] ([2n]), row_scale float32 [t], residual float32 / bfloat16 [t][n] (out may be it)."""
+    if a.dim() != 2 or b.dim() != 2:
+        _bad(ESHAPE, "a and b are matrices")
+    t, k = a.shape
+    rows = b.shape[0]
+    n = rows // 2 if gated else rows
+    dev = _device(a, "a")
+    ap = _arg(a, "a", (t, k), _BF16, dev)
+    bp = _arg(b, "b", (2 * n if gated else n, k), _BF16, dev)
+    op = _arg(out, "out", (t, n), _FLOATS, dev)
+    epi = None
+    if act != "none" or bias is not None or row_scale is not None or residual is not None:
+        if act not in ACTS:
+            _bad(EINVAL, f"unknown act {act!r}")
+        epi = MoeEpilogue(ACTS[act], F32, None if bias is None else _whole(bias, "bias", (rows,), _F32, dev),
+                          None if row_scale is None else _whole(row_scale, "row_scale", (t,), _F32, dev))
+        if residual is not None:
+            epi.residual = _arg(residual, "residual", (t, n), _FLOATS, dev)
+            epi.res_dtype, epi.ldr = _FLOATS[residual.dtype], _ld(residual, t, n)
+    _check((_lib or lib()).moe_mm16(ap, _ld16(a, t, k), t, bp, _ld16(b, rows, k), n, k, epi, op, _FLOATS[out.dtype],
+                                    _ld(out, t, n), flags | MM16_GATED if gated else flags,
+                                    _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
 
 
 def logprobs(logits: torch.Tensor, tokens=None, logp=None, entropy=None, top_idx=None, top_logp=None, scale: float = 1.0,

@@ -114,3 +114,34 @@ def logprobs(x, tokens, k, scale=1.0):
     order = np.argsort(np.where(live, -x, np.inf), axis=1, kind="stable")[:, :k]
     none = ~np.take_along_axis(live, order, 1)
     return given, ent, np.where(none, -1, order), np.where(none, -np.inf, np.take_along_axis(lp, order, 1)), dz[:, None]
+
+
+def act_bound(name, x, h):
+    """What 32 bits may change in h = act(x): exponentials and quotients of two steps each, and their arguments' roundings."""
+    own = {"none": 0, "relu": 0, "silu": 16, "sigmoid": 16, "gelu": 32 + 4 * x * x,
+           "gelu_tanh": 32 + 8 * (1.6 * np.abs(x) + 0.072 * np.abs(x) ** 3)}[name]
+    return np.abs(h) * own * U
+
+
+def mm16(a, b, gated=False, a_act="none", bias=None, row_scale=None, res=None):
+    """(out, bound before the output's rounding) in 64 bits.  Sums: every term of a 16-wide step may lose what lies below
+    2^-23 of the sum, in all k 2^-23 of the terms' magnitudes; the activations: exponentials and quotients of two steps
+    each, and what their arguments' roundings do."""
+    k = a.shape[1]
+    z, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+    if bias is not None:
+        z, mag = z + bias, mag + np.abs(bias)
+    dz = (k + 2) * 2.0 ** -23 * mag
+    n = b.shape[0] // 2 if gated else b.shape[0]
+    x, dx = z[:, :n], dz[:, :n]
+    h = act(a_act, x)
+    dh = dx * 1.2 + act_bound(a_act, x, h)
+    if gated:
+        u, du = z[:, n:], dz[:, n:]
+        h, dh = h * u, dh * np.abs(u) + np.abs(h) * du + dh * du + np.abs(h * u) * U
+    if row_scale is not None:
+        h, dh = h * row_scale[:, None], dh * np.abs(row_scale[:, None]) + np.abs(h * row_scale[:, None]) * U
+    if res is not None:
+        h = h + res
+        dh = dh + np.abs(h) * U
+    return h, dh

@@ -131,3 +131,40 @@ def test_reference_logprobs_by_hand():
     assert idx.tolist() == [[3, 1, 2]] and np.allclose(tl, np.log([[0.5, 0.2, 0.2]]))
     lp, ent, idx, tl, _ = refblock.logprobs(np.array([[np.nan, -np.inf]]), np.array([[0]]), 2)
     assert np.isneginf(lp).all() and ent[0] == 0 and idx.tolist() == [[-1, -1]]
+
+
+A, B2, RES, ST = 0x1000000, 0x2000000, 0x3000000, 0x4000000
+
+
+def _mm(m, a=A, lda=256, t=64, b=B2, ldb=256, n=128, k=256, out=O, od=0, ldo=128, flags=0, st=ST, epi=True, **e):
+    ep = m.MoeEpilogue(*(dict(act=0, res_dtype=0, bias=None, row_scale=None, residual=None, ldr=128) | e).values()) if epi else None
+    return m.lib().moe_mm16(a, lda, t, b, ldb, n, k, ep, out, od, ldo, flags, st, None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(od=2), -1), (dict(flags=2), -1), (dict(act=6), -1), (dict(t=-1), -2), (dict(n=0), -2), (dict(k=0), -2), (dict(k=(1 << 24) + 1), -2),
+    (dict(t=(1 << 30) + 1), -2), (dict(n=1 << 30, flags=1), -2), (dict(t=1 << 30, n=1 << 20, ldo=1 << 20), -2), (dict(residual=RES, res_dtype=2), -1),
+    (dict(st=None), -1), (dict(st=ST + 2), -3), (dict(a=None), -1), (dict(b=None), -1), (dict(out=None), -1), (dict(lda=248), -2),
+    (dict(ldb=0), -2), (dict(ldo=127), -2), (dict(residual=RES, ldr=127), -2), (dict(a=A + 8), -3), (dict(b=B2 + 2), -3), (dict(lda=260), -3),
+    (dict(ldb=257), -3), (dict(out=O + 2), -3), (dict(residual=RES + 1), -3), (dict(bias=W + 1), -3), (dict(row_scale=W + 2), -3),
+    (dict(out=A + 64), -1), (dict(out=B2), -1), (dict(bias=O + 4), -1), (dict(row_scale=O), -1), (dict(residual=O + 512), -1),
+    (dict(residual=O, res_dtype=1), -1), (dict(residual=O, ldr=136), -1), (dict(st=A + 8), -1), (dict(st=B2 + 4), -1), (dict(st=O), -1),
+    (dict(st=RES + 4, residual=RES), -1), (dict(st=W + 4, bias=W), -1), (dict(st=W + 8, row_scale=W), -1), (dict(flags=1, st=B2 + 65536 + 8), -1),
+])
+def test_mm16_refusals(m, over, code):
+    assert _mm(m, **over) == code, m.last_error()
+
+
+def test_mm16_struct_and_bindings(m):
+    assert ctypes.sizeof(m.MoeEpilogue) == 40
+    assert _mm(m, epi=False, k=0) == -2
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    with pytest.raises(m.MoeError):
+        m.mm16(x, x, torch.zeros(2, 2), torch.zeros(1, dtype=torch.int32))
+
+
+def test_reference_mm16_by_hand():
+    a, b = np.array([[1.0, 2.0]]), np.array([[3.0, 1.0], [1.0, -1.0]])
+    assert np.allclose(refblock.mm16(a, b)[0], [[5, -1]])
+    assert np.allclose(refblock.mm16(a, b, True, "relu", np.array([1.0, 2.0]), np.array([2.0]), np.array([[10.0]]))[0], [[22.0]])
