@@ -240,18 +240,15 @@ int moe_mm16(const uint16_t *a, int64_t lda, int t, const uint16_t *b, int64_t l
   p.out = out, p.ldo = ldo, p.out_bf16 = out_dtype == MOE_BF16;
   auto whole = [](const Mat &m) { return !m.p || (((uintptr_t)m.p | (uintptr_t)(m.ld * m.size)) & (4u * m.size - 1)) == 0; };
   p.wide = whole(mo) && whole(mr);
+  auto runs = [](const Mat &m) { return !m.p || (((uintptr_t)m.p | (uintptr_t)(m.ld * m.size)) & 31u) == 0; };
+  p.wide8 = runs(mo) && runs(mr);
   p.withhold = (flags & MOE_TEST_WITHHOLD) != 0;
   p.status = dev_status;
   p.timeout_ns = moe::timeout_ns();
   if (p.timeout_ns < 1000000) p.timeout_ns = 1000000;  // a wait gives up no sooner than the status is zeroed
-  cudaError_t e;
-  if (moe::mm16_few(t, n, k) && !p.withhold) {
-    e = moe::launch_mm16_few(p, st);
-  } else {
-    int n_sms = 0;
-    if (int r = sm_count(&n_sms)) return r;
-    e = moe::launch_mm16_tc(p, n_sms, st);
-  }
+  int n_sms = 0;
+  if (int r = sm_count(&n_sms)) return r;
+  const cudaError_t e = moe::mm16_few(p, n_sms) && !p.withhold ? moe::launch_mm16_few(p, n_sms, st) : moe::launch_mm16_tc(p, n_sms, st);
   return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, "launch failed: %s", cudaGetErrorString(e));
 }
 

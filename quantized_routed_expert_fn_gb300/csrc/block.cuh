@@ -71,20 +71,31 @@ struct Mm16Args {
   int res_bf16, out_bf16;
   void *out;
   int64_t ldo;
-  int wide;  // four neighbouring values of out (and residual) are one access
+  int wide;   // four neighbouring values of out (and residual) are one access
+  int wide8;  // their rows start on 32 bytes
   int withhold;
   int *status;
   unsigned long long timeout_ns;
-  // tensor cores: tokens of a tile, k blocks, weight and token tiles, CTAs
-  // that split k, ring
-  int w, nk, nmt, ntt, split, stage, stages;
+  // tensor cores: N side of a tile, k blocks, M and N tiles, CTAs that split
+  // k, ring, columns of tensor memory
+  int w, nk, nmt, ntt, split, stage, stages, tmem_cols;
 };
 struct Mm16P : Mm16Args {
   CUtensorMap tm_a, tm_b;
 };
-// Whether the few-row kernel takes t rows.
-inline bool mm16_few(int64_t t, int64_t, int64_t) { return t <= 8; }
-cudaError_t launch_mm16_few(const Mm16Args &p, cudaStream_t st);
+// Whether the few-row kernel takes the rows.  us a call, few-row /
+// tensor-core, in a graph of calls on weights that are not in L2 (fp32 out):
+//   n x k             1 row        8 rows       16 rows
+//   512 x 2048        5.4 / 7.5    5.2 / 7.7    6.2 / 8.0
+//   2048 x 512        2.6 / 6.9    2.8 / 7.1    3.0 / 7.4
+//   2048 x 2048       5.7 / 8.9    5.7 / 9.0    6.9 / 9.2
+//   2048 x 8192      11.4 / 15.1  11.4 / 15.3  13.6 / 15.5
+//   4096 x 2048       6.7 / 9.0    6.9 / 9.2   11.9 / 9.4
+//   8192 x 2048       9.1 / 11.2   9.3 / 11.2  16.2 / 11.3
+//   131072 x 2048    83.0 / 85.0  85.0 / 86.0   155 / 88.1
+// (of 16 rows one thread block an SM fits: good as long as each tile has an SM)
+bool mm16_few(const Mm16Args &p, int n_sms);
+cudaError_t launch_mm16_few(const Mm16Args &p, int n_sms, cudaStream_t st);
 cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -25,10 +25,19 @@ namespace {
 
 constexpr unsigned FULLM = 0xffffffffu;
 
-// 1 / (1 + exp(-x)), small values to their last bits
+// 1 / (1 + exp(-x)) of a number, small values to their last bits.  exp(-|x|)
+// is 2^t, t = -|x| log2(e) carried in two terms, so that its relative error
+// does not grow with |x|; the quotient's by an approximate reciprocal of 1 ..
+// 2: 2^-22 in all.  (With expf and a division the epilogue of 8192 x 8192 x
+// 2048 took 250 us instead of the product's 151.)
 __device__ __forceinline__ float logistic(float x) {
-  const float e = expf(-fabsf(x));
-  return (x < 0.f ? e : 1.f) / (1.f + e);
+  constexpr float kHi = 1.44269502f, kLo = 1.9259629e-8f;  // log2(e)
+  const float y = fmaxf(-fabsf(x), -150.f), t = y * kHi, r = fmaf(y, kLo, fmaf(y, kHi, -t));
+  float e, q;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  e = fmaf(e * r, 0.693147181f, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
+  return (x < 0.f ? e : 1.f) * q;
 }
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
@@ -37,8 +46,25 @@ __device__ __forceinline__ float activate(float z, int act) {
     case kActGeluTanh:  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
       return z * logistic(z * fmaf(z * z, 0.07135481627f, 1.5957691216f));
     case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays
-    case kActSigmoid: return logistic(z);
+    case kActSigmoid: return z == z ? logistic(z) : z;
     default: return z;
+  }
+}
+
+// the same of N values: one look at what is asked for
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+  auto all = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < N; i++) z[i] = f(z[i]);
+  };
+  switch (act) {
+    case kActSilu: return all([](float x) { return activate(x, kActSilu); });
+    case kActGelu: return all([](float x) { return activate(x, kActGelu); });
+    case kActGeluTanh: return all([](float x) { return activate(x, kActGeluTanh); });
+    case kActRelu: return all([](float x) { return activate(x, kActRelu); });
+    case kActSigmoid: return all([](float x) { return activate(x, kActSigmoid); });
+    default: return;
   }
 }
 
@@ -54,61 +80,63 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 // One output: row r, column j, from h = the activated product.
-__device__ __forceinline__ void finish1(const Mm16Args &P, int64_t r, int j, float h, float rs) {
-  h *= rs;
-  if (P.res) {
-    const int64_t i = r * P.ldr + j;
-    h += P.res_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(P.res)[i] << 16)
-                    : static_cast<const float *>(P.res)[i];
-  }
-  const int64_t o = r * P.ldo + j;
-  if (P.out_bf16) static_cast<uint16_t *>(P.out)[o] = bf16_of(h);
-  else static_cast<float *>(P.out)[o] = h;
+__device__ __forceinline__ uint32_t residual1(const Mm16Args &P, int64_t r, int j) {
+  const int64_t i = r * P.ldr + j;
+  return P.res_bf16 ? (uint32_t)static_cast<const uint16_t *>(P.res)[i] << 16 : static_cast<const uint32_t *>(P.res)[i];
 }
-// Four neighbouring ones, in rows that allow whole accesses (P.wide).
-__device__ __forceinline__ void finish4(const Mm16Args &P, int64_t r, int j, float4 h, float rs) {
-  h.x *= rs, h.y *= rs, h.z *= rs, h.w *= rs;
+__device__ __forceinline__ void store1(const Mm16Args &P, int64_t r, int j, float v) {
+  const int64_t o = r * P.ldo + j;
+  if (P.out_bf16) static_cast<uint16_t *>(P.out)[o] = bf16_of(v);
+  else static_cast<float *>(P.out)[o] = v;
+}
+__device__ __forceinline__ void finish1(const Mm16Args &P, int64_t r, int j, float h, float rs) {
+  const float v = h * rs;
+  store1(P, r, j, P.res ? v + __uint_as_float(residual1(P, r, j)) : v);
+}
+// Four neighbouring ones, in rows that allow whole accesses (P.wide); the
+// residual's come first, so that they are on their way meanwhile.
+__device__ __forceinline__ uint4 residual4(const Mm16Args &P, int64_t r, int j) {
+  const int64_t i = r * P.ldr + j;
+  if (!P.res_bf16) return *reinterpret_cast<const uint4 *>(static_cast<const float *>(P.res) + i);
+  const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.res) + i);
+  return make_uint4(u.x, u.y, 0u, 0u);
+}
+__device__ __forceinline__ void finish4(const Mm16Args &P, int64_t r, int j, const float *h, float rs, const uint4 &u) {
+  float4 v = make_float4(h[0] * rs, h[1] * rs, h[2] * rs, h[3] * rs);
   if (P.res) {
-    const int64_t i = r * P.ldr + j;
-    if (P.res_bf16) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.res) + i);
-      h.x += bf16lo(u.x), h.y += bf16hi(u.x), h.z += bf16lo(u.y), h.w += bf16hi(u.y);
-    } else {
-      const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(P.res) + i);
-      h.x += u.x, h.y += u.y, h.z += u.z, h.w += u.w;
-    }
+    if (P.res_bf16) v.x += bf16lo(u.x), v.y += bf16hi(u.x), v.z += bf16lo(u.y), v.w += bf16hi(u.y);
+    else
+      v.x += __uint_as_float(u.x), v.y += __uint_as_float(u.y), v.z += __uint_as_float(u.z), v.w += __uint_as_float(u.w);
   }
   const int64_t o = r * P.ldo + j;
   if (P.out_bf16)
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + o) = make_uint2(bf16x2(h.x, h.y), bf16x2(h.z, h.w));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + o) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
   else
-    *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + o) = h;
+    *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + o) = v;
 }
 
 // ------------------------------------------------------------ few rows
 
 constexpr int kFewWarps = 8;
-constexpr int kFewDepth = 4;  // blocks of 64 k whose weights a warp has in flight
 
-// One CTA: 16 weight rows (gated: 8 gate rows and the 8 up rows of the same
-// outputs), 8 * NT token rows.  Lane (g, q) = (lane / 4, lane % 4) loads 16
-// bytes of weight rows g and g + 8 at k = 8q and 32 + 8q of a block: the four
-// words of a piece serve as the k halves of two MMAs, and the same pieces of
-// the token rows as B, so the order of k is permuted alike on both sides.
-// Warp w takes the blocks w, w + 8, ...; the warps' sums meet in shared
-// memory in a fixed order.
-template <int NT>
+// A tile: 16 weight rows (gated: 8 gate rows and the 8 up rows of the same
+// outputs) by 8 * NT token rows.  Lane (g, q) = (lane / 4, lane % 4) loads 16
+// bytes of weight rows g and g + 8 at k = 8q and 32 + 8q of a block of 64: the
+// four words of a piece serve as the k halves of two MMAs, and the same
+// pieces of the token rows as B, so the order of k is permuted alike on both
+// sides.  Warp w takes the blocks w, w + 8, ...; the warps' sums meet in
+// shared memory in a fixed order.  A CTA walks the tiles i, i + grid, ...,
+// the next D blocks' weights always on their way, across the tiles' ends.
+template <int NT, int D>
 __global__ void __launch_bounds__(32 * kFewWarps) mm16_few_rows(const __grid_constant__ Mm16Args P) {
-  __shared__ float red[kFewWarps][16][8 * NT + 1];
+  __shared__ float red[2][kFewWarps][16][8 * NT + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   pdl_wait_prev();
   pdl_launch_next();
   if (blockIdx.x == 0 && tid == 0) *P.status = 0;
-  const int per = P.gated ? 8 : 16, n0 = blockIdx.x * per, nb = (P.k + 63) / 64;
+  const int per = P.gated ? 8 : 16, nb = (P.k + 63) / 64, tiles = (P.n + per - 1) / per;
+  const int mine = (nb - warp + kFewWarps - 1) / kFewWarps, rounds = (mine + D - 1) / D * D;  // blocks a tile
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int r0 = n0 + g, r1 = P.gated ? P.n + n0 + g : n0 + g + 8;
-  const bool ok0 = r0 < P.n, ok1 = P.gated ? ok0 : r1 < P.n;
-  const uint16_t *w0 = P.b + (int64_t)r0 * P.ldb, *w1 = P.b + (int64_t)r1 * P.ldb;
   // 8 values from k on; the last ones of a row may be fewer
   auto piece = [&](const uint16_t *row, int k, bool ok, bool stream) {
     if (!ok || k >= P.k) return zero;
@@ -121,99 +149,109 @@ __global__ void __launch_bounds__(32 * kFewWarps) mm16_few_rows(const __grid_con
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   };
-  float acc[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; j++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) acc[j][i] = 0.f;
-  uint4 a[kFewDepth][2][2];  // [block][piece][row]
-  auto load = [&](uint4 (&x)[2][2], int kb) {
-    const int k0 = kb * 64 + q * 8;
+  // the weights' place: block `at` (of the warp's) of tile `pt`
+  int pt = blockIdx.x, at = 0;
+  const uint16_t *w0, *w1;
+  bool ok0, ok1;
+  auto place = [&] {
+    const int r0 = pt * per + g, r1 = P.gated ? P.n + r0 : r0 + 8;
+    ok0 = pt < tiles && r0 < P.n, ok1 = P.gated ? ok0 : pt < tiles && r1 < P.n;
+    w0 = P.b + (int64_t)r0 * P.ldb, w1 = P.b + (int64_t)r1 * P.ldb;
+  };
+  place();
+  uint4 a[D][2][2], b[D][NT][2];  // [block][piece][row], [block][token rows][piece]
+  auto load = [&](uint4 (&x)[2][2], uint4 (&y)[NT][2]) {
+    const int k0 = (warp + at * kFewWarps) * 64 + q * 8;  // blocks beyond the warp's last are beyond k
 #pragma unroll
     for (int p = 0; p < 2; p++) x[p][0] = piece(w0, k0 + 32 * p, ok0, true), x[p][1] = piece(w1, k0 + 32 * p, ok1, true);
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int p = 0; p < 2; p++) y[j][p] = piece(P.a + (int64_t)(8 * j + g) * P.lda, k0 + 32 * p, 8 * j + g < P.t, false);
+    if (++at == rounds) at = 0, pt += gridDim.x, place();
   };
-  auto step = [&](const uint4 (&x)[2][2], int kb) {
-    const int k0 = kb * 64 + q * 8;
+  if (mine > 0)
+#pragma unroll
+    for (int i = 0; i < D; i++) load(a[i], b[i]);
+  int buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[j][i] = 0.f;
+    for (int i0 = 0; i0 < rounds; i0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; d++) {
+        if (i0 + d < mine) {
+#pragma unroll
+          for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int p = 0; p < 2; p++) {
+              mma_bf16_16816(acc[j], a[d][p][0].x, a[d][p][1].x, a[d][p][0].y, a[d][p][1].y, b[d][j][p].x, b[d][j][p].y);
+              mma_bf16_16816(acc[j], a[d][p][0].z, a[d][p][1].z, a[d][p][0].w, a[d][p][1].w, b[d][j][p].z, b[d][j][p].w);
+            }
+        }
+        load(a[d], b[d]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-      const int r = 8 * j + g;
-      const uint16_t *xr = P.a + (int64_t)r * P.lda;
-#pragma unroll
-      for (int p = 0; p < 2; p++) {
-        const uint4 b = piece(xr, k0 + 32 * p, r < P.t, false);
-        mma_bf16_16816(acc[j], x[p][0].x, x[p][1].x, x[p][0].y, x[p][1].y, b.x, b.y);
-        mma_bf16_16816(acc[j], x[p][0].z, x[p][1].z, x[p][0].w, x[p][1].w, b.z, b.w);
-      }
+      const int c = 8 * j + 2 * q;
+      red[buf][warp][g][c] = acc[j][0], red[buf][warp][g][c + 1] = acc[j][1];
+      red[buf][warp][g + 8][c] = acc[j][2], red[buf][warp][g + 8][c + 1] = acc[j][3];
     }
-  };
+    __syncthreads();  // the other buffer is read: every thread is past the tile before
+    auto sum = [&](int row, int c) {
+      float v = 0.f;
 #pragma unroll
-  for (int i = 0; i < kFewDepth; i++) load(a[i], warp + i * kFewWarps);
-  for (int kb = warp; kb < nb; kb += kFewDepth * kFewWarps) {
-#pragma unroll
-    for (int i = 0; i < kFewDepth; i++) {
-      const int k1 = kb + i * kFewWarps;
-      if (k1 < nb) {
-        step(a[i], k1);
-        load(a[i], k1 + kFewDepth * kFewWarps);
+      for (int w = 0; w < kFewWarps; w++) v += red[buf][w][row][c];
+      return v;
+    };
+    const int n0 = tile * per;
+    for (int i = tid; i < per * 8 * NT; i += 32 * kFewWarps) {
+      const int j = i & (per - 1), c = i / per;
+      if (c < P.t && n0 + j < P.n) {
+        float z = sum(j, c);
+        if (P.bias) z += P.bias[n0 + j];
+        z = activate(z, P.act);
+        if (P.gated) {
+          float u = sum(j + 8, c);
+          if (P.bias) u += P.bias[P.n + n0 + j];
+          z *= u;
+        }
+        finish1(P, c, n0 + j, z, P.row_scale ? P.row_scale[c] : 1.f);
       }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < NT; j++) {
-    const int c = 8 * j + 2 * q;
-    red[warp][g][c] = acc[j][0], red[warp][g][c + 1] = acc[j][1];
-    red[warp][g + 8][c] = acc[j][2], red[warp][g + 8][c + 1] = acc[j][3];
-  }
-  __syncthreads();
-  auto sum = [&](int row, int c) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; w++) v += red[w][row][c];
-    return v;
-  };
-  for (int i = tid; i < per * 8 * NT; i += 32 * kFewWarps) {
-    const int j = i & (per - 1), c = i / per;
-    if (c < P.t && n0 + j < P.n) {
-      float z = sum(j, c);
-      if (P.bias) z += P.bias[n0 + j];
-      z = activate(z, P.act);
-      if (P.gated) {
-        float u = sum(j + 8, c);
-        if (P.bias) u += P.bias[P.n + n0 + j];
-        z *= u;
-      }
-      finish1(P, c, n0 + j, z, P.row_scale ? P.row_scale[c] : 1.f);
     }
   }
 }
 
 // ------------------------------------------------------------ tensor cores
 //
-//   warps 0-7 epilogue, four for the even and four for the odd pieces of 32
-//             tokens: TMEM -> registers -> shared memory [token][128 rows] ->
-//             whole runs of a token's outputs, from one of two accumulators
-//             while the MMAs fill the other
-//   warp 8    (even CTA) issues a stage's MMAs once its operands are there
-//   warp 9    TMA: 128 weight rows x 64 k a stage, the CTA's share of the tokens
+//   warps 0-15 epilogue, in four groups
+//   warp 16   (even CTA) issues a stage's MMAs once its operands are there
+//   warp 17   TMA
 // gated: a tile's 128 weight rows are 64 gate rows and the 64 up rows of the
 // same outputs, so that both meet in the piece in shared memory.
 // The full and acc_empty barriers of a pair are the even CTA's; the others are
 // each CTA's own, committed to both.
-constexpr int kTcThreads = 320;
+constexpr int kEpi = 16;  // epilogue warps, in groups of four (one for each 32 lanes of TMEM)
+constexpr int kTcThreads = 32 * (kEpi + 2);
 constexpr int kMaxStages = 10;
-constexpr int kPiece = 32 * 128 * 4;  // bytes of 32 tokens x 128 rows
+constexpr int kPiece = 16 * 128 * 4;  // bytes of 16 tokens x 128 rows
 
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
 };
-constexpr int kOffBars = 2 * kPiece;
+constexpr int kOffBars = kEpi / 4 * kPiece;
 constexpr int kOffRing = (kOffBars + (int)sizeof(Bars) + 1023) / 1024 * 1024;
 constexpr int kRoom = 226 * 1024 - kOffRing;
 
 template <bool CL>
 __device__ bool tc_wait(uint64_t *bar, uint32_t par, const Mm16Args &P) {
-  auto done = [&] { return CL ? tc05::mbar_try_wait_cluster(bar, par) : mbar_try_wait(bar, par); };
+  // asleep on the barrier meanwhile: polling takes issue slots and power
+  auto done = [&] { return CL ? tc05::mbar_sleep_wait_cluster(bar, par) : tc05::mbar_sleep_wait(bar, par); };
   if (done()) return true;
   const uint64_t t0 = globaltimer();
   while (!done()) {
@@ -231,38 +269,163 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t par, const 
   return __shfl_sync(FULLM, ok ? 1 : 0, 0) != 0;
 }
 
-// Warp: the outputs of one token of a tile (row r of out) from its 128 values
-// z, which get(i) reads for i % 4 == 0 four at a time, get1(i) one.  Gated:
-// 64 outputs, from values i and 64 + i.
-template <class G4, class G1>
-__device__ __forceinline__ void token_out(const Mm16Args &P, int64_t r, int nbase, G4 get4, G1 get1) {
-  const int lane = threadIdx.x & 31;
-  const float rs = P.row_scale ? P.row_scale[r] : 1.f;
-  if (!P.gated) {
-    if (P.wide && nbase + 128 <= P.n) {
-      float4 z = get4(4 * lane);
-      z.x = activate(z.x, P.act), z.y = activate(z.y, P.act), z.z = activate(z.z, P.act), z.w = activate(z.w, P.act);
-      finish4(P, r, nbase + 4 * lane, z, rs);
-    } else {
+// 16 neighbouring values of SIZE bytes, 32 bytes an access
+template <int SIZE>
+__device__ __forceinline__ void load_run(const void *p, uint32_t *v) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int j = lane + 32 * i;
-        if (nbase + j < P.n) finish1(P, r, nbase + j, activate(get1(j), P.act), rs);
-      }
+  for (int i = 0; i < SIZE / 2; i++)
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[8 * i]), "=r"(v[8 * i + 1]), "=r"(v[8 * i + 2]), "=r"(v[8 * i + 3]), "=r"(v[8 * i + 4]),
+                   "=r"(v[8 * i + 5]), "=r"(v[8 * i + 6]), "=r"(v[8 * i + 7])
+                 : "l"(static_cast<const uint8_t *>(p) + 32 * i));
+}
+template <int SIZE>
+__device__ __forceinline__ void store_run(void *p, const uint32_t *v) {
+#pragma unroll
+  for (int i = 0; i < SIZE / 2; i++)
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[8 * i]), "r"(v[8 * i + 1]),
+                 "r"(v[8 * i + 2]), "r"(v[8 * i + 3]), "r"(v[8 * i + 4]), "r"(v[8 * i + 5]), "r"(v[8 * i + 6]),
+                 "r"(v[8 * i + 7]), "l"(static_cast<uint8_t *>(p) + 32 * i)
+                 : "memory");
+}
+// the same n values for every lane
+__device__ __forceinline__ void add_bias(float (&v)[16], const float *bias, int n) {
+  if (n == 16 && ((uintptr_t)bias & 15u) == 0) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 b = *reinterpret_cast<const float4 *>(bias + j);
+      v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int j = lane + 32 * i;
-      if (nbase + j < P.n) finish1(P, r, nbase + j, activate(get1(j), P.act) * get1(64 + j), rs);
-    }
+    for (int j = 0; j < 16; j++)
+      if (j < n) v[j] += bias[j];
   }
 }
 
-template <int CG, bool SPLIT>
+// Warp: outputs of the tokens of a piece, which lie as z [token][128] in
+// shared memory (plain: 128 outputs a token; gated: 64, from the values i and
+// 64 + i).  In whole rows (four values a lane, a token's row by one warp, or
+// half a warp where it is gated) fetch() asks for the residuals and row
+// scales of NP such rows, before the piece is there; else of values one by
+// one, neighbouring lanes on neighbouring columns.
+template <int NP>
+struct Outputs {
+  uint4 res[NP];
+  float rs[NP];
+  // row i of this lane: its token among the piece's `j0 + i * step`
+  __device__ __forceinline__ static int token(const Mm16Args &P, int i, int j0, int step) {
+    return P.gated ? j0 + step * (2 * i + ((threadIdx.x & 31) >> 4)) : j0 + step * i;
+  }
+  // whole: rows of whole accesses
+  __device__ __forceinline__ void fetch(const Mm16Args &P, int64_t r0, int n, int nbase, int j0, int step, bool whole) {
+    const int lane = threadIdx.x & 31;
+    if (whole) {
+      const int col = nbase + 4 * (P.gated ? lane & 15 : lane), rows = P.gated ? NP / 2 : NP;
+#pragma unroll
+      for (int i = 0; i < NP; i++) {
+        const int j = token(P, i, j0, step);
+        if (i < rows && j < n) {
+          if (P.res) res[i] = residual4(P, r0 + j, col);
+          rs[i] = P.row_scale ? P.row_scale[r0 + j] : 1.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; i++) {
+        const int j = j0 + step * i;
+        if (j < n) {
+          if (P.res) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const int c = nbase + lane + 32 * e;
+              x[e] = c < P.n && (e < 2 || !P.gated) ? residual1(P, r0 + j, c) : 0u;
+            }
+            res[i] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+          rs[i] = P.row_scale ? P.row_scale[r0 + j] : 1.f;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void write(const Mm16Args &P, int64_t r0, int n, int nbase, const float *z, int j0, int step,
+                                        bool whole) const {
+    if (whole) write4(P, r0, n, nbase, z, j0, step);
+    else write1(P, r0, n, nbase, z, j0, step);
+  }
+  __device__ __forceinline__ void write4(const Mm16Args &P, int64_t r0, int n, int nbase, const float *z, int j0, int step) const {
+    const int lane = threadIdx.x & 31;
+    if (!P.gated) {
+#pragma unroll
+      for (int i0 = 0; i0 < NP; i0 += 4) {
+        float h[16];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int j = j0 + step * (i0 + i);
+          const float4 v = j < n ? *reinterpret_cast<const float4 *>(z + j * 128 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+          h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
+        }
+        activate_all(h, P.act);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int j = j0 + step * (i0 + i);
+          if (j < n) finish4(P, r0 + j, nbase + 4 * lane, h + 4 * i, rs[i0 + i], res[i0 + i]);
+        }
+      }
+    } else {
+      const int l = lane & 15;
+#pragma unroll
+      for (int i0 = 0; i0 < NP / 2; i0 += 2) {
+        float h[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const int j = token(P, i0 + i, j0, step);
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 v = j < n ? *reinterpret_cast<const float4 *>(z + j * 128 + 4 * l) : zero;
+          const float4 x = j < n ? *reinterpret_cast<const float4 *>(z + j * 128 + 64 + 4 * l) : zero;
+          h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
+          u[4 * i] = x.x, u[4 * i + 1] = x.y, u[4 * i + 2] = x.z, u[4 * i + 3] = x.w;
+        }
+        activate_all(h, P.act);
+#pragma unroll
+        for (int i = 0; i < 8; i++) h[i] *= u[i];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const int j = token(P, i0 + i, j0, step);
+          if (j < n) finish4(P, r0 + j, nbase + 4 * l, h + 4 * i, rs[i0 + i], res[i0 + i]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void write1(const Mm16Args &P, int64_t r0, int n, int nbase, const float *z, int j0, int step) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < NP; i++) {
+      const int j = j0 + step * i;
+      if (j < n) {
+        const float *x = z + j * 128 + lane;
+        float h[4] = {x[0], x[32], P.gated ? 0.f : x[64], P.gated ? 0.f : x[96]};
+        activate_all(h, P.act);
+        if (P.gated) h[0] *= x[64], h[1] *= x[96];
+        const uint32_t u[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int c = nbase + lane + 32 * e;
+          const float v = h[e] * rs[i];
+          if (c < P.n && (e < 2 || !P.gated)) store1(P, r0 + j, c, P.res ? v + __uint_as_float(u[e]) : v);
+        }
+      }
+    }
+  }
+};
+
+enum { kWeights = 0, kSplit = 1, kTokens = 2 };  // what is on the M side; kSplit: weights, k split over a cluster
+
+template <int CG, int FORM>
 __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__ Mm16P P) {
+  constexpr bool CL = CG == 2, SPLIT = FORM == kSplit, TOK = FORM == kTokens;
   static_assert(!SPLIT || CG == 1, "a split tile is one CTA's rows");
-  constexpr bool CL = CG == 2;
   pdl_launch_next();
   extern __shared__ __align__(1024) uint8_t smraw[];
   // the same offset in all CTAs of a cluster: dynamic shared memory starts alike
@@ -275,12 +438,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
 
   if (tid == 0) {
     for (int s = 0; s < S; s++) mbar_init(&B.full[s], 1), mbar_init(&B.empty[s], 1);
-    for (int b = 0; b < 2; b++) mbar_init(&B.acc_full[b], 1), mbar_init(&B.acc_empty[b], 8 * CG);
+    for (int b = 0; b < 2; b++) mbar_init(&B.acc_full[b], 1), mbar_init(&B.acc_empty[b], kEpi * CG);
     mbar_init(&B.drain, 1);
     fence_mbar_init();
   }
-  if (warp == 8) {
-    if constexpr (CG == 1) tc05::alloc(&B.tmem, 512);
+  if (warp == kEpi) {
+    if constexpr (CG == 1) tc05::alloc(&B.tmem, P.tmem_cols);
     else tc05::alloc_pair(&B.tmem, 512);
   }
   pdl_wait_prev();  // the operands may be the previous kernel's
@@ -293,31 +456,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
   const uint32_t tmem = B.tmem;
 
   const int w = P.w, mrank = CG == 2 ? rank : 0;
-  const int rows = P.gated ? 64 : 128;         // outputs of a CTA's tile
-  const int nmp = (P.nmt + CG - 1) / CG;       // weight tiles, CG at a time
+  const int rows = P.gated ? 64 : 128;         // weights on the M side: outputs of a CTA's tile
+  const int cols = P.gated ? w / 2 : w;        // tokens on it: outputs of a tile
+  const int nmp = (P.nmt + CG - 1) / CG;       // M tiles, CG at a time
   const int ntiles = P.ntt * nmp;
   const int width = CG == 2 ? 2 : (SPLIT ? P.split : 1);  // CTAs of a tile
   const int cl = (int)blockIdx.x / width, ncl = (int)gridDim.x / width;
   const int my_tiles = cl < ntiles ? (ntiles - 1 - cl) / ncl + 1 : 0;
   int kb0 = 0, kb1 = P.nk;
   if constexpr (SPLIT) kb0 = (int)((int64_t)P.nk * rank / P.split), kb1 = (int)((int64_t)P.nk * (rank + 1) / P.split);
-  // tile i: the weight tiles of a token tile follow one another
+  // tile i: the M tiles of an N tile follow one another
   int tt = cl / nmp, mp = cl - tt * nmp;
   const int step_t = ncl / nmp, step_m = ncl - step_t * nmp;
   struct Tile {
-    int mt, n0, nlen;
+    int mt, n0, nlen;  // M tile; N side: first token and their number, or first output column
   };
   auto next_tile = [&] {
     Tile T;
     T.mt = mp * CG + mrank;
-    T.n0 = tt * w;
+    T.n0 = tt * (TOK ? cols : w);
     T.nlen = min(w, P.t - T.n0);
     tt += step_t, mp += step_m;
     if (mp >= nmp) mp -= nmp, tt++;
     return T;
   };
 
-  if (warp == 8) {
+  if (warp == kEpi) {
     // ---------------------------------------------------------------- MMA issue
     if (mrank == 0 && tc05::elect_one()) {
       int s = 0;
@@ -354,7 +518,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
       tc_wait<CL>(&B.drain, 0, P);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kEpi + 1) {
     // ---------------------------------------------------------------- TMA
     int f = 0, s = 0;
     uint32_t ph = 0;
@@ -375,9 +539,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
           uint8_t *st = ring + s * P.stage;
           if (mrank == 0) mbar_expect_tx(&B.full[s], bytes);
           const uint32_t bar = CG == 1 ? smem_u32(&B.full[s]) : tc05::map_rank(&B.full[s], 0);
-          tc05::tma_load_xy<CG>(st, &P.tm_b, kb * 64, wr, bar);
-          if (P.gated) tc05::tma_load_xy<CG>(st + 8192, &P.tm_b, kb * 64, P.n + wr, bar);
-          tc05::tma_load_xy<CG>(st + 16384, &P.tm_a, kb * 64, T.n0 + mrank * tok, bar);
+          if constexpr (!TOK) {
+            tc05::tma_load_xy<CG>(st, &P.tm_b, kb * 64, wr, bar);
+            if (P.gated) tc05::tma_load_xy<CG>(st + 8192, &P.tm_b, kb * 64, P.n + wr, bar);
+            tc05::tma_load_xy<CG>(st + 16384, &P.tm_a, kb * 64, T.n0 + mrank * tok, bar);
+          } else {
+            tc05::tma_load_xy<CG>(st, &P.tm_a, kb * 64, T.mt * 128, bar);
+            // columns: gated, the gates and then the up rows, of a pair one each
+            const int first = P.gated ? T.n0 + mrank * P.n : T.n0 + mrank * tok;
+            tc05::tma_load_xy<CG>(st + 16384, &P.tm_b, kb * 64, first, bar);
+            if (CG == 1 && P.gated) tc05::tma_load_xy<CG>(st + 16384 + tok * 64, &P.tm_b, kb * 64, P.n + first, bar);
+          }
         }
         __syncwarp();
         if (++s == S) s = 0, ph ^= 1;
@@ -389,65 +561,127 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3, grp = warp >> 2;  // TMEM lane quadrant; even or odd pieces
+    const int q = warp & 3, grp = warp >> 2;  // TMEM lane quadrant; group: pieces grp, grp + 4, ...
     const int row = 32 * q + lane;            // the tile's weight row of this thread
     float *stg = reinterpret_cast<float *>(sm + grp * kPiece);
     bool fine = true;
     for (int lt = 0; lt < my_tiles; lt++) {
       const Tile T = next_tile();
-      const int b = lt & 1;
+      const int b = lt & 1, nbase = T.mt * rows;
+      const bool rows4 = P.wide && nbase + rows <= P.n;
+      Outputs<FORM == kWeights ? 4 : 2> O;  // the first piece's residuals, and later the next one's
+      if (FORM == kWeights && T.mt < P.nmt && 16 * grp < T.nlen) O.fetch(P, T.n0 + 16 * grp, min(16, T.nlen - 16 * grp), nbase, q, 4, rows4);
+      // tokens on the M side: the residuals of this lane's runs of 16 columns
+      // (four of them in bf16, the first two in fp32) on their way meanwhile
+      uint32_t res[32];
+      const int r = T.mt * 128 + row;
+      const bool live = r < P.t;
+      if (TOK && P.res && P.wide8 && live) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int c0 = 16 * (grp + 4 * i), col = T.n0 + c0;
+          if (c0 < cols && col + 16 <= P.n) {
+            if (P.res_bf16) load_run<2>(static_cast<const uint16_t *>(P.res) + (int64_t)r * P.ldr + col, res + 8 * i);
+            else if (i < 2) load_run<4>(static_cast<const float *>(P.res) + (int64_t)r * P.ldr + col, res + 16 * i);
+          }
+        }
+      }
       // the warps stop together (they share named barriers)
-      fine = tc05::named_and(3, 256, tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)((lt >> 1) & 1), P));
+      // (one waits for the MMAs, the others for it)
+      fine = tc05::named_and(5, 32 * kEpi, warp != 0 || tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)((lt >> 1) & 1), P));
       if (!fine) break;
       tc05::fence_after();
       const uint32_t tl = tmem + (uint32_t)(b * 256) + ((uint32_t)(32 * q) << 16);
-      const int nbase = T.mt * rows, o = nbase + (P.gated ? row & 63 : row);
+      const int o = nbase + (P.gated ? row & 63 : row);
       const int brow = P.gated && row >= 64 ? P.n + o : o;
-      if constexpr (SPLIT) {
+      auto release = [&] {  // the accumulator is read: the MMAs may fill it again
+        tc05::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) tc05::mbar_arrive(&B.acc_empty[b]);
+          else tc05::mbar_arrive_cluster(tc05::map_rank(&B.acc_empty[b], 0));
+        }
+      };
+      if constexpr (TOK) {
+        // a lane has a token, and its columns one after another: no exchange
+        // (through shared memory, which copies and MMAs keep busy, the
+        // product with silu took 208 us at 8192 x 8192 x 2048)
+        const float rs = live && P.row_scale ? P.row_scale[r] : 1.f;
+        const int last = (min(cols, P.n - T.n0) + 15) / 16;
+        if (grp >= last) release();
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int c0 = 16 * (grp + 4 * i), col = T.n0 + c0, n = min(16, P.n - col);
+          if (c0 >= cols || n <= 0) break;
+          const bool run = P.wide8 && n == 16;
+          float v[16], u[16];
+          tc05::ld16(tl + c0, v);
+          if (P.gated) tc05::ld16(tl + cols + c0, u);
+          if (grp + 4 * (i + 1) >= last) release();
+          if (live) {
+            if (P.bias) add_bias(v, P.bias + col, n);
+            activate_all(v, P.act);
+            if (P.gated) {
+              if (P.bias) add_bias(u, P.bias + P.n + col, n);
+#pragma unroll
+              for (int j = 0; j < 16; j++) v[j] *= u[j];
+            }
+            if (run) {
+#pragma unroll
+              for (int j = 0; j < 16; j++) v[j] *= rs;
+              if (P.res) {
+                if (P.res_bf16) {
+#pragma unroll
+                  for (int j = 0; j < 16; j++) v[j] += (j & 1) ? bf16hi(res[8 * i + j / 2]) : bf16lo(res[8 * i + j / 2]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 16; j++) v[j] += __uint_as_float(res[16 * (i & 1) + j]);
+                  if (i < 2 && c0 + 128 < cols && col + 144 <= P.n)
+                    load_run<4>(static_cast<const float *>(P.res) + (int64_t)r * P.ldr + col + 128, res + 16 * i);
+                }
+              }
+              uint32_t o[16];
+              if (P.out_bf16) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) o[j] = bf16x2(v[2 * j], v[2 * j + 1]);
+                store_run<2>(static_cast<uint16_t *>(P.out) + (int64_t)r * P.ldo + col, o);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; j++) o[j] = __float_as_uint(v[j]);
+                store_run<4>(static_cast<float *>(P.out) + (int64_t)r * P.ldo + col, o);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j++)
+                if (j < n) finish1(P, r, col + j, v[j], rs);
+            }
+          }
+          __syncwarp();
+        }
+      } else if constexpr (SPLIT) {
         // all of the accumulator to this CTA's shared memory, [token][128]
         // (the ring: every copy has landed and every MMA has read its operands)
         float *z = reinterpret_cast<float *>(ring);
-        for (int c0 = 32 * grp; c0 < w; c0 += 64) {
-          float v[32];
-          const bool whole = c0 + 32 <= w;
-          if (whole) tc05::ld32(tl + c0, v);
-          else tc05::ld16(tl + c0, v);
+        for (int c0 = 16 * grp; c0 < w; c0 += 4 * kEpi) {
+          float v[16];
+          tc05::ld16(tl + c0, v);
 #pragma unroll
-          for (int j = 0; j < 32; j++)
-            if (whole || j < 16) z[(c0 + j) * 128 + row] = v[j];
+          for (int j = 0; j < 16; j++) z[(c0 + j) * 128 + row] = v[j];
         }
       } else {
-        auto release = [&] {  // the accumulator is read: the MMAs may fill it again
-          tc05::fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 1) tc05::mbar_arrive(&B.acc_empty[b]);
-            else tc05::mbar_arrive_cluster(tc05::map_rank(&B.acc_empty[b], 0));
-          }
-        };
-        const int last = (T.mt < P.nmt ? (T.nlen + 31) / 32 : 0);  // pieces with a token
+        const int last = (T.mt < P.nmt ? (T.nlen + 15) / 16 : 0);  // pieces with a token
         const float bias = P.bias && o < P.n ? P.bias[brow] : 0.f;
         if (grp >= last) release();
-        for (int c = grp; c < last; c += 2) {
-          float v[32];
-          const int c0 = 32 * c;
-          const bool whole = c0 + 32 <= w;
-          if (whole) tc05::ld32(tl + c0, v);
-          else tc05::ld16(tl + c0, v);
-          if (c + 2 >= last) release();
+        for (int c = grp; c < last; c += kEpi / 4) {
+          const int c0 = 16 * c, n = min(16, T.nlen - c0), c1 = c0 + 4 * kEpi;
+          float v[16];
+          tc05::ld16(tl + c0, v);
+          if (c + kEpi / 4 >= last) release();
 #pragma unroll
-          for (int j = 0; j < 32; j++)
-            if (whole || j < 16) stg[j * 128 + row] = v[j] + bias;
+          for (int j = 0; j < 16; j++) stg[j * 128 + row] = v[j] + bias;
           tc05::named_sync(1 + grp, 128);
-#pragma unroll 1
-          for (int i = 0; i < 8; i++) {
-            const int j = 4 * i + q;
-            if (c0 + j < T.nlen) {
-              const float *z = stg + j * 128;
-              token_out(P, T.n0 + c0 + j, nbase, [&](int x) { return *reinterpret_cast<const float4 *>(z + x); },
-                        [&](int x) { return z[x]; });
-            }
-          }
+          O.write(P, T.n0 + c0, n, nbase, stg, q, 4, rows4);
+          if (c1 < T.nlen) O.fetch(P, T.n0 + c1, min(16, T.nlen - c1), nbase, q, 4, rows4);
           tc05::named_sync(1 + grp, 128);  // the piece is free again
         }
       }
@@ -459,40 +693,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
       tc05::cluster_sync();
       if (fine && my_tiles > 0) {
         const int t0 = cl / nmp, m0 = cl - t0 * nmp, nbase = m0 * rows, n0 = t0 * w, nlen = min(w, P.t - n0);
-        for (int j = rank + P.split * warp; j < nlen; j += P.split * 8) {
-          auto bias_at = [&](int x) {
-            const int c = nbase + (P.gated ? x & 63 : x);
-            return P.bias && c < P.n ? P.bias[P.gated && x >= 64 ? P.n + c : c] : 0.f;
-          };
-          auto get4 = [&](int x) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < P.split; r++) {
-              const float4 u = tc05::ld_cluster4(tc05::map_rank(ring + (size_t)(j * 128 + x) * 4, r));
-              v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-            }
-            v.x += bias_at(x), v.y += bias_at(x + 1), v.z += bias_at(x + 2), v.w += bias_at(x + 3);
-            return v;
-          };
-          auto get1 = [&](int x) {
-            float v = 0.f;
-            for (int r = 0; r < P.split; r++) v += tc05::ld_cluster(tc05::map_rank(ring + (size_t)(j * 128 + x) * 4, r));
-            return v + bias_at(x);
-          };
-          token_out(P, n0 + j, nbase, get4, get1);
+        const bool rows4 = P.wide && nbase + rows <= P.n;
+        float bias[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int x = 4 * lane + e, c = nbase + (P.gated ? x & 63 : x);
+          bias[e] = P.bias && c < P.n ? P.bias[P.gated && x >= 64 ? P.n + c : c] : 0.f;
+        }
+        // four tokens at a time: the CTAs' sums of them, added in the order
+        // of k, then as a piece of four of the warp's own
+        float *mine = reinterpret_cast<float *>(sm) + warp * 4 * 128;
+        for (int j = rank * 4 + P.split * 4 * warp; j < nlen; j += P.split * 4 * kEpi) {
+          const int n = min(4, nlen - j);
+          Outputs<4> O;
+          O.fetch(P, n0 + j, n, nbase, 0, 1, rows4);
+          float4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[i] = make_float4(bias[0], bias[1], bias[2], bias[3]);
+#pragma unroll 2
+          for (int r = 0; r < P.split; r++) {
+            const uint32_t at = tc05::map_rank(ring + (size_t)(j * 128 + 4 * lane) * 4, r);
+            float4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) u[i] = tc05::ld_cluster4(at + (i < n ? i * 512 : 0));
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i].x += u[i].x, v[i].y += u[i].y, v[i].z += u[i].z, v[i].w += u[i].w;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; i++) *reinterpret_cast<float4 *>(mine + i * 128 + 4 * lane) = v[i];
+          __syncwarp();
+          O.write(P, n0 + j, n, nbase, mine, 0, 1, rows4);
+          __syncwarp();
         }
       }
       __syncwarp();
     }
   }
   if constexpr (SPLIT) {
-    if (warp >= 8) tc05::cluster_sync();  // the first of the two that the epilogue warps wait at
+    if (warp >= kEpi) tc05::cluster_sync();  // the first of the two that the epilogue warps wait at
   }
 
   tc05::fence_before();
   if constexpr (CG == 1 && !SPLIT) __syncthreads();
   else tc05::cluster_sync();
-  if (warp == 8) {
-    if constexpr (CG == 1) tc05::dealloc(tmem, 512);
+  if (warp == kEpi) {
+    if constexpr (CG == 1) tc05::dealloc(tmem, P.tmem_cols);
     else tc05::dealloc_pair(tmem, 512);
   }
 }
@@ -522,19 +767,28 @@ bool make_map16(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uin
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, bool SPLIT>
+template <int CG, int FORM>
 cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
-  const int tok = p.w / CG;
-  p.stage = 16384 + tok * 128;
+  constexpr bool SPLIT = FORM == kSplit;
+  const int nrows = p.w / CG;  // rows of the N side that a CTA loads
+  p.stage = 16384 + nrows * 128;
   p.stages = kRoom / p.stage < kMaxStages ? kRoom / p.stage : kMaxStages;
+  p.tmem_cols = 512;
+  if (SPLIT) {
+    // no more than the one tile needs, so that the next launch's blocks may
+    // begin beside it: its k blocks (or the sums, [w][128]), its accumulator
+    const int need = (p.nk + p.split - 1) / p.split, sums = (p.w * 512 + p.stage - 1) / p.stage;
+    p.stages = min(p.stages, need > sums ? need : sums);
+    p.tmem_cols = p.w <= 32 ? 32 : (p.w <= 64 ? 64 : 128);
+  }
   // the most any launch asks for: another host thread's launch of the same
   // kernel may stand between this and the launch below.  Before the tensor
   // maps: it makes the device's context this thread's, which they need
-  cudaError_t e = cudaFuncSetAttribute(mm16_tc<CG, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOffRing + kRoom + 1024);
+  cudaError_t e = cudaFuncSetAttribute(mm16_tc<CG, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOffRing + kRoom + 1024);
   if (e != cudaSuccess) return e;
-  if (encode_fn() == nullptr ||
-      !make_map16(&p.tm_b, p.b, p.k, (uint64_t)p.n * (p.gated ? 2 : 1), p.ldb, p.gated ? 64 : 128) ||
-      !make_map16(&p.tm_a, p.a, p.k, p.t, p.lda, (uint32_t)tok))
+  const int box_a = FORM == kTokens ? 128 : nrows, box_b = FORM == kTokens ? (p.gated ? p.w / 2 : nrows) : (p.gated ? 64 : 128);
+  if (encode_fn() == nullptr || !make_map16(&p.tm_b, p.b, p.k, (uint64_t)p.n * (p.gated ? 2 : 1), p.ldb, (uint32_t)box_b) ||
+      !make_map16(&p.tm_a, p.a, p.k, p.t, p.lda, (uint32_t)box_a))
     return cudaErrorNotSupported;
   const int smem = kOffRing + p.stages * p.stage + 1024;
   const int64_t tiles = (int64_t)p.ntt * ((p.nmt + CG - 1) / CG);
@@ -558,41 +812,72 @@ cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = (unsigned)n;
-  return cudaLaunchKernelEx(&cfg, mm16_tc<CG, SPLIT>, p);
+  return cudaLaunchKernelEx(&cfg, mm16_tc<CG, FORM>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_mm16_few(const Mm16Args &p, cudaStream_t st) {
-  const int per = p.gated ? 8 : 16, nt = (p.t + 7) / 8;
-  auto f = nt <= 1 ? mm16_few_rows<1> : (nt <= 2 ? mm16_few_rows<2> : mm16_few_rows<4>);
-  return launch_pdl(f, dim3((unsigned)((p.n + per - 1) / per)), 32 * kFewWarps, 0, st, p);
+template <int NT>
+cudaError_t launch_few(const Mm16Args &p, int n_sms, cudaStream_t st) {
+  const int per = p.gated ? 8 : 16, tiles = (p.n + per - 1) / per, blocks = ((p.k + 63) / 64 + kFewWarps - 1) / kFewWarps;
+  // as many of a warp's blocks in flight as it has in a tile, four at the
+  // most; two (three) thread blocks an SM fit
+  const int most = n_sms * (blocks > 2 ? 2 : 3);
+  const dim3 grid((unsigned)(tiles < most ? tiles : most));
+  auto f = blocks > 2 ? mm16_few_rows<NT, 4> : (blocks > 1 ? mm16_few_rows<NT, 2> : mm16_few_rows<NT, 1>);
+  return launch_pdl(f, grid, 32 * kFewWarps, 0, st, p);
+}
+
+bool mm16_few(const Mm16Args &p, int n_sms) {
+  const int per = p.gated ? 8 : 16;
+  return p.t <= 8 || (p.t <= 16 && (p.n + per - 1) / per <= n_sms);
+}
+
+cudaError_t launch_mm16_few(const Mm16Args &p, int n_sms, cudaStream_t st) {
+  return p.t <= 8 ? launch_few<1>(p, n_sms, st) : launch_few<2>(p, n_sms, st);
 }
 
 cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st) {
   const int rows = p.gated ? 64 : 128;
   p.nmt = (p.n + rows - 1) / rows, p.nk = (p.k + 63) / 64;
-  // too few tiles for the SMs: k is split over a cluster
+  // Too few tiles for the SMs: k is split over a cluster.  Clusters of 4 and 8
+  // CTAs of this size do not fill every SM (36 and 15 fit at once).
   {
     const int w = p.t <= 128 ? (p.t + 15) / 16 * 16 : 128;
     const int64_t tiles = (int64_t)((p.t + w - 1) / w) * p.nmt;
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= n_sms && p.nk / (s * 2) >= 2) s *= 2;
+    if (p.nk >= 4 && tiles <= n_sms / 2) s = 2;
+    if (p.nk >= 8 && tiles <= n_sms / 4 - 2) s = 4;
+    if (p.nk >= 16 && tiles <= n_sms / 8 - 4) s = 8;
     if (s > 1) {
       p.w = w, p.ntt = (p.t + w - 1) / w, p.split = s;
-      return launch_tc<1, true>(p, n_sms, st);
+      return launch_tc<1, kSplit>(p, n_sms, st);
     }
   }
-  const int cg = p.nmt > 1 ? 2 : 1, nmp = (p.nmt + cg - 1) / cg;
-  // the tile width with the least (rounds of tiles) x (width + what a tile
-  // costs whatever its width)
+  // The tile width with the least (rounds of tiles) x (width + what a tile
+  // costs whatever its width), with the weights or the tokens on the M side.
   int64_t best = INT64_MAX;
-  for (int w = 256; w >= 16 * cg; w -= 16 * cg) {
-    const int64_t rounds = ((int64_t)(p.t + w - 1) / w * nmp + n_sms / cg - 1) / (n_sms / cg), cost = rounds * (w + 48);
-    if (cost < best) best = cost, p.w = w;
+  bool tokens = false;
+  int cg = 1;
+  auto look = [&](bool tok, int nmt, int other, int per) {  // other: what the N side holds, per / 2 of a column
+    const int c = nmt > 1 ? 2 : 1, nmp = (nmt + c - 1) / c;
+    for (int w = 256; w >= 32 * c; w -= 16 * c) {
+      const int cols = w * per / 2;
+      const int64_t rounds = ((int64_t)((other + cols - 1) / cols) * nmp + n_sms / c - 1) / (n_sms / c), cost = rounds * (w + 48);
+      if (cost < best) best = cost, p.w = w, tokens = tok, cg = c;
+    }
+  };
+  const int tok_tiles = (p.t + 127) / 128;
+  const bool can = p.wide8 && !p.res;
+  if (can) look(true, tok_tiles, p.n, p.gated ? 1 : 2);
+  look(false, p.nmt, p.t, 2);
+  if (tokens) {
+    const int cols = p.gated ? p.w / 2 : p.w;
+    p.nmt = tok_tiles, p.ntt = (p.n + cols - 1) / cols;
+    return cg == 2 ? launch_tc<2, kTokens>(p, n_sms, st) : launch_tc<1, kTokens>(p, n_sms, st);
   }
   p.ntt = (p.t + p.w - 1) / p.w;
-  return cg == 2 ? launch_tc<2, false>(p, n_sms, st) : launch_tc<1, false>(p, n_sms, st);
+  return cg == 2 ? launch_tc<2, kWeights>(p, n_sms, st) : launch_tc<1, kWeights>(p, n_sms, st);
 }
 
 }  // namespace moe
