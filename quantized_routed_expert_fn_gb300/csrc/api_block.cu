@@ -98,7 +98,7 @@ int moe_norm(const void *x, int x_dtype, int64_t ldx, const float *w, float eps,
   if (!apart_or_same(mo, mx) || !apart(mo, mw) || !apart(ms, mx) || !apart(ms, mw))
     return fail(MOE_EINVAL, "out or scales overlap the inputs (out may be x itself, in its type)");
   moe::NormP p{};
-  p.t = t, p.h = h, p.eps = eps;
+  p.t = t, p.h = h, p.eps = eps, p.inv_h = 1.f / (float)h;
   p.y = x, p.ldy = ldx, p.y_bf16 = x_dtype == MOE_BF16;
   p.out_kind = norm_out_kind(out_dtype);
   p.w = w, p.out = out, p.ldo = ldo, p.s = scales, p.lds = lds;
@@ -147,7 +147,7 @@ int moe_add_norm(const moe_add_norm_cfg *c, const void *y, int y_dtype, int64_t 
     return fail(MOE_EINVAL, "scales without out");
   }
   moe::NormP p{};
-  p.t = t, p.h = h, p.eps = c->eps;
+  p.t = t, p.h = h, p.eps = c->eps, p.inv_h = 1.f / (float)h;
   p.y = y, p.ldy = ldy, p.y_bf16 = y_dtype == MOE_BF16;
   p.post = post, p.scale = c->scale, p.res_scale = c->res_scale, p.wp = c->w_post;
   p.gate = c->gate, p.ldg = c->ldg, p.gate_bf16 = c->gate_dtype == MOE_BF16, p.gate_cols = c->gate_cols;

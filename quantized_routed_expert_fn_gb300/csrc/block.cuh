@@ -14,7 +14,7 @@ namespace moe {
 enum { kNormOutF32 = 0, kNormOutBf16 = 1, kNormOutE4m3 = 2, kNormOutNone = 3 };
 struct NormP {
   int t, h;
-  float eps;
+  float eps, inv_h;  // inv_h = 1 / h
   const void *y;  // [t][h]: what is normalised, or the block's output
   int64_t ldy;
   int y_bf16;
@@ -36,10 +36,11 @@ struct NormP {
   int64_t ldo;
   uint8_t *s;  // e4m3: a scale byte per 128 of a row
   int64_t lds;
-  int T;  // threads of a row
+  int T;    // threads of a row
+  int ld8;  // rows that start anywhere, but alike: all strides' remainder by 8
 };
 constexpr int kNormMaxCols = 32768;
-cudaError_t launch_norm(const NormP &p, int n_sms, cudaStream_t st);
+cudaError_t launch_norm(NormP p, int n_sms, cudaStream_t st);
 
 // ---- log probabilities (logprobs.cu)
 struct LogprobsP {
@@ -97,5 +98,24 @@ struct Mm16P : Mm16Args {
 bool mm16_few(const Mm16Args &p, int n_sms);
 cudaError_t launch_mm16_few(const Mm16Args &p, int n_sms, cudaStream_t st);
 cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// 1 / (1 + exp(-x)) of a number, small values to their last bits.  exp(-|x|)
+// is 2^t, t = -|x| log2(e) carried in two terms, so that its relative error
+// does not grow with |x|; the quotient's by an approximate reciprocal of 1 ..
+// 2: 2^-22 in all.  (With expf and a division the epilogue of 8192 x 8192 x
+// 2048 took 250 us instead of the product's 151.)
+__device__ __forceinline__ float logistic(float x) {
+  constexpr float kHi = 1.44269502f, kLo = 1.9259629e-8f;  // log2(e)
+  const float y = fmaxf(-fabsf(x), -150.f), t = y * kHi, r = fmaf(y, kLo, fmaf(y, kHi, -t));
+  float e, q;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  e = fmaf(e * r, 0.693147181f, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
+  return (x < 0.f ? e : 1.f) * q;
+}
+
+#endif
 
 }  // namespace moe

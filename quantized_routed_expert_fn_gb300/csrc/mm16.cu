@@ -25,20 +25,6 @@ namespace {
 
 constexpr unsigned FULLM = 0xffffffffu;
 
-// 1 / (1 + exp(-x)) of a number, small values to their last bits.  exp(-|x|)
-// is 2^t, t = -|x| log2(e) carried in two terms, so that its relative error
-// does not grow with |x|; the quotient's by an approximate reciprocal of 1 ..
-// 2: 2^-22 in all.  (With expf and a division the epilogue of 8192 x 8192 x
-// 2048 took 250 us instead of the product's 151.)
-__device__ __forceinline__ float logistic(float x) {
-  constexpr float kHi = 1.44269502f, kLo = 1.9259629e-8f;  // log2(e)
-  const float y = fmaxf(-fabsf(x), -150.f), t = y * kHi, r = fmaf(y, kLo, fmaf(y, kHi, -t));
-  float e, q;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
-  e = fmaf(e * r, 0.693147181f, e);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
-  return (x < 0.f ? e : 1.f) * q;
-}
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case kActSilu: return z * logistic(z);
