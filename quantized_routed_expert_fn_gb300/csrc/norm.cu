@@ -9,14 +9,16 @@
 // values: V = 8 where all rows start on 16 bytes, or anywhere but alike (the
 // pieces then begin on 16 bytes in the row, see SH); 2 or 1 otherwise, so that
 // neighbouring lanes always touch neighbouring bytes.  Sums are 32-bit, in a
-// fixed tree.  65536 x 2048 bf16: 89 us, 6.0 TB/s; fp32 32768 x 2048: 80, 6.7;
-// 32816 x 4090 bf16 122 (with pieces of 2: 160).
+// fixed tree.  65536 x 2048 bf16: 87 us, 6.2 TB/s; fp32 32768 x 2048: 78, 6.9;
+// 32816 x 4090 bf16 114 (with pieces of 2: 160).  add_norm, 30000 x 4096, all
+// bf16, a gate a channel: 161 us, 6.1 TB/s; 30011 x 4090 214.
 #include <cuda_runtime.h>
 
 #include <type_traits>
 
 #include "block.cuh"
 #include "fp8.cuh"
+#include "tc05.cuh"
 
 namespace moe {
 namespace {
@@ -131,14 +133,13 @@ __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP 
 
 // SH (V = 8): rows that do not start on 16 bytes, but all matrices' alike: the
 // pieces begin `lead` values into a row, on 16 bytes; those before them and the
-// last ones are one value more for 16 of the row's threads.  What is per column
-// lies in shared memory as fp32, a word left out after each eight, so that
-// lanes that read 8 words apart meet no bank twice; a block keeps it over its
-// rows.
+// last ones are one value more for 16 of the row's threads.  Blocks walk over
+// the rows by a multiple of 8, so that a thread's columns stay the same ones;
+// what is per column lies in shared memory as each thread will read it.
 constexpr int kMaxVec = 96 * 1024;  // bytes of those
-__host__ __device__ constexpr int vec_words(int h) { return (h + 7) / 8 * 9; }
 struct Vecs {
-  const float *w, *wp, *g;
+  const float4 *w, *wp, *g;  // halves of pieces, blockDim apart
+  float xw, xwp, xg;         // of the value more
 };
 
 __device__ __forceinline__ float load1(const void *p, int bf16, int64_t i) {
@@ -149,30 +150,83 @@ __device__ __forceinline__ float load1(const void *p, int bf16, int64_t i) {
 }
 __device__ __forceinline__ float gate_of(const NormP &P, float g) { return P.gate_sigmoid && g == g ? logistic(g) : g; }
 
-// One row, in the registers of T threads (all of a warp's, or a block's, come
-// here together).
-template <int V, int NV, bool ADD, bool SH>
-__device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red)[4][32], const Vecs &vecs, uint32_t *s_max) {
-  constexpr int N = NV / V;
-  const int T = P.T, l = P.T >= (int)blockDim.x ? (int)threadIdx.x : (int)threadIdx.x & (T - 1);
-  const bool live = row < P.t;
-  const int h = live ? P.h : 0, lead = SH ? (int)(-((row & 7) * P.ld8) & 7) : 0;
-  auto col = [&](int j) { return lead + (j * T + l) * V; };
-  auto pieces = [&](auto f) {
+// What a thread holds of a row: pieces of V columns, and, SH, one value more.
+template <int V, int NV, bool SH>
+struct Place {
+  int T, l, h, lead, xc;  // xc: its column, < 0: none
+  __device__ __forceinline__ Place(const NormP &P, int64_t row) {
+    T = P.T, l = T >= (int)blockDim.x ? (int)threadIdx.x : (int)threadIdx.x & (T - 1);
+    h = row < P.t ? P.h : 0, lead = SH ? (int)(-((row & 7) * P.ld8) & 7) : 0, xc = -1;
+    if (SH && l < 8 && l < lead) xc = l;
+    if (SH && l >= 8 && l < 16) xc = h - (h - lead) % 8 + l - 8;
+    if (xc >= h) xc = -1;
+  }
+  __device__ __forceinline__ int col(int j) const { return lead + (j * T + l) * V; }
+  template <class F>
+  __device__ __forceinline__ void pieces(F f) const {
 #pragma unroll
-    for (int j = 0; j < N; j++)
+    for (int j = 0; j < NV / V; j++)
       if (col(j) + (SH ? V : 1) <= h) f(j);
+  }
+};
+
+// Several rows' values on their way to shared memory (RING): each thread
+// copies what it will hold itself, so that its own wait is all it needs.
+constexpr int kRing = 2;  // (3: fewer blocks fit; 30011 x 4090 254 us instead of 214)
+constexpr int kMaxRing = 200 * 1024;
+struct Ring {
+  uint8_t *y, *res;  // this thread's first 16 bytes of the first row's; others blockDim apart
+};
+// bytes of a thread's row of NV values
+__host__ __device__ constexpr int ring_row(int nv, int bf16) { return nv * (bf16 ? 2 : 4); }
+
+// The row's copies, into the ring's place `at`; no row: none.
+template <int V, int NV, bool ADD, bool SH>
+__device__ __forceinline__ void row_copies(const NormP &P, int64_t row, const Ring &ring, int at) {
+  const Place<V, NV, SH> L(P, row);
+  auto copy = [&](const void *p, int bf16, int64_t first, uint8_t *to) {
+    to += (size_t)at * ring_row(NV, bf16) * blockDim.x;
+    L.pieces([&](int j) {
+      const uint8_t *from = static_cast<const uint8_t *>(p) + (first + L.col(j)) * (bf16 ? 2 : 4);
+      if (bf16) {
+        cp_async16(to + (size_t)j * 16 * blockDim.x, from);
+      } else {
+        cp_async16(to + (size_t)(2 * j) * 16 * blockDim.x, from);
+        cp_async16(to + (size_t)(2 * j + 1) * 16 * blockDim.x, from + 16);
+      }
+    });
   };
-  // SH: the value more, of column xc (< 0: none)
-  int xc = -1;
-  if (SH && l < 8 && l < lead) xc = l;
-  if (SH && l >= 8 && l < 16) xc = h - (h - lead) % 8 + l - 8;
-  if (xc >= h) xc = -1;
-  int word[SH ? 8 : 1];  // of a piece's i-th column, behind 9 words for each piece before it
-  if constexpr (SH)
-#pragma unroll
-    for (int i = 0; i < 8; i++) word[i] = lead + i + ((lead + i) >> 3);
-  auto load = [&](const void *p, int bf16, int64_t at, float *to, float &x) {
+  copy(P.y, P.y_bf16, row * P.ldy, ring.y);
+  if constexpr (ADD) copy(P.res, P.res_bf16, row * P.ldr, ring.res);
+}
+
+// One row, in the registers of T threads (all of a warp's, or a block's, come
+// here together).  RING: its values lie in the ring's place `at`, but for the
+// one more, which is x0 and r0.
+template <int V, int NV, bool ADD, bool SH, bool RING>
+__device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red)[4][32], const Vecs &vecs, uint32_t *s_max,
+                                        const Ring &ring = Ring(), int at_ring = 0, float x0 = 0.f, float r0 = 0.f) {
+  constexpr int N = NV / V;
+  const Place<V, NV, SH> L(P, row);
+  const int T = L.T, l = L.l, h = L.h, xc = L.xc;
+  const bool live = row < P.t;
+  auto col = [&](int j) { return L.col(j); };
+  auto pieces = [&](auto f) { L.pieces(f); };
+  auto load = [&](const void *p, int bf16, int64_t at, float *to, float &x, const uint8_t *from, float value) {
+    if constexpr (RING) {
+      from += (size_t)at_ring * ring_row(NV, bf16) * blockDim.x;
+      const size_t step = 16 * blockDim.x;
+      if (bf16)
+        pieces([&](int j) { load_as<8, true>(from + j * step, 0, to + j * 8); });
+      else
+        pieces([&](int j) {
+          const float4 a = *reinterpret_cast<const float4 *>(from + 2 * j * step), b = *reinterpret_cast<const float4 *>(from + (2 * j + 1) * step);
+          float *v = to + j * 8;
+          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        });
+      x = value;
+      return;
+    }
     if (bf16) pieces([&](int j) { load_as<V, true>(p, at + col(j), to + j * V); });
     else pieces([&](int j) { load_as<V, false>(p, at + col(j), to + j * V); });
     if (SH && xc >= 0) x = load1(p, bf16, at + xc);
@@ -187,33 +241,31 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
       if (SH && xc >= 0) store_as<1, false>(p, at + xc, &x);
     }
   };
-  auto weigh = [&](const float *weights, const float *words) {
-    if constexpr (SH) {
-      pieces([&](int j) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[8 * j + i] *= words[9 * (j * T + l) + word[i]];
-      });
-      if (xc >= 0) x *= words[xc + (xc >> 3)];
-    } else {
-      pieces([&](int j) {
-        float w[V];
+  auto weigh = [&](const float *weights, const float4 *mine, float xw) {
+    pieces([&](int j) {
+      float w[V];
+      if constexpr (SH) {
+        const float4 a = mine[2 * j * blockDim.x], b = mine[(2 * j + 1) * blockDim.x];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      } else {
         load_as<V, false>(weights, col(j), w);
+      }
 #pragma unroll
-        for (int i = 0; i < V; i++) v[j * V + i] *= w[i];
-      });
-    }
+      for (int i = 0; i < V; i++) v[j * V + i] *= w[i];
+    });
+    if (SH) x *= xw;
   };
 #pragma unroll
   for (int i = 0; i < NV; i++) v[i] = 0.f;
-  load(P.y, P.y_bf16, row * P.ldy, v, x);
+  load(P.y, P.y_bf16, row * P.ldy, v, x, ring.y, x0);
   if constexpr (ADD) {
     float r[NV], rx = 0.f;  // on its way before the first store: the residual may be what is written
 #pragma unroll
     for (int i = 0; i < NV; i++) r[i] = 0.f;
-    load(P.res, P.res_bf16, row * P.ldr, r, rx);
+    load(P.res, P.res_bf16, row * P.ldr, r, rx, ring.res, r0);
     if (P.post) {
       normalise(v, x, P, red[0]);
-      if (P.wp) weigh(P.wp, vecs.wp);
+      if (P.wp) weigh(P.wp, vecs.wp, vecs.xwp);
     }
     // (gate by value first: a gate of 0 closes, whatever the scale)
     if (P.gate) {
@@ -223,7 +275,7 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
 #pragma unroll
         for (int i = 0; i < NV; i++) v[i] *= g;
       } else if (SH && P.ldg == 0) {
-        weigh(nullptr, vecs.g);
+        weigh(nullptr, vecs.g, vecs.xg);
       } else {
         auto by = [&](auto bf16, auto sigmoid) {
           pieces([&](int j) {
@@ -247,7 +299,7 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
     if (P.out_kind == kNormOutNone) return;
   }
   normalise(v, x, P, red[2]);
-  if (P.w) weigh(P.w, vecs.w);
+  if (P.w) weigh(P.w, vecs.w, vecs.xw);
   if (P.out_kind != kNormOutE4m3) {
     store(P.out, P.out_kind == kNormOutBf16, row * P.ldo);
     return;
@@ -298,33 +350,83 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
   }
 }
 
-// Without SH the grid covers the rows; with it, blocks walk over them.
-template <int V, int NV, bool ADD, bool SH>
-__global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__ NormP P) {
-  static_assert(!SH || V == 8, "");
-  __shared__ float s_red[SH ? 2 : 1][4][32];
-  extern __shared__ uint32_t s_dyn[];  // e4m3, V < 8: maxima [N][warps]; SH: vectors
+// Without SH and RING the grid covers the rows; with them, blocks walk over them.
+template <int V, int NV, bool ADD, bool SH, bool RING>
+__global__ void __launch_bounds__(kMaxThreads, NV <= 16 ? 2 : 0) norm_rows(const __grid_constant__ NormP P) {
+  static_assert(V == 8 || !(SH || RING), "");
+  constexpr bool WALK = SH || RING;
+  __shared__ float s_red[WALK ? 2 : 1][4][32];
+  extern __shared__ __align__(16) uint32_t s_dyn[];  // e4m3, V < 8: maxima [N][warps]; the ring; SH: vectors
   pdl_wait_prev();
   pdl_launch_next();
   const int per = P.T >= (int)blockDim.x ? 1 : (int)blockDim.x / P.T, mine = per > 1 ? (int)threadIdx.x / P.T : 0;
-  if constexpr (!SH) {
-    one_row<V, NV, ADD, SH>(P, (int64_t)blockIdx.x * per + mine, s_red[0], Vecs(), s_dyn);
-  } else {
-    float *at = reinterpret_cast<float *>(s_dyn);
-    auto place = [&](auto get) {
-      float *to = at;
-      for (int i = threadIdx.x; i < P.h; i += blockDim.x) to[i + (i >> 3)] = get(i);
-      at += vec_words(P.h);
+  if constexpr (!WALK) {
+    one_row<V, NV, ADD, SH, false>(P, (int64_t)blockIdx.x * per + mine, s_red[0], Vecs(), s_dyn);
+    return;
+  }
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t first = (int64_t)blockIdx.x * per;
+  uint8_t *at = reinterpret_cast<uint8_t *>(s_dyn);
+  Ring ring = {};
+  float x = 0.f, rx = 0.f;
+  // the value more of a row, a row ahead
+  auto more = [&](int64_t row) {
+    if constexpr (SH && RING) {
+      const Place<V, NV, SH> L(P, row);
+      if (L.xc >= 0) {
+        x = load1(P.y, P.y_bf16, row * P.ldy + L.xc);
+        if constexpr (ADD) rx = load1(P.res, P.res_bf16, row * P.ldr + L.xc);
+      } else {
+        x = rx = 0.f;
+      }
+    }
+  };
+  if constexpr (RING) {
+    ring.y = at + 16 * threadIdx.x;
+    at += (size_t)kRing * ring_row(NV, P.y_bf16) * blockDim.x;
+    if (ADD) {
+      ring.res = at + 16 * threadIdx.x;
+      at += (size_t)kRing * ring_row(NV, P.res_bf16) * blockDim.x;
+    }
+#pragma unroll
+    for (int i = 0; i < kRing - 1; i++) {
+      row_copies<V, NV, ADD, SH>(P, first + i * step + mine, ring, i);
+      tc05::cp_commit();
+    }
+    more(first + mine);
+  }
+  Vecs vecs = {};
+  if constexpr (SH) {
+    Place<V, NV, SH> L(P, first + mine < P.t ? first + mine : 0);
+    auto place = [&](auto get, float &xv) {
+      float4 *to = reinterpret_cast<float4 *>(at) + threadIdx.x;
+      L.pieces([&](int j) {
+        const int c = L.col(j);
+        to[2 * j * blockDim.x] = make_float4(get(c), get(c + 1), get(c + 2), get(c + 3));
+        to[(2 * j + 1) * blockDim.x] = make_float4(get(c + 4), get(c + 5), get(c + 6), get(c + 7));
+      });
+      xv = L.xc >= 0 ? get(L.xc) : 0.f;
+      at += (size_t)NV * 4 * blockDim.x;
       return to;
     };
-    Vecs vecs = {};
-    if (P.w) vecs.w = place([&](int c) { return P.w[c]; });
-    if (ADD && P.wp) vecs.wp = place([&](int c) { return P.wp[c]; });
-    if (ADD && P.gate && P.gate_cols != 1 && P.ldg == 0) vecs.g = place([&](int c) { return gate_of(P, load1(P.gate, P.gate_bf16, c)); });
-    __syncthreads();
-    int half = 0;  // the next row's sums lie in the other half
-    for (int64_t first = (int64_t)blockIdx.x * per; first < P.t; first += (int64_t)gridDim.x * per, half ^= 1)
-      one_row<V, NV, ADD, SH>(P, first + mine, s_red[half], vecs, s_dyn);
+    if (P.w) vecs.w = place([&](int c) { return P.w[c]; }, vecs.xw);
+    if (ADD && P.wp) vecs.wp = place([&](int c) { return P.wp[c]; }, vecs.xwp);
+    if (ADD && P.gate && P.gate_cols != 1 && P.ldg == 0)
+      vecs.g = place([&](int c) { return gate_of(P, load1(P.gate, P.gate_bf16, c)); }, vecs.xg);
+  }
+  int half = 0, slot = 0;  // the next row's sums lie in the other half
+  for (; first < P.t; first += step, half ^= 1) {
+    if constexpr (RING) {
+      row_copies<V, NV, ADD, SH>(P, first + (kRing - 1) * step + mine, ring, slot ? slot - 1 : kRing - 1);
+      tc05::cp_commit();
+      const float x0 = x, r0 = rx;
+      more(first + step + mine);
+      tc05::cp_wait_group<kRing - 1>();
+      one_row<V, NV, ADD, SH, true>(P, first + mine, s_red[half], vecs, s_dyn, ring, slot, x0, r0);
+      if (++slot == kRing) slot = 0;
+    } else {
+      one_row<V, NV, ADD, SH, false>(P, first + mine, s_red[half], vecs, s_dyn);
+    }
   }
 }
 
@@ -349,11 +451,12 @@ int piece(const NormP &p) {
   return v;
 }
 
+// vectors that SH holds in shared memory
+int vecs_of(const NormP &p) { return (p.w != nullptr) + (p.wp != nullptr) + (p.gate && p.gate_cols != 1 && p.ldg == 0); }
+
 // Whether no row starts on 16 bytes, but all matrices' rows alike.
 bool alike(NormP &p) {
   if (p.out_kind == kNormOutE4m3) return false;
-  const int vecs = (p.w != nullptr) + (p.wp != nullptr) + (p.gate && p.gate_cols != 1 && p.ldg == 0);
-  if (vecs * vec_words(p.h) * 4 > kMaxVec) return false;
   bool ok = true;
   int rem = -1;
   auto take = [&](const void *a, int64_t ld) {
@@ -374,24 +477,49 @@ int registers(F f) {
   return cudaFuncGetAttributes(&a, f) == cudaSuccess && a.numRegs > 0 ? (a.numRegs + 7) / 8 * 8 : 128;
 }
 
-template <int NV>
-cudaError_t launch_alike(NormP p, int T, int n_sms, cudaStream_t st) {
+// Bytes of shared memory of a walking launch, and whether it may be.
+int ring_bytes(const NormP &p, int nv, int block) {
+  return kRing * block * (ring_row(nv, p.y_bf16) + (p.res ? ring_row(nv, p.res_bf16) : 0));
+}
+
+// Blocks that stay resident walk over the rows; where each has several, the
+// values are bf16 and shared memory allows, with the next rows on their way
+// (30000 rows x 4096 with a gate a channel: 225 -> 161 us; of fp32 values
+// enough are in flight without: 32768 x 2048 160 us without, 310 with).
+// done: launched.
+template <int NV, bool SH>
+cudaError_t launch_walk(NormP p, int T, int n_sms, cudaStream_t st, bool &done) {
   p.T = T;
   const int block = T <= 32 ? 256 : T, rows = block / T;
-  const int vecs = (p.w != nullptr) + (p.wp != nullptr) + (p.gate && p.gate_cols != 1 && p.ldg == 0);
-  const size_t smem = (size_t)vecs * vec_words(p.h) * 4;
-  auto f = p.res ? norm_rows<8, NV, true, true> : norm_rows<8, NV, false, true>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxVec);
-    if (e != cudaSuccess) return e;
+  const int vecs = SH ? vecs_of(p) * NV * 4 * block : 0;
+  const int64_t need = ((int64_t)p.t + rows - 1) / rows;
+  static const int regs[4] = {SH ? registers(norm_rows<8, NV, false, SH, false>) : 128, SH ? registers(norm_rows<8, NV, true, SH, false>) : 128,
+                              registers(norm_rows<8, NV, false, SH, true>), registers(norm_rows<8, NV, true, SH, true>)};
+  if (vecs > kMaxVec) return cudaSuccess;
+  const bool small = p.y_bf16 && (!p.res || p.res_bf16);
+  for (int ring = small ? 1 : 0; ring >= (SH ? 0 : 1); ring--) {
+    const int smem = vecs + (ring ? ring_bytes(p, NV, block) : 0);
+    if (smem > kMaxRing) continue;
+    int fit = 65536 / (regs[2 * ring + (p.res != nullptr)] * block);
+    if (fit > 2048 / block) fit = 2048 / block;
+    if (fit > 226 * 1024 / (smem + 2048)) fit = 226 * 1024 / (smem + 2048);
+    int64_t cap = (int64_t)n_sms * (fit < 1 ? 1 : fit);
+    if (SH && cap > 8) cap -= cap % 8;
+    const int64_t rounds = (need + cap - 1) / cap;
+    if (ring && rounds < 2) continue;
+    auto f = p.res ? norm_rows<8, NV, true, SH, true> : norm_rows<8, NV, false, SH, true>;
+    if constexpr (SH)
+      if (!ring) f = p.res ? norm_rows<8, NV, true, SH, false> : norm_rows<8, NV, false, SH, false>;
+    if (smem > 46 * 1024) {  // (beside a kilobyte that is there anyway)
+      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+      if (e != cudaSuccess) return e;
+    }
+    done = true;
+    int64_t grid = (need + rounds - 1) / rounds;  // each with the same number of rounds
+    if (SH && rounds > 1) grid = (grid + 7) / 8 * 8;
+    return launch_pdl(f, dim3((unsigned)grid), block, smem, st, p);
   }
-  static const int regs[2] = {registers(norm_rows<8, NV, false, true>), registers(norm_rows<8, NV, true, true>)};
-  // as many thread blocks as stay resident, each with the same number of rounds
-  const int by_regs = 65536 / (regs[p.res != nullptr] * block), by_smem = (int)(220 * 1024 / (smem + 1024));
-  const int fit = by_regs < by_smem ? by_regs : by_smem;
-  const int64_t need = ((int64_t)p.t + rows - 1) / rows, cap = (int64_t)n_sms * (fit < 1 ? 1 : (fit > 2048 / block ? 2048 / block : fit));
-  const int64_t rounds = (need + cap - 1) / cap;
-  return launch_pdl(f, dim3((unsigned)((need + rounds - 1) / rounds)), block, smem, st, p);
+  return cudaSuccess;
 }
 
 template <int V, int NV>
@@ -400,8 +528,8 @@ cudaError_t launch_form(NormP p, int T, cudaStream_t st) {
   const int block = T <= 32 ? 128 : T, rows = block / T;  // (T above 32: a block a row)
   const size_t smem = p.out_kind == kNormOutE4m3 && V < 8 ? (size_t)(NV / V) * (block / 32) * 4 : 0;
   const dim3 grid((unsigned)(((int64_t)p.t + rows - 1) / rows));
-  return p.res ? launch_pdl(norm_rows<V, NV, true, false>, grid, block, smem, st, p)
-               : launch_pdl(norm_rows<V, NV, false, false>, grid, block, smem, st, p);
+  return p.res ? launch_pdl(norm_rows<V, NV, true, false, false>, grid, block, smem, st, p)
+               : launch_pdl(norm_rows<V, NV, false, false, false>, grid, block, smem, st, p);
 }
 
 // Values a thread holds.  What a thread does whatever their number (addresses,
@@ -413,7 +541,8 @@ cudaError_t launch_form(NormP p, int T, cudaStream_t st) {
 template <class T>
 int values_a_thread(const NormP &p, int n_sms, T threads) {
   int nv = 8;
-  const int most = p.res ? 16 : 32;
+  const bool ahead = p.y_bf16 && (!p.res || p.res_bf16) && (p.out_kind != kNormOutE4m3 || p.h > 8192);
+  const int most = p.res || ahead ? 16 : 32;
   while (nv < most && threads(2 * nv) < threads(nv) && (int64_t)p.t * threads(2 * nv) >= (int64_t)n_sms * 64 * 32) nv *= 2;
   while (threads(nv) > kMaxThreads) nv *= 2;
   return nv;
@@ -440,12 +569,19 @@ cudaError_t launch_v(const NormP &p, int n_sms, cudaStream_t st) {
 
 cudaError_t launch_norm(NormP p, int n_sms, cudaStream_t st) {
   const int v = piece(p);
-  if (v == 8) return launch_v<8>(p, n_sms, st);
+  const bool sh = v < 8 && p.h >= 32 && alike(p);
   auto threads = [&](int nv) { return threads_for(p.h, nv, 16); };
-  const int nv = values_a_thread(p, n_sms, threads), T = threads(nv);
-  if (nv <= 32 && p.h >= 32 && alike(p))
-    return nv == 8 ? launch_alike<8>(p, T, n_sms, st) : (nv == 16 ? launch_alike<16>(p, T, n_sms, st) : launch_alike<32>(p, T, n_sms, st));
-  return v == 2 ? launch_v<2>(p, n_sms, st) : launch_v<1>(p, n_sms, st);
+  if (v == 8 || sh) {
+    const int nv = values_a_thread(p, n_sms, threads), T = threads(nv);
+    bool done = false;
+    cudaError_t e = cudaSuccess;
+    if (sh) e = nv == 8 ? launch_walk<8, true>(p, T, n_sms, st, done) : (nv == 16 ? launch_walk<16, true>(p, T, n_sms, st, done) :
+                (nv == 32 ? launch_walk<32, true>(p, T, n_sms, st, done) : cudaSuccess));
+    else e = nv == 8 ? launch_walk<8, false>(p, T, n_sms, st, done) : (nv == 16 ? launch_walk<16, false>(p, T, n_sms, st, done) :
+             (nv == 32 ? launch_walk<32, false>(p, T, n_sms, st, done) : cudaSuccess));
+    if (done || e != cudaSuccess) return e;
+  }
+  return v == 8 ? launch_v<8>(p, n_sms, st) : (v == 2 ? launch_v<2>(p, n_sms, st) : launch_v<1>(p, n_sms, st));
 }
 
 }  // namespace moe

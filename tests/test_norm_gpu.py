@@ -118,6 +118,48 @@ def test_add_norm(moe, o, kinds):
             check_out(to, s, out, n, dn, (t, h))
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16", "e4m3", None])
+@pytest.mark.parametrize("t,h,pad,yk,rk", [(20000, 72, 0, "bf16", "bf16"), (40000, 33, 0, "bf16", "f32"), (6000, 1000, 8, "bf16", "f32"),
+                                           (4001, 4090, 0, "bf16", "bf16"), (9000, 2047, 0, "f32", "f32"), (2500, 8191, 0, "bf16", "f32"),
+                                           (2000, 16376, 0, "f32", "bf16"), (30000, 130, 3, "bf16", "bf16"), (5000, 2048, 0, "bf16", "f32")])
+def test_many_rows(moe, t, h, pad, yk, rk, out):
+    """Blocks that walk over rows, with the next ones on their way: every row against 64 bits (on the GPU)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(t + h)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    y, res = (rnd(t, h + pad).to(TYPES[k])[:, :h] for k in (yk, rk))
+    w, wp, gate = 1 + 0.2 * rnd(h), 1 + 0.2 * rnd(h), rnd(1, h)
+    y0, r0 = y.double(), res.double()
+    ro, (to, s) = torch.empty(t, h, dtype=TYPES[rk], device="cuda"), outputs(t, h, out) if out else (None, None)
+    moe.add_norm(y, res, ro, post=True, w_post=wp, gate=gate, gate_sigmoid=True, scale=0.5, out=to, w=w, scales=s)
+    n64 = lambda x, v: x / torch.sqrt((x * x).mean(1, keepdim=True) + 1e-6) * v  # noqa: E731
+    v = n64(y0, wp.double()) * torch.sigmoid(gate.double())
+    r = r0 + 0.5 * v
+    dr = ((0.5 * v).abs() * (rb.NORM + 12) + r0.abs() * 2 + r.abs()) * rb.U
+    assert ((ro.double() - r).abs() <= dr * 1.01 + r.abs() * rb.HALF[rk]).all()
+    if out:
+        rms = torch.sqrt((r * r).mean(1, keepdim=True) + 1e-6)
+        ref = n64(r, w.double())
+        bound = dr / rms * w.abs() + ref.abs() * (torch.sqrt((dr * dr).mean(1, keepdim=True)) / rms + (rb.NORM + 2) * rb.U)
+        if out == "e4m3":
+            step = torch.exp2(s.double() - 127).repeat_interleave(128, 1)[:, :h]
+            got = to.view(torch.float8_e4m3fn).double() * step
+            # half a step: 2^-4 of the value, or 2^-10 of the scale
+            assert ((got - ref).abs() <= bound * 1.1 + torch.maximum(ref.abs() * 2.0 ** -4, step * 2.0 ** -10)).all()
+            top = (ref.abs() / step).amax(1)
+            assert (top <= 448 * 1.001).all()
+        else:
+            assert ((to.double() - ref).abs() <= bound * 1.01 + ref.abs() * rb.HALF[out]).all()
+    # in place, and the plain norm
+    moe.add_norm(y, res, res, post=True, w_post=wp, gate=gate, gate_sigmoid=True, scale=0.5)
+    # (another form of the kernel may take it, whose sums have another order)
+    assert ((res.double() - r).abs() <= dr * 1.01 + r.abs() * rb.HALF[rk]).all()
+    n = torch.empty(t, h, dtype=TYPES[yk], device="cuda")
+    moe.norm(y, n, w=w)
+    ref = n64(y0, w.double())
+    assert ((n.double() - ref).abs() <= ref.abs() * ((rb.NORM + 2) * rb.U * 1.01 + rb.HALF[yk])).all()
+
+
 @pytest.mark.parametrize("h", [64, 2048, 2047])
 @pytest.mark.parametrize("out", ["f32", "bf16", "e4m3"])
 def test_norm_special_rows(moe, h, out):
