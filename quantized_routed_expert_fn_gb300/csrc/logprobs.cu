@@ -7,15 +7,21 @@
 //   log Z = ln(s0),  entropy = ln(2) (log2 s0 - s1 / s0),
 // both whatever the reference.  Moving it by d: s1 = 2^-d (s1 - d s0), s0 =
 // 2^-d s0.  The top_k tokens are the largest 64-bit keys (the logit in the
-// order of unsigned numbers, then the complement of the id): a threshold that
-// at least top_k of the row reach (of the maxima of 32 groups of the first
-// values the top_k-th) lets only few values into a list in shared memory,
-// which is cut to its largest 32 whenever it fills, raising the threshold.
+// order of unsigned numbers, then the complement of the id).  Each thread keeps
+// the largest value it saw; at least top_k of the row reach the top_k-th of
+// those, and only threads whose own does have such values: those threads'
+// values are looked at again, by the whole block, and the ones that reach it
+// go through lists in shared memory that are cut to their largest 32.  (With
+// candidates collected in the one pass, 4096 rows of 131072 with top 5 took 272
+// us instead of 182.)
 //
 // A row is a cluster of S blocks (few rows) or one block; the blocks' sums
-// and lists meet in the first one's shared memory.  The bound is HBM; per
-// value some eight instructions.
+// and lists meet in the first one's shared memory.  The bound is HBM, beside
+// some six instructions a value: 4096 x 131072 bf16 182 us, 5.9 TB/s (without
+// alternatives 156, 6.9); 1 x 131072 fp32, top 20: 8.0, of which launch, the
+// orders and exchanges are nearly all.
 #include <cuda_runtime.h>
+#include <type_traits>
 
 #include "block.cuh"
 #include "fp8.cuh"
@@ -27,8 +33,7 @@ namespace {
 constexpr unsigned FULLM = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kU = 4;         // 16-byte chunks of a thread in flight
-constexpr int kSlack = 1024;  // list entries beyond what one chunk a thread can add
+constexpr int kU = 4;  // 16-byte chunks of a thread at a time, as many on their way
 constexpr int kMaxS = 8;
 
 typedef unsigned long long key_t64;
@@ -45,17 +50,20 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ key_t64 shfl_xor64(key_t64 v, int m) {
+__device__ __forceinline__ key_t64 shfl_xor_of(key_t64 v, int m) {
   return (key_t64)__shfl_xor_sync(FULLM, (unsigned)(v >> 32), m) << 32 | __shfl_xor_sync(FULLM, (unsigned)v, m);
 }
+__device__ __forceinline__ uint32_t shfl_xor_of(uint32_t v, int m) { return __shfl_xor_sync(FULLM, v, m); }
 
 // Warp: 32 keys, one a lane, into descending order (a bitonic network), and
 // the largest 32 of two such lists.
-__device__ __forceinline__ key_t64 exchange(key_t64 v, int j, bool larger) {
-  const key_t64 o = shfl_xor64(v, j);
+template <class K>
+__device__ __forceinline__ K exchange(K v, int j, bool larger) {
+  const K o = shfl_xor_of(v, j);
   return (o > v) == larger ? o : v;
 }
-__device__ __forceinline__ key_t64 sort32(key_t64 v) {
+template <class K>
+__device__ __forceinline__ K sort32(K v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 2; n <= 32; n *= 2)
@@ -63,13 +71,27 @@ __device__ __forceinline__ key_t64 sort32(key_t64 v) {
     for (int j = n / 2; j; j /= 2) v = exchange(v, j, ((lane & j) == 0) == ((lane & n) == 0 || n == 32));
   return v;
 }
-__device__ __forceinline__ key_t64 merge32(key_t64 a, key_t64 b) {
+template <class K>
+__device__ __forceinline__ K merge32(K a, K b) {
   const int lane = threadIdx.x & 31;
-  const key_t64 r = (key_t64)__shfl_sync(FULLM, (unsigned)(b >> 32), 31 - lane) << 32 | __shfl_sync(FULLM, (unsigned)b, 31 - lane);
-  key_t64 v = a > r ? a : r;
+  const K r = shfl_xor_of(b, 31);  // the other way round
+  K v = a > r ? a : r;
 #pragma unroll
   for (int j = 16; j; j /= 2) v = exchange(v, j, (lane & j) == 0);
   return v;
+}
+// Block: the largest 32 of n sorted lists (a power of two of them, no more
+// than the block's warps), into the first; mine: this warp's list (warps from n
+// on: anything).
+template <class K>
+__device__ __forceinline__ void merge_lists(K (*lists)[32], int n, K mine) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < n) lists[warp][lane] = mine;
+  __syncthreads();
+  for (n /= 2; n; n /= 2) {
+    if (warp < n) lists[warp][lane] = mine = merge32(mine, lists[warp + n][lane]);
+    __syncthreads();
+  }
 }
 
 // What a thread, a block or a row has summed.  ref: the reference logit (-inf:
@@ -110,15 +132,58 @@ struct Chunk {
   }
 };
 
+// Largest of a chunk's values, without NaN.
+template <bool BF16>
+__device__ __forceinline__ float chunk_max(const uint4 &r) {
+  if constexpr (BF16) {
+    uint32_t m, n;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(r.x), "r"(r.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(r.z), "r"(r.w));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    return fmaxf(bf16lo(m), bf16hi(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+}
+
+// A chunk's terms.  SAFE: masked values (infinities below, NaN) count nothing,
+// and references may be so large that l * c overflows; without it such values
+// leave s1 no number.
+template <bool BF16, bool SAFE>
+__device__ __forceinline__ void add_chunk(Sums &a, const uint4 &r, float c) {
+  constexpr int CH = Chunk<BF16>::n;
+  float v[CH], t0 = 0.f, t1 = 0.f;
+  Chunk<BF16>::unpack(r, v);
+  if (!SAFE || !a.big) {
+#pragma unroll
+    for (int e = 0; e < CH; e++) {
+      float x = fmaf(v[e], c, -a.mu);
+      if (SAFE) x = fmaxf(x, -200.f);  // 2^-200 is 0
+      const float p = ex2(x);
+      t0 += p, t1 = fmaf(p, x, t1);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < CH; e++) {
+      const float x = fmaxf((v[e] - a.ref) * c, -200.f), p = ex2(x);
+      t0 += p, t1 = fmaf(p, x, t1);
+    }
+  }
+  a.s0 += t0, a.s1 += t1;
+}
+
 template <bool BF16, int T>
 __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ LogprobsP P) {
   using C = Chunk<BF16>;
-  constexpr int CH = C::n, W = T / 32, kCap = T * CH + kSlack, kSize = BF16 ? 2 : 4;
-  __shared__ key_t64 s_list[kCap];
+  constexpr int CH = C::n, W = T / 32, kSize = BF16 ? 2 : 4;
+  constexpr int kAdd = 32 * CH, kCap = 32 + kAdd;  // list entries that a warp's chunk can add; of a warp
+  __shared__ key_t64 s_list[W][kCap];
   __shared__ key_t64 s_top[W][32], s_lists[kMaxS][32];  // of the block's warps, of the row's blocks
-  __shared__ key_t64 s_tau;
-  __shared__ float s_gm[32], s_ref[32], s_s0[32], s_s1[32];
-  __shared__ int s_cnt, s_inf[32];
+  __shared__ uint32_t s_max[W][32];
+  __shared__ uint16_t s_cand[T];  // threads whose values may be among the largest
+  __shared__ int s_cand_n;
+  __shared__ float s_ref[32], s_s0[32], s_s1[32];
+  __shared__ int s_inf[32];
   __shared__ float s_rank[kMaxS][4];  // of the row's blocks: reference, s0, s1, infinities
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait_prev();
@@ -134,6 +199,7 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
   const int off = (int)(((uintptr_t)at & 15u) / kSize), nch = (len + off + CH - 1) / CH;
   const uint4 *chunks = reinterpret_cast<const uint4 *>(at - off * kSize);
   const int niter = (nch + T * kU - 1) / (T * kU);
+  const int whole0 = off ? 1 : 0, whole1 = (len + off) / CH;  // chunks that lie in the row
 
   float tok = 0.f;  // this thread's first given token
   int tok_id = -1;
@@ -142,171 +208,153 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     if ((unsigned)tok_id < (unsigned)P.v) tok = C::load1(base, tok_id);
   }
 
-  auto load = [&](uint4 (&r)[kU], int it) {
+  // chunk i; edges value by value, NaN (masked) outside the row
+  auto load_one = [&](int i) {
+    const int first = i * CH - off;
+    if (first >= 0 && first + CH <= len) return ldg_stream4(chunks + i);
+    uint32_t w[4];
 #pragma unroll
-    for (int u = 0; u < kU; u++) {
-      const int i = (it * kU + u) * T + tid, first = i * CH - off;
-      if (first >= 0 && first + CH <= len) {
-        r[u] = ldg_stream4(chunks + i);
-      } else {  // edges, value by value; NaN (masked) outside
-        uint32_t w[4];
+    for (int j = 0; j < 4; j++) {
+      if constexpr (BF16) {
+        uint32_t h[2];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          if constexpr (BF16) {
-            uint32_t h[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              const int x = first + 2 * j + e;
-              h[e] = x >= 0 && x < len ? reinterpret_cast<const uint16_t *>(at)[x] : 0x7fffu;
-            }
-            w[j] = h[0] | h[1] << 16;
-          } else {
-            const int x = first + j;
-            w[j] = x >= 0 && x < len ? reinterpret_cast<const uint32_t *>(at)[x] : 0x7fffffffu;
-          }
+        for (int e = 0; e < 2; e++) {
+          const int x = first + 2 * j + e;
+          h[e] = x >= 0 && x < len ? reinterpret_cast<const uint16_t *>(at)[x] : 0x7fffu;
         }
-        r[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        w[j] = h[0] | h[1] << 16;
+      } else {
+        const int x = first + j;
+        w[j] = x >= 0 && x < len ? reinterpret_cast<const uint32_t *>(at)[x] : 0x7fffffffu;
       }
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   };
-  auto max_of = [&](const float (&v)[CH]) {
+  // whether all of iteration it's chunks lie in the row
+  auto inside = [&](int it) { return it * kU * T >= whole0 && (it + 1) * kU * T <= whole1; };
+  auto load = [&](uint4 (&r)[kU], int it) {
+    if (inside(it)) {
+#pragma unroll
+      for (int u = 0; u < kU; u++) r[u] = ldg_stream4(chunks + (it * kU + u) * T + tid);
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; u++) r[u] = load_one((it * kU + u) * T + tid);
+  };
+  auto max_of = [&](const uint4 (&r)[kU]) {
     float m = -kInf;
 #pragma unroll
-    for (int e = 0; e < CH; e++) m = fmaxf(m, v[e]);  // drops NaN
+    for (int u = 0; u < kU; u++) m = fmaxf(m, chunk_max<BF16>(r[u]));  // drops NaN
     return m;
   };
 
   uint4 cur[kU], nxt[kU];
   load(cur, 0);
-  if (tid == 0) s_cnt = 0;
-  // ---- the first values: the reference, and a first threshold
+  // ---- the sums, and the largest value of each thread
   Sums sum;
-  key_t64 tau = 0;
   {
-    float m = -kInf;
+    float m = max_of(cur);
 #pragma unroll
-    for (int u = 0; u < kU; u++) {
-      float v[CH];
-      C::unpack(cur[u], v);
-      m = fmaxf(m, max_of(v));
-    }
-    constexpr int per = T / 32;  // threads of a group
-#pragma unroll
-    for (int o = 1; o < per && o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(FULLM, m, o));
-    if (lane % per == 0) s_gm[tid / per] = m;
-    __syncthreads();
-    const float g = s_gm[lane];
-    float b = g;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) b = fmaxf(b, __shfl_xor_sync(FULLM, b, o));
-    set_ref(sum, b, c);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULLM, m, o));
+    set_ref(sum, m, c);
     sum.s0 = sum.s1 = 0.f;
-    if (P.k > 0) {
-      int r = 0;
-#pragma unroll
-      for (int j = 0; j < 32; j++) {
-        const float o = __shfl_sync(FULLM, g, j);
-        r += o > g || (o == g && j < lane);
-      }
-      const unsigned who = __ballot_sync(FULLM, r == P.k - 1);
-      const float t = __shfl_sync(FULLM, g, __ffs(who) - 1);
-      if (t > -kInf) tau = (key_t64)okey(t) << 32;
-    }
   }
-  if (tid == 0) s_tau = tau;
-  float tau_v = tau ? of_okey((uint32_t)(tau >> 32)) : -kInf;
-  int seen = 0;  // entries of the list, as far as this thread's own places tell
-
-  // values of a chunk that pass the threshold, into the list
-  auto push = [&](const uint4 &r, int i) {
-    float v[CH];
-    C::unpack(r, v);
-#pragma unroll
-    for (int e = 0; e < CH; e++) {
-      if (v[e] >= tau_v && v[e] > -kInf) {
-        const key_t64 key = (key_t64)okey(v[e]) << 32 | (uint32_t)~(uint32_t)(lo + i * CH - off + e);
-        if (key > tau) {
-          const int n = atomicAdd(&s_cnt, 1);
-          if (n < kCap) s_list[n] = key;
-          seen = n + 1;
-        }
-      }
-    }
-  };
-  // All threads: the list's largest 32 become the list.  [drop0, drop1): ids
-  // that are left out.
-  auto compact = [&](int drop0, int drop1) {
-    const int n = min(s_cnt, kCap);
-    key_t64 r = 0;
-    for (int b = warp * 32; b < n; b += T) {
-      key_t64 x = b + lane < n ? s_list[b + lane] : 0;
-      const int id = (int)~(uint32_t)x - lo;
-      if (x && id >= drop0 && id < drop1) x = 0;
-      r = merge32(r, sort32(x));
-    }
-    s_top[warp][lane] = r;
-    __syncthreads();
-#pragma unroll
-    for (int s = W / 2; s; s /= 2) {
-      if (warp < s) s_top[warp][lane] = r = merge32(r, s_top[warp + s][lane]);
-      __syncthreads();
-    }
-    if (warp == 0) {
-      s_list[lane] = r;
-      const unsigned any = __ballot_sync(FULLM, r != 0);
-      if (lane == 0) s_cnt = __popc(any);
-      if (lane == P.k - 1 && r > s_tau) s_tau = r;
-    }
-    __syncthreads();
-    tau = s_tau;
-    tau_v = tau ? of_okey((uint32_t)(tau >> 32)) : -kInf;
-    seen = 0;
-  };
-
+  const float room = 4.f / c;  // how far above its reference a value may lie
+  float most = -kInf;
+  bool safe = false;
   for (int it = 0; it < niter; it++) {
     if (it + 1 < niter) load(nxt, it + 1);
-#pragma unroll
-    for (int u = 0; u < kU; u++) {
-      float v[CH];
-      C::unpack(cur[u], v);
-      const float m = max_of(v);
-      if (m > sum.ref) {
-        Sums to;
-        set_ref(to, m, c);
-        move_to(sum, to, c);
-      }
-      if (!sum.big) {
-#pragma unroll
-        for (int e = 0; e < CH; e++) {
-          const float x = fmaxf(fmaf(v[e], c, -sum.mu), -200.f), p = ex2(x);  // masked values: 2^-200 is 0
-          sum.s0 += p, sum.s1 = fmaf(p, x, sum.s1);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < CH; e++) {
-          const float x = fmaxf((v[e] - sum.ref) * c, -200.f), p = ex2(x);
-          sum.s0 += p, sum.s1 = fmaf(p, x, sum.s1);
-        }
-      }
-      if (P.k > 0 && m >= tau_v) push(cur[u], (it * kU + u) * T + tid);
+    const float m = max_of(cur);
+    most = fmaxf(most, m);
+    if (__any_sync(FULLM, !(m <= sum.ref + room)) && m > sum.ref) {  // (not of an infinite reference)
+      Sums to;
+      set_ref(to, m, c);
+      move_to(sum, to, c);
     }
-    if (P.k > 0 && __syncthreads_or(seen > kSlack)) {
-      // the list is long: cut it, and if it did not hold all of these values,
-      // take them again a chunk at a time
-      const bool over = s_cnt > kCap;
-      const int d0 = it * kU * T * CH - off, d1 = d0 + kU * T * CH;
-      __syncthreads();
-      compact(over ? d0 : 0, over ? d1 : 0);
-      if (over)
+    const Sums before = sum;
+    const bool careful = safe || !inside(it) || __any_sync(FULLM, sum.big);
+    if (careful) {
 #pragma unroll 1
-        for (int u = 0; u < kU; u++) {
-          push(u == 0 ? cur[0] : (u == 1 ? cur[1] : (u == 2 ? cur[2] : cur[3])), (it * kU + u) * T + tid);
-          __syncthreads();
-          compact(0, 0);
-        }
+      for (int u = 0; u < kU; u++) add_chunk<BF16, true>(sum, u == 0 ? cur[0] : (u == 1 ? cur[1] : (u == 2 ? cur[2] : cur[3])), c);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kU; u++) add_chunk<BF16, false>(sum, cur[u], c);
+      // masked values: these again, and the rest of the row, with care
+      if (__any_sync(FULLM, !(fabsf(sum.s1) < kInf))) {
+        safe = true;
+        sum = before;
+#pragma unroll 1
+        for (int u = 0; u < kU; u++) add_chunk<BF16, true>(sum, u == 0 ? cur[0] : (u == 1 ? cur[1] : (u == 2 ? cur[2] : cur[3])), c);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kU; u++) cur[u] = nxt[u];
+  }
+
+  // ---- the largest values
+  key_t64 tau = 0;
+  float tau_v = -kInf;
+  int cnt = 0;  // entries of the warp's list
+
+  // Warp: the list's largest 32 become the list, in descending order; the
+  // threshold rises to its top_k-th.
+  auto compact = [&] {
+    __syncwarp();
+    key_t64 r = 0;
+    for (int b = 0; b < cnt; b += 32) r = merge32(r, sort32(b + lane < cnt ? s_list[warp][b + lane] : 0));
+    __syncwarp();
+    s_list[warp][lane] = r;
+    cnt = __popc(__ballot_sync(FULLM, r != 0));
+    const key_t64 t = (key_t64)__shfl_sync(FULLM, (unsigned)(r >> 32), P.k - 1) << 32 | __shfl_sync(FULLM, (unsigned)r, P.k - 1);
+    if (t > tau) tau = t, tau_v = of_okey((uint32_t)(tau >> 32));
+    __syncwarp();
+  };
+  // Warp: values of its chunk i that pass the threshold, into the list.
+  auto push = [&](const uint4 &r, int i) {
+    float v[CH];
+    C::unpack(r, v);
+    if (cnt > kCap - kAdd) compact();
+    unsigned left = 0;  // values of this lane's that may
+#pragma unroll
+    for (int e = 0; e < CH; e++) left |= (unsigned)(v[e] >= tau_v && v[e] > -kInf) << e;  // false for NaN
+    while (__any_sync(FULLM, left != 0)) {
+      const int e = __ffs(left) - 1;
+      float x = v[0];
+#pragma unroll
+      for (int j = 1; j < CH; j++) x = e == j ? v[j] : x;
+      const key_t64 key = (key_t64)okey(x) << 32 | (uint32_t)~(uint32_t)(lo + i * CH - off + e);
+      const bool in = left && key > tau;
+      const unsigned who = __ballot_sync(FULLM, in);
+      if (in) s_list[warp][cnt + __popc(who & ((1u << lane) - 1u))] = key;
+      cnt += __popc(who);
+      left &= left - 1;
+    }
+  };
+  if (P.k > 0) {
+    // the threads' maxima in order: top_k of the row reach the top_k-th, and
+    // only the threads whose own does have such values: their chunks again,
+    // shared out over the block (they lie in L2, or did not long ago)
+    const uint32_t mine = most > -kInf ? okey(most) : 0u;
+    if (tid == 0) s_cand_n = 0;
+    merge_lists(s_max, W, sort32(mine));
+    const uint32_t least = s_max[0][P.k - 1];
+    tau = (key_t64)least << 32, tau_v = least ? of_okey(least) : -kInf;
+    const bool has = mine != 0 && mine >= least;
+    const unsigned who = __ballot_sync(FULLM, has);
+    int first = 0;
+    if (lane == 0 && who) first = atomicAdd(&s_cand_n, __popc(who));
+    first = __shfl_sync(FULLM, first, 0);
+    if (has) s_cand[first + __popc(who & ((1u << lane) - 1u))] = (uint16_t)tid;
+    __syncthreads();
+    const int n = s_cand_n, total = n * niter * kU;
+    for (int b = 0; b < total; b += T) {
+      const int x = b + tid, j = n ? x / n : 0, i = j * T + (x < total ? s_cand[x - j * n] : 0);
+      const bool in = x < total && i < nch;
+      uint4 r = in ? load_one(i) : make_uint4(~0u, ~0u, ~0u, ~0u);  // (no numbers)
+      if (__any_sync(FULLM, in && chunk_max<BF16>(r) >= tau_v)) push(r, i);
+    }
+    compact();
+    merge_lists(s_top, W, s_list[warp][lane]);
   }
 
   // ---- the block's sums and list
@@ -331,7 +379,6 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     ninf += __shfl_xor_sync(FULLM, ninf, o);
   }
   if (lane == 0) s_s0[warp] = sum.s0, s_s1[warp] = sum.s1, s_inf[warp] = ninf;
-  if (P.k > 0) compact(0, 0);  // begins after a barrier of its own: the list's last entries are there
   __syncthreads();
   if (warp == 0) {
     all.s0 = lane < W ? s_s0[lane] : 0.f, all.s1 = lane < W ? s_s1[lane] : 0.f;
@@ -348,7 +395,7 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
   if (S > 1) {
     tc05::cluster_wait();  // every block of the row has begun: its shared memory can be written
     if (warp == 0) {
-      tc05::st_cluster(tc05::map_rank(&s_lists[rank][lane], 0), P.k > 0 ? s_list[lane] : 0ull);
+      tc05::st_cluster(tc05::map_rank(&s_lists[rank][lane], 0), P.k > 0 ? s_top[0][lane] : 0ull);
       if (lane == 0) {
         const uint32_t f = tc05::map_rank(&s_rank[rank][0], 0);
         tc05::st_cluster(f, all.ref), tc05::st_cluster(f + 4, all.s0), tc05::st_cluster(f + 8, all.s1);
@@ -379,10 +426,13 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
       }
       all.s0 = __shfl_sync(FULLM, all.s0, 0), all.s1 = __shfl_sync(FULLM, all.s1, 0);
       ninf = (int)__shfl_sync(FULLM, fi, 0);
-      for (int b = 0; b < S; b++) top = merge32(top, s_lists[b][lane]);
+    }
+    if (P.k > 0) {  // (a row of several blocks has 256 threads a block or more: a warp a list)
+      merge_lists(s_lists, S, warp < S ? s_lists[warp][lane] : 0ull);
+      top = s_lists[0][lane];
     }
   } else if (warp == 0 && P.k > 0) {
-    top = s_list[lane];
+    top = s_top[0][lane];
   }
   // ---- the answers
   if (warp == 0) {
@@ -442,9 +492,20 @@ cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st) {
   p.S = 1;
   while (p.S < kMaxS && (int64_t)p.t * p.S * 2 <= 2 * n_sms && p.v / (p.S * 2) >= 4096) p.S *= 2;
   p.seg = ((p.v + p.S - 1) / p.S + 7) / 8 * 8;
-  if (p.seg <= 2048) return p.bf16 ? launch_t<true, 128>(p, st) : launch_t<false, 128>(p, st);
-  if (p.seg <= 8192) return p.bf16 ? launch_t<true, 256>(p, st) : launch_t<false, 256>(p, st);
-  return p.bf16 ? launch_t<true, 512>(p, st) : launch_t<false, 512>(p, st);
+  // Threads of a block: what it does once a row (orders, exchanges) costs as
+  // much as some values of each thread.  us, 16384 rows, top 5, fp32, with 32 /
+  // 64 / 128 / 256 threads: of 1000 27 / 44 / 76 / 153, of 4000 61 / 68 / 94 /
+  // 164, of 8000 136 / 103 / 121 / 189, of 32000 531 / 437 / 359 / 371; few
+  // rows (256) of 4000 8.1 / 6.3 / 5.8 / 6.0, of 32000 33 / 17 / 10.6 / 9.4.
+  const int64_t bytes = (int64_t)p.seg * (p.bf16 ? 2 : 4);
+  const bool few = (int64_t)p.t < 8 * (int64_t)n_sms;
+  int T = bytes <= (few ? 4096 : 20480) ? 32 : (bytes <= (few ? 8192 : 40960) ? 64 : (bytes <= (few ? 20480 : 131072) ? 128 : 256));
+  if (p.S > 1) T = 256;  // a warp for each of a row's lists
+  auto go = [&](auto n) { return p.bf16 ? launch_t<true, decltype(n)::value>(p, st) : launch_t<false, decltype(n)::value>(p, st); };
+  if (T == 32) return go(std::integral_constant<int, 32>());
+  if (T == 64) return go(std::integral_constant<int, 64>());
+  if (T == 128) return go(std::integral_constant<int, 128>());
+  return go(std::integral_constant<int, 256>());
 }
 
 }  // namespace moe

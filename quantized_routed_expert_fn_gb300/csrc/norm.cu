@@ -571,7 +571,7 @@ cudaError_t launch_norm(NormP p, int n_sms, cudaStream_t st) {
   const int v = piece(p);
   const bool sh = v < 8 && p.h >= 32 && alike(p);
   auto threads = [&](int nv) { return threads_for(p.h, nv, 16); };
-  if (v == 8 || sh) {
+  if (sh || (v == 8 && p.h >= 256)) {  // (shorter rows of whole pieces have fewer threads than a walk takes)
     const int nv = values_a_thread(p, n_sms, threads), T = threads(nv);
     bool done = false;
     cudaError_t e = cudaSuccess;
