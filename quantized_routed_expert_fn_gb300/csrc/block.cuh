@@ -80,9 +80,10 @@ struct Mm16Args {
   // tensor cores: N side of a tile, k blocks, M and N tiles, CTAs that split
   // k, ring, columns of tensor memory
   int w, nk, nmt, ntt, split, stage, stages, tmem_cols;
+  int two;  // k in two halves, each with an accumulator
 };
 struct Mm16P : Mm16Args {
-  CUtensorMap tm_a, tm_b;
+  CUtensorMap tm_a, tm_b, tm_r;
 };
 // Whether the few-row kernel takes the rows.  us a call, few-row /
 // tensor-core, in a graph of calls on weights that are not in L2 (fp32 out):

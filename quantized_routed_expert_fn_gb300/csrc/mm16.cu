@@ -25,10 +25,28 @@ namespace {
 
 constexpr unsigned FULLM = 0xffffffffu;
 
+// z times the normal distribution's function P(z).  P(-a) = exp(-a^2 / 2) q(u),
+// u = 1 / (1 + 0.23 a), q a polynomial fitted to erfcx(a / sqrt 2) / 2 over 0
+// <= a <= 14.5 (least relative error, by reweighted least squares: 5e-8); the
+// square and its multiple of log2(e) are carried in two terms.
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fminf(fabsf(z), 15.f);
+  float u, e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u) : "f"(fmaf(0.23f, a, 1.f)));
+  float q = -7.84846712e-02f;
+  q = fmaf(q, u, 2.90501394e-01f), q = fmaf(q, u, -2.78316041e-01f), q = fmaf(q, u, 3.01701127e-01f);
+  q = fmaf(q, u, -3.30880031e-02f), q = fmaf(q, u, 1.19590782e-01f), q = fmaf(q, u, 8.57416379e-02f);
+  q = fmaf(q, u, 9.23817254e-02f), q = fmaf(q, u, -2.79751048e-05f);
+  constexpr float kHi = 0.72134751f, kLo = 9.6298150e-9f;  // log2(e) / 2
+  const float s = a * a, t = s * kHi, r = fmaf(s, kLo, fmaf(fmaf(a, a, -s), kHi, fmaf(s, kHi, -t)));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-t));
+  const float below = q * fmaf(-e * r, 0.693147181f, e);
+  return z * (z < 0.f ? below : 1.f - below);
+}
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case kActSilu: return z * logistic(z);
-    case kActGelu: return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    case kActGelu: return gelu(z);
     case kActGeluTanh:  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
       return z * logistic(z * fmaf(z * z, 0.07135481627f, 1.5957691216f));
     case kActRelu: return z < 0.f ? 0.f : z;  // NaN stays
@@ -222,14 +240,17 @@ __global__ void __launch_bounds__(32 * kFewWarps) mm16_few_rows(const __grid_con
 // The full and acc_empty barriers of a pair are the even CTA's; the others are
 // each CTA's own, committed to both.
 constexpr int kEpi = 16;  // epilogue warps, in groups of four (one for each 32 lanes of TMEM)
-constexpr int kTcThreads = 32 * (kEpi + 2);
+constexpr int kTcThreads = 32 * (kEpi + 3);
+constexpr int kResBufs = 2;  // pieces of residuals on their way
 constexpr int kMaxStages = 10;
 constexpr int kPiece = 16 * 128 * 4;  // bytes of 16 tokens x 128 rows
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], res_full[kResBufs], res_empty[kResBufs], drain;
   uint32_t tmem;
 };
+constexpr int kResPiece = 128 * 128;      // bytes of 128 tokens' residuals: 64 columns of bf16, 32 of fp32
+static_assert(kResBufs * kResPiece <= kEpi / 4 * kPiece, "they lie where the other forms have their pieces");
 constexpr int kOffBars = kEpi / 4 * kPiece;
 constexpr int kOffRing = (kOffBars + (int)sizeof(Bars) + 1023) / 1024 * 1024;
 constexpr int kRoom = 226 * 1024 - kOffRing;
@@ -256,15 +277,6 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t par, const 
 }
 
 // 16 neighbouring values of SIZE bytes, 32 bytes an access
-template <int SIZE>
-__device__ __forceinline__ void load_run(const void *p, uint32_t *v) {
-#pragma unroll
-  for (int i = 0; i < SIZE / 2; i++)
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[8 * i]), "=r"(v[8 * i + 1]), "=r"(v[8 * i + 2]), "=r"(v[8 * i + 3]), "=r"(v[8 * i + 4]),
-                   "=r"(v[8 * i + 5]), "=r"(v[8 * i + 6]), "=r"(v[8 * i + 7])
-                 : "l"(static_cast<const uint8_t *>(p) + 32 * i));
-}
 template <int SIZE>
 __device__ __forceinline__ void store_run(void *p, const uint32_t *v) {
 #pragma unroll
@@ -425,6 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
   if (tid == 0) {
     for (int s = 0; s < S; s++) mbar_init(&B.full[s], 1), mbar_init(&B.empty[s], 1);
     for (int b = 0; b < 2; b++) mbar_init(&B.acc_full[b], 1), mbar_init(&B.acc_empty[b], kEpi * CG);
+    for (int b = 0; b < kResBufs; b++) mbar_init(&B.res_full[b], 1), mbar_init(&B.res_empty[b], kEpi);
     mbar_init(&B.drain, 1);
     fence_mbar_init();
   }
@@ -475,11 +488,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
       bool ok = true;
       const uint32_t base = smem_u32(ring), idesc = tc05::idesc_f16(128 * CG, w);
       for (int lt = 0; lt < my_tiles && ok; lt++) {
-        const int b = lt & 1;
-        if (!tc_wait<CL>(&B.acc_empty[b], (uint32_t)(((lt >> 1) & 1) ^ 1), P)) break;
+        const int b = P.two ? 0 : lt & 1, use = P.two ? lt : lt >> 1;
+        if (!tc_wait<CL>(&B.acc_empty[b], (uint32_t)((use & 1) ^ 1), P)) break;
         tc05::fence_after();
-        const uint32_t d = tmem + (uint32_t)(b * 256);
+        uint32_t d = tmem + (uint32_t)(b * 256);
+        int start = kb0;
         for (int kb = kb0; kb < kb1; kb++) {
+          if (P.two && kb == P.nk / 2) d += 256, start = kb;
           if (!tc_wait<CL>(&B.full[s], ph, P)) {
             ok = false;
             break;
@@ -488,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
           const uint32_t st = base + (uint32_t)(s * P.stage);
           const uint64_t ad = tc05::sdesc(st), bd = tc05::sdesc(st + 16384);
 #pragma unroll
-          for (int j = 0; j < 4; j++) tc05::mma_f16<CG>(d, ad + 2 * j, bd + 2 * j, idesc, kb != kb0 || j != 0);
+          for (int j = 0; j < 4; j++) tc05::mma_f16<CG>(d, ad + 2 * j, bd + 2 * j, idesc, kb != start || j != 0);
           if constexpr (CG == 1) tc05::commit(&B.empty[s]);
           else tc05::commit_pair(&B.empty[s]);
           if (++s == S) s = 0, ph ^= 1;
@@ -545,39 +560,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
     if (lane == 0 && mrank == 0)
       for (int g = f > S ? f - S : 0; g < f; g++) tc_wait<CL>(&B.full[g % S], (uint32_t)((g / S) & 1), P);
     __syncwarp();
+  } else if (warp == kEpi + 2) {
+    // ---------------------------------------------------------------- residuals
+    // (tokens on the M side) this CTA's 128 tokens' of a tile, a piece of
+    // columns after the other
+    if (TOK && P.res) {
+      int f = 0;
+      bool ok = true;
+      const int step = P.res_bf16 ? 64 : 32;
+      for (int lt = 0; lt < my_tiles && ok; lt++) {
+        const Tile T = next_tile();
+        const int end = min(cols, P.n - T.n0);
+        for (int c = 0; c < end; c += step, f++) {
+          const int b = f % kResBufs;
+          if (!tc_warp_wait<false>(&B.res_empty[b], (uint32_t)(((f / kResBufs) & 1) ^ 1), P)) {
+            ok = false;
+            break;
+          }
+          if (tc05::elect_one()) {
+            mbar_expect_tx(&B.res_full[b], kResPiece);
+            tc05::tma_load_xy<1>(sm + b * kResPiece, &P.tm_r, T.n0 + c, T.mt * 128, smem_u32(&B.res_full[b]));
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0)
+        for (int g = f > kResBufs ? f - kResBufs : 0; g < f; g++)
+          tc_wait<false>(&B.res_full[g % kResBufs], (uint32_t)((g / kResBufs) & 1), P);
+      __syncwarp();
+    }
   } else {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3, grp = warp >> 2;  // TMEM lane quadrant; group: pieces grp, grp + 4, ...
     const int row = 32 * q + lane;            // the tile's weight row of this thread
     float *stg = reinterpret_cast<float *>(sm + grp * kPiece);
-    bool fine = true;
+    bool fine = true, res_ok = true;
+    int res_at = 0;  // pieces of residuals before the tile
     for (int lt = 0; lt < my_tiles; lt++) {
       const Tile T = next_tile();
-      const int b = lt & 1, nbase = T.mt * rows;
+      const int b = P.two ? 0 : lt & 1, use = P.two ? lt : lt >> 1, nbase = T.mt * rows;
       const bool rows4 = P.wide && nbase + rows <= P.n;
       Outputs<FORM == kWeights ? 4 : 2> O;  // the first piece's residuals, and later the next one's
       if (FORM == kWeights && T.mt < P.nmt && 16 * grp < T.nlen) O.fetch(P, T.n0 + 16 * grp, min(16, T.nlen - 16 * grp), nbase, q, 4, rows4);
-      // tokens on the M side: the residuals of this lane's runs of 16 columns
-      // (four of them in bf16, the first two in fp32) on their way meanwhile
-      uint32_t res[32];
-      const int r = T.mt * 128 + row;
-      const bool live = r < P.t;
-      if (TOK && P.res && P.wide8 && live) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int c0 = 16 * (grp + 4 * i), col = T.n0 + c0;
-          if (c0 < cols && col + 16 <= P.n) {
-            if (P.res_bf16) load_run<2>(static_cast<const uint16_t *>(P.res) + (int64_t)r * P.ldr + col, res + 8 * i);
-            else if (i < 2) load_run<4>(static_cast<const float *>(P.res) + (int64_t)r * P.ldr + col, res + 16 * i);
-          }
-        }
-      }
       // the warps stop together (they share named barriers)
       // (one waits for the MMAs, the others for it)
-      fine = tc05::named_and(5, 32 * kEpi, warp != 0 || tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)((lt >> 1) & 1), P));
+      fine = tc05::named_and(5, 32 * kEpi, res_ok && (warp != 0 || tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)(use & 1), P)));
       if (!fine) break;
       tc05::fence_after();
       const uint32_t tl = tmem + (uint32_t)(b * 256) + ((uint32_t)(32 * q) << 16);
+      auto read = [&](int at, float (&x)[16]) {  // 16 columns of the tile's sums
+        tc05::ld16(tl + at, x);
+        if (P.two) {
+          float y[16];
+          tc05::ld16(tl + 256 + at, y);
+#pragma unroll
+          for (int j = 0; j < 16; j++) x[j] += y[j];
+        }
+      };
       const int o = nbase + (P.gated ? row & 63 : row);
       const int brow = P.gated && row >= 64 ? P.n + o : o;
       auto release = [&] {  // the accumulator is read: the MMAs may fill it again
@@ -592,19 +631,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
         // a lane has a token, and its columns one after another: no exchange
         // (through shared memory, which copies and MMAs keep busy, the
         // product with silu took 208 us at 8192 x 8192 x 2048)
+        const int r = T.mt * 128 + row;
+        const bool live = r < P.t;
         const float rs = live && P.row_scale ? P.row_scale[r] : 1.f;
-        const int last = (min(cols, P.n - T.n0) + 15) / 16;
+        const int end = min(cols, P.n - T.n0), last = (end + 15) / 16;
+        const int pieces = P.res ? (P.res_bf16 ? (end + 63) / 64 : (end + 31) / 32) : 0;
         if (grp >= last) release();
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; i++) {
           const int c0 = 16 * (grp + 4 * i), col = T.n0 + c0, n = min(16, P.n - col);
-          if (c0 >= cols || n <= 0) break;
-          const bool run = P.wide8 && n == 16;
+          const bool here = c0 < end;
           float v[16], u[16];
-          tc05::ld16(tl + c0, v);
-          if (P.gated) tc05::ld16(tl + cols + c0, u);
-          if (grp + 4 * (i + 1) >= last) release();
-          if (live) {
+          if (here) {
+            read(c0, v);
+            if (P.gated) read(cols + c0, u);
+            if (grp + 4 * (i + 1) >= last) release();
+          }
+          // the residuals' pieces in turn, those of other groups too: a warp
+          // that skips a phase of a barrier cannot tell the next from the one
+          // before the last
+          uint32_t res[16];
+          for (int p = P.res_bf16 ? i : 2 * i; p < pieces && p <= (P.res_bf16 ? i : 2 * i + 1); p++) {
+            const int s = res_at + p, rb = s % kResBufs;
+            if (res_ok) res_ok = tc_warp_wait<false>(&B.res_full[rb], (uint32_t)((s / kResBufs) & 1), P);
+            if (here && (P.res_bf16 || p == 2 * i + (grp >> 1))) {
+              const uint8_t *line = sm + rb * kResPiece + row * 128;
+              const int first = P.res_bf16 ? 2 * grp : 4 * (grp & 1);  // 16-byte chunk, at its place ^ (row & 7)
+#pragma unroll
+              for (int j = 0; j < 4; j++)
+                if (j < 2 || !P.res_bf16) {
+                  const uint4 x = *reinterpret_cast<const uint4 *>(line + (((first + j) ^ (row & 7)) << 4));
+                  res[4 * j] = x.x, res[4 * j + 1] = x.y, res[4 * j + 2] = x.z, res[4 * j + 3] = x.w;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc05::mbar_arrive(&B.res_empty[rb]);
+          }
+          if (here && live) {
             if (P.bias) add_bias(v, P.bias + col, n);
             activate_all(v, P.act);
             if (P.gated) {
@@ -612,20 +675,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
 #pragma unroll
               for (int j = 0; j < 16; j++) v[j] *= u[j];
             }
-            if (run) {
 #pragma unroll
-              for (int j = 0; j < 16; j++) v[j] *= rs;
-              if (P.res) {
-                if (P.res_bf16) {
+            for (int j = 0; j < 16; j++) v[j] *= rs;
+            if (P.res) {
 #pragma unroll
-                  for (int j = 0; j < 16; j++) v[j] += (j & 1) ? bf16hi(res[8 * i + j / 2]) : bf16lo(res[8 * i + j / 2]);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 16; j++) v[j] += __uint_as_float(res[16 * (i & 1) + j]);
-                  if (i < 2 && c0 + 128 < cols && col + 144 <= P.n)
-                    load_run<4>(static_cast<const float *>(P.res) + (int64_t)r * P.ldr + col + 128, res + 16 * i);
-                }
-              }
+              for (int j = 0; j < 16; j++)
+                v[j] += P.res_bf16 ? ((j & 1) ? bf16hi(res[j / 2]) : bf16lo(res[j / 2])) : __uint_as_float(res[j]);
+            }
+            if (n == 16) {
               uint32_t o[16];
               if (P.out_bf16) {
 #pragma unroll
@@ -639,11 +696,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
             } else {
 #pragma unroll
               for (int j = 0; j < 16; j++)
-                if (j < n) finish1(P, r, col + j, v[j], rs);
+                if (j < n) store1(P, r, col + j, v[j]);
             }
           }
           __syncwarp();
         }
+        res_at += pieces;
       } else if constexpr (SPLIT) {
         // all of the accumulator to this CTA's shared memory, [token][128]
         // (the ring: every copy has landed and every MMA has read its operands)
@@ -661,7 +719,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
         for (int c = grp; c < last; c += kEpi / 4) {
           const int c0 = 16 * c, n = min(16, T.nlen - c0), c1 = c0 + 4 * kEpi;
           float v[16];
-          tc05::ld16(tl + c0, v);
+          read(c0, v);
           if (c + kEpi / 4 >= last) release();
 #pragma unroll
           for (int j = 0; j < 16; j++) stg[j * 128 + row] = v[j] + bias;
@@ -744,11 +802,11 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 rows of k values, ld apart: boxes of 64 values x box_rows, 128B swizzle, zeros outside
-bool make_map16(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uint64_t ld, uint32_t box_rows) {
-  const cuuint64_t dims[2] = {k, rows}, strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {64, box_rows}, estr[2] = {1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+// rows of k values (bf16 or fp32), ld apart: boxes of 128 bytes x box_rows, 128B swizzle, zeros outside
+bool make_map16(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uint64_t ld, uint32_t box_rows, bool f32 = false) {
+  const cuuint64_t dims[2] = {k, rows}, strides[1] = {ld * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, box_rows}, estr[2] = {1, 1};
+  return encode_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -774,7 +832,8 @@ cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int box_a = FORM == kTokens ? 128 : nrows, box_b = FORM == kTokens ? (p.gated ? p.w / 2 : nrows) : (p.gated ? 64 : 128);
   if (encode_fn() == nullptr || !make_map16(&p.tm_b, p.b, p.k, (uint64_t)p.n * (p.gated ? 2 : 1), p.ldb, (uint32_t)box_b) ||
-      !make_map16(&p.tm_a, p.a, p.k, p.t, p.lda, (uint32_t)box_a))
+      !make_map16(&p.tm_a, p.a, p.k, p.t, p.lda, (uint32_t)box_a) ||
+      (FORM == kTokens && p.res && !make_map16(&p.tm_r, p.res, p.n, p.t, p.ldr, 128, !p.res_bf16)))
     return cudaErrorNotSupported;
   const int smem = kOffRing + p.stages * p.stage + 1024;
   const int64_t tiles = (int64_t)p.ntt * ((p.nmt + CG - 1) / CG);
@@ -840,6 +899,10 @@ cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st) {
       return launch_tc<1, kSplit>(p, n_sms, st);
     }
   }
+  // fp32 results of long sums: the two halves of k in an accumulator each, as
+  // the tensor cores cut off what lies below 2^-23 of a sum at every step
+  // (1024 x 1024 x 8192: 1.1e-6 of the result in one sum)
+  p.two = !p.out_bf16 && p.k > 4096;
   // The tile width with the least (rounds of tiles) x (width + what a tile
   // costs whatever its width), with the weights or the tokens on the M side.
   int64_t best = INT64_MAX;
@@ -854,7 +917,7 @@ cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st) {
     }
   };
   const int tok_tiles = (p.t + 127) / 128;
-  const bool can = p.wide8 && !p.res;
+  const bool can = p.wide8;
   if (can) look(true, tok_tiles, p.n, p.gated ? 1 : 2);
   look(false, p.nmt, p.t, 2);
   if (tokens) {

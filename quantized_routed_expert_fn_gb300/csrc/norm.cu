@@ -125,7 +125,10 @@ __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP 
     ss = row_sum(ss, P.T, red + 32, large);
     eps = eps * c * c;
   }
-  const float inv = rsqrtf(fmaf(ss, P.inv_h, eps));
+  const float m = fmaf(ss, P.inv_h, eps), r = rsqrtf(m);
+  // one step of Newton's: the root's error is the last bit's (e4m3 values
+  // next to a border are told apart as by a division)
+  const float inv = m < 1e38f ? fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r) : r;
   x *= inv;
 #pragma unroll
   for (int i = 0; i < NV; i++) v[i] *= inv;

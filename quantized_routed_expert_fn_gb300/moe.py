@@ -401,11 +401,6 @@ def _ld(t, rows: int, cols: int) -> int:
     return t.stride(0) if rows > 1 else cols
 
 
-def _ld16(t, rows: int, cols: int) -> int:
-    """The same for rows that start on 16 bytes."""
-    return t.stride(0) if rows > 1 else -(-cols // 8) * 8
-
-
 @functools.lru_cache(maxsize=64)
 def _gate_cfg(n_experts, top_k, score, n_groups, top_groups, group_top, flags, scale) -> MoeGateCfg:
     if score not in SCORES:
@@ -523,26 +518,49 @@ def experts8(layer: Layer8, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: tor
 
 # ---- around the experts' step: norms, products with an epilogue, log probabilities
 
-def _norm_out(out, scales, t: int, h: int, dev: int) -> tuple:
-    """(out, its type, its row stride, scales, their row stride) of a norm."""
-    if scales is None:
-        return _arg(out, "out", (t, h), _FLOATS, dev), _FLOATS[out.dtype], _ld(out, t, h), None, 0
-    sc = -(-h // 128)
-    return (_arg(out, "out", (t, h), _E4M3, dev), E4M3, _ld(out, t, h), _arg(scales, "scales", (t, sc), _E8M0, dev),
-            _ld(scales, t, sc))
+def _mat(t, name: str, shape, dtypes, dev: int) -> tuple:
+    """(address, row stride) of a CUDA matrix after checking type, shape, device and that its rows are contiguous."""
+    if t.dtype not in dtypes:
+        _bad(EINVAL, f"{name} is {t.dtype}")
+    if t.shape != shape:
+        _bad(ESHAPE, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        _bad(EINVAL, f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        _bad(EINVAL, f"{name}'s last dimension is not contiguous")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _matrix(t, name: str) -> tuple:
+    """Shape of a call's first matrix, and the call's device."""
+    shape = t.shape
+    if len(shape) != 2:
+        _bad(ESHAPE, f"{name} is a matrix")
+    return shape, _device(t, name)
+
+
+def _vector(t, name: str, n: int, dev: int):
+    return None if t is None else _whole(t, name, (n,), _F32, dev)
 
 
 def norm(x: torch.Tensor, out: torch.Tensor, w=None, eps: float = 1e-6, scales=None, stream=None) -> None:
     """moe_norm: x float32 / bfloat16 [t][h] -> out = x / sqrt(mean(x^2) + eps) * w in float32 / bfloat16, or with
     scales (E8M0 [t][ceil(h / 128)]) in e4m3 as quant8 gives it; w float32 [h]; row strides as they are."""
-    if x.dim() != 2:
-        _bad(ESHAPE, "x is a matrix")
-    t, h = x.shape
-    dev = _device(x, "x")
-    xp = _arg(x, "x", (t, h), _FLOATS, dev)
-    wp = None if w is None else _whole(w, "w", (h,), _F32, dev)
-    _check((_lib or lib()).moe_norm(xp, _FLOATS[x.dtype], _ld(x, t, h), wp, eps, t, h, *_norm_out(out, scales, t, h, dev),
-                                    _stream_on(stream, dev)))
+    shape, dev = _matrix(x, "x")
+    t, h = shape
+    xp, ldx = _mat(x, "x", shape, _FLOATS, dev)
+    if scales is None:
+        op, ldo = _mat(out, "out", shape, _FLOATS, dev)
+        kind, sp, lds = _FLOATS[out.dtype], None, 0
+    else:
+        op, ldo = _mat(out, "out", shape, _E4M3, dev)
+        kind = E4M3
+        sp, lds = _mat(scales, "scales", (t, -(-h // 128)), _E8M0, dev)
+    _check((_lib or lib()).moe_norm(xp, _FLOATS[x.dtype], ldx, None if w is None else _whole(w, "w", (h,), _F32, dev), eps, t, h,
+                                    op, kind, ldo, sp, lds, _stream_on(stream, dev)))
 
 
 def add_norm(y: torch.Tensor, residual: torch.Tensor, res_out: torch.Tensor, post: bool = False, w_post=None, gate=None,
@@ -551,28 +569,34 @@ def add_norm(y: torch.Tensor, residual: torch.Tensor, res_out: torch.Tensor, pos
     """moe_add_norm: res_out = res_scale * residual + scale * gate * v, v = y or (post) its norm with w_post; with out,
     out = the norm of that sum with w, as norm gives it.  y, residual, res_out float32 / bfloat16 [t][h] (res_out may be
     residual or y); gate float32 / bfloat16 [t or 1][h or 1], with gate_sigmoid through a sigmoid."""
-    if y.dim() != 2:
-        _bad(ESHAPE, "y is a matrix")
-    t, h = y.shape
-    dev = _device(y, "y")
-    yp = _arg(y, "y", (t, h), _FLOATS, dev)
-    rp = _arg(residual, "residual", (t, h), _FLOATS, dev)
-    op = _arg(res_out, "res_out", (t, h), _FLOATS, dev)
-    cfg = MoeAddNormCfg((NORM_POST if post else 0) | (NORM_GATE_SIGMOID if gate_sigmoid else 0), eps, scale, res_scale,
-                        None if w_post is None else _whole(w_post, "w_post", (h,), _F32, dev),
-                        None if w is None else _whole(w, "w", (h,), _F32, dev))
+    shape, dev = _matrix(y, "y")
+    t, h = shape
+    yp, ldy = _mat(y, "y", shape, _FLOATS, dev)
+    rp, ldr = _mat(residual, "residual", shape, _FLOATS, dev)
+    ap, lda = _mat(res_out, "res_out", shape, _FLOATS, dev)
+    gp, ldg, gd, gc = None, 0, F32, 1
     if gate is not None:
-        if gate.dim() != 2 or gate.shape[0] not in (1, t) or gate.shape[1] not in (1, h):
-            _bad(ESHAPE, f"gate has shape {tuple(gate.shape)}, expected [{t} or 1][{h} or 1]")
-        cfg.gate = _arg(gate, "gate", gate.shape, _FLOATS, dev)
-        cfg.gate_dtype, cfg.gate_cols = _FLOATS[gate.dtype], gate.shape[1]
-        cfg.ldg = gate.stride(0) if gate.shape[0] > 1 else 0
-    if out is None and scales is not None:
+        gs = gate.shape
+        if len(gs) != 2 or gs[0] not in (1, t) or gs[1] not in (1, h):
+            _bad(ESHAPE, f"gate has shape {tuple(gs)}, expected [{t} or 1][{h} or 1]")
+        gp, ldg = _mat(gate, "gate", gs, _FLOATS, dev)
+        gd, gc = _FLOATS[gate.dtype], gs[1]
+        if gs[0] == 1:
+            ldg = 0
+    op, kind, ldo, sp, lds = None, F32, h, None, 0
+    if out is not None and scales is None:
+        op, ldo = _mat(out, "out", shape, _FLOATS, dev)
+        kind = _FLOATS[out.dtype]
+    elif out is not None:
+        op, ldo = _mat(out, "out", shape, _E4M3, dev)
+        kind = E4M3
+        sp, lds = _mat(scales, "scales", (t, -(-h // 128)), _E8M0, dev)
+    elif scales is not None:
         _bad(EINVAL, "scales without out")
-    to = (None, F32, h, None, 0) if out is None else _norm_out(out, scales, t, h, dev)
-    _check((_lib or lib()).moe_add_norm(cfg, yp, _FLOATS[y.dtype], _ld(y, t, h), rp, _FLOATS[residual.dtype],
-                                        _ld(residual, t, h), op, _FLOATS[res_out.dtype], _ld(res_out, t, h), t, h, *to,
-                                        _stream_on(stream, dev)))
+    cfg = MoeAddNormCfg((NORM_POST if post else 0) | (NORM_GATE_SIGMOID if gate_sigmoid else 0), eps, scale, res_scale,
+                        _vector(w_post, "w_post", h, dev), _vector(w, "w", h, dev), gp, ldg, gd, gc)
+    _check((_lib or lib()).moe_add_norm(cfg, yp, _FLOATS[y.dtype], ldy, rp, _FLOATS[residual.dtype], ldr, ap,
+                                        _FLOATS[res_out.dtype], lda, t, h, op, kind, ldo, sp, lds, _stream_on(stream, dev)))
 
 
 _BF16 = (torch.bfloat16,)
@@ -583,53 +607,57 @@ def mm16(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, status: torch.Tens
     """moe_mm16: z = a b^T + bias of a bfloat16 [t][k], b bfloat16 [n][k] (gated: [2n][k], the gate's rows first; rows of
     both start on 16 bytes) -> out float32 / bfloat16 [t][n] = row_scale * act(z) + residual, gated row_scale * act(z[:, :n])
     * z[:, n:] + residual; bias float32 [n] ([2n]), row_scale float32 [t], residual float32 / bfloat16 [t][n] (out may be it)."""
-    if a.dim() != 2 or b.dim() != 2:
-        _bad(ESHAPE, "a and b are matrices")
-    t, k = a.shape
-    rows = b.shape[0]
+    shape, dev = _matrix(a, "a")
+    t, k = shape
+    bs = b.shape
+    if len(bs) != 2 or bs[1] != k or (gated and bs[0] % 2):
+        _bad(ESHAPE, f"b has shape {tuple(bs)}, expected [n][{k}], gated [2n][{k}]")
+    rows = bs[0]
     n = rows // 2 if gated else rows
-    dev = _device(a, "a")
-    ap = _arg(a, "a", (t, k), _BF16, dev)
-    bp = _arg(b, "b", (2 * n if gated else n, k), _BF16, dev)
-    op = _arg(out, "out", (t, n), _FLOATS, dev)
+    ap, lda = _mat(a, "a", shape, _BF16, dev)
+    bp, ldb = _mat(b, "b", bs, _BF16, dev)
+    op, ldo = _mat(out, "out", (t, n), _FLOATS, dev)
+    if k % 8:  # a single row's stride means nothing
+        lda, ldb = lda if t > 1 else -(-k // 8) * 8, ldb if rows > 1 else -(-k // 8) * 8
     epi = None
     if act != "none" or bias is not None or row_scale is not None or residual is not None:
         if act not in ACTS:
             _bad(EINVAL, f"unknown act {act!r}")
-        epi = MoeEpilogue(ACTS[act], F32, None if bias is None else _whole(bias, "bias", (rows,), _F32, dev),
-                          None if row_scale is None else _whole(row_scale, "row_scale", (t,), _F32, dev))
+        rp, rd, ldr = None, F32, n
         if residual is not None:
-            epi.residual = _arg(residual, "residual", (t, n), _FLOATS, dev)
-            epi.res_dtype, epi.ldr = _FLOATS[residual.dtype], _ld(residual, t, n)
-    _check((_lib or lib()).moe_mm16(ap, _ld16(a, t, k), t, bp, _ld16(b, rows, k), n, k, epi, op, _FLOATS[out.dtype],
-                                    _ld(out, t, n), flags | MM16_GATED if gated else flags,
-                                    _whole(status, "status", (1,), _I32, dev), _stream_on(stream, dev)))
+            rp, ldr = _mat(residual, "residual", (t, n), _FLOATS, dev)
+            rd = _FLOATS[residual.dtype]
+        epi = MoeEpilogue(ACTS[act], rd, _vector(bias, "bias", rows, dev), _vector(row_scale, "row_scale", t, dev), rp, ldr)
+    _check((_lib or lib()).moe_mm16(ap, lda, t, bp, ldb, n, k, epi, op, _FLOATS[out.dtype], ldo,
+                                    flags | MM16_GATED if gated else flags, _whole(status, "status", (1,), _I32, dev),
+                                    _stream_on(stream, dev)))
 
 
 def logprobs(logits: torch.Tensor, tokens=None, logp=None, entropy=None, top_idx=None, top_logp=None, scale: float = 1.0,
              stream=None) -> None:
     """moe_logprobs: logits float32 / bfloat16 [t][v] (any row stride), p = softmax(scale * logits) -> logp float32 [t][m]
     of tokens int32 [t][m], entropy float32 [t], top_idx int32 and top_logp float32 [t][k]; any of the three."""
-    if logits.dim() != 2 or (tokens is None) != (logp is None) or (top_idx is None) != (top_logp is None):
-        _bad(ESHAPE, "logits is a matrix; tokens and logp, top_idx and top_logp go together")
-    t, v = logits.shape
-    dev = _device(logits, "logits")
-    lp = _arg(logits, "logits", (t, v), _FLOATS, dev)
+    shape, dev = _matrix(logits, "logits")
+    t, v = shape
+    lp, ld = _mat(logits, "logits", shape, _FLOATS, dev)
+    if (tokens is None) != (logp is None) or (top_idx is None) != (top_logp is None):
+        _bad(EINVAL, "tokens and logp, top_idx and top_logp go together")
     m = k = 0
     tp = op = ip = xp = None
     if tokens is not None:
-        if tokens.dim() != 2 or not tokens.shape[1]:
-            _bad(ESHAPE, "tokens is [t][m]")
-        m = tokens.shape[1]
-        tp, op = _whole(tokens, "tokens", (t, m), _I32, dev), _whole(logp, "logp", (t, m), _F32, dev)
+        ts = tokens.shape
+        if len(ts) != 2 or ts[0] != t or not ts[1]:
+            _bad(ESHAPE, f"tokens has shape {tuple(ts)}, expected [{t}][m]")
+        m = ts[1]
+        tp, op = _whole(tokens, "tokens", ts, _I32, dev), _whole(logp, "logp", ts, _F32, dev)
     if top_idx is not None:
-        if top_idx.dim() != 2 or not top_idx.shape[1]:
-            _bad(ESHAPE, "top_idx is [t][k]")
-        k = top_idx.shape[1]
-        ip, xp = _whole(top_idx, "top_idx", (t, k), _I32, dev), _whole(top_logp, "top_logp", (t, k), _F32, dev)
-    ep = None if entropy is None else _whole(entropy, "entropy", (t,), _F32, dev)
-    _check((_lib or lib()).moe_logprobs(lp, _FLOATS[logits.dtype], _ld(logits, t, v), t, v, scale, tp, m, op, ep, ip, xp, k,
-                                        _stream_on(stream, dev)))
+        ks = top_idx.shape
+        if len(ks) != 2 or ks[0] != t or not ks[1]:
+            _bad(ESHAPE, f"top_idx has shape {tuple(ks)}, expected [{t}][k]")
+        k = ks[1]
+        ip, xp = _whole(top_idx, "top_idx", ks, _I32, dev), _whole(top_logp, "top_logp", ks, _F32, dev)
+    _check((_lib or lib()).moe_logprobs(lp, _FLOATS[logits.dtype], ld, t, v, scale, tp, m, op, _vector(entropy, "entropy", t, dev), ip,
+                                        xp, k, _stream_on(stream, dev)))
 
 
 class Tier:

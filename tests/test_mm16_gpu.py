@@ -81,6 +81,32 @@ EPI = [dict(), dict(act="silu", gated=True), dict(act="gelu", bias=True, res="bf
        dict(act="sigmoid", scale=True, res="f32"), dict(bias=True, scale=True, res="bf16", gated=True), dict(act="relu", res="f32")]
 
 
+@pytest.mark.parametrize("res", [None, "f32", "bf16"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("t,n,k", [(2300, 1296, 136), (1300, 2000, 64), (3100, 784, 72), (260, 5008, 40), (700, 1200, 5000), (300, 4000, 8200),
+                                   (20000, 48, 64), (9000, 160, 200), (333, 1008, 4160)], ids=lambda v: str(v))
+def test_large_tiles_are_exact(moe, t, n, k, gated, kind, res):
+    """Several tiles a block, whole rows, residuals by pieces, k in two halves: exact products of whole numbers, on the GPU."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(t + n)
+    whole = lambda *s: torch.randint(-2, 3, s, device="cuda", generator=g).float()  # noqa: E731
+    a, b = whole(t, k), whole(2 * n if gated else n, k)
+    r = None if res is None else whole(t, n).to(TYPES[res])
+    bias, scale = whole(b.shape[0]), whole(t)
+    z = a @ b.T + bias  # sums below 2^24: exact
+    ref = torch.relu(z[:, :n]).double() * (z[:, n:] if gated else 1) * scale[:, None] + (0 if r is None else r)
+    out = run(moe, a.bfloat16(), b.bfloat16(), kind, res=r, act="relu", gated=gated, bias=bias, row_scale=scale)
+    if kind == "f32":
+        fine = ref.abs() < 2 ** 24  # (products of the two halves may be larger: rounded once or twice)
+        assert torch.equal(out.double()[fine], ref[fine])
+        assert ((out.double() - ref).abs() <= ref.abs() * 2.0 ** -23).all()
+    else:
+        assert ((out.double() - ref).abs() <= ref.abs() * (2.0 ** -8 + 2.0 ** -22)).all()
+        small = ref.abs() <= 256
+        assert torch.equal(out.double()[small], ref[small])
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("t,n,k", [(1, 96, 256), (7, 513, 2048), (20, 200, 520), (150, 264, 1024), (300, 1001, 200), (1100, 640, 96)],
                          ids=lambda v: str(v))
