@@ -157,8 +157,8 @@ __device__ __forceinline__ float gate_of(const NormP &P, float g) { return P.gat
 template <int V, int NV, bool SH>
 struct Place {
   int T, l, h, lead, xc;  // xc: its column, < 0: none
-  __device__ __forceinline__ Place(const NormP &P, int64_t row) {
-    T = P.T, l = T >= (int)blockDim.x ? (int)threadIdx.x : (int)threadIdx.x & (T - 1);
+  __device__ __forceinline__ Place(const NormP &P, int64_t row, int thread) {
+    T = P.T, l = T >= (int)blockDim.x ? thread : thread & (T - 1);
     h = row < P.t ? P.h : 0, lead = SH ? (int)(-((row & 7) * P.ld8) & 7) : 0, xc = -1;
     if (SH && l < 8 && l < lead) xc = l;
     if (SH && l >= 8 && l < 16) xc = h - (h - lead) % 8 + l - 8;
@@ -173,34 +173,48 @@ struct Place {
   }
 };
 
-// Several rows' values on their way to shared memory (RING): each thread
-// copies what it will hold itself, so that its own wait is all it needs.
+// The next rows' values on their way to shared memory (RING), copied by the
+// warp that will hold them, 16 bytes a lane, neighbouring lanes neighbouring
+// bytes: of bf16 a thread copies its own pieces, of fp32 the first 16 lanes'
+// pieces are a copy of the whole warp's and the others' the next (each lane
+// its own two halves: every 32 bytes asked for twice, 310 us instead of 184 at
+// 32768 x 2048).
 constexpr int kRing = 2;  // (3: fewer blocks fit; 30011 x 4090 254 us instead of 214)
 constexpr int kMaxRing = 200 * 1024;
 struct Ring {
-  uint8_t *y, *res;  // this thread's first 16 bytes of the first row's; others blockDim apart
+  uint8_t *y, *res;  // a place is [pieces][blockDim][values of a piece]
 };
 // bytes of a thread's row of NV values
 __host__ __device__ constexpr int ring_row(int nv, int bf16) { return nv * (bf16 ? 2 : 4); }
 
-// The row's copies, into the ring's place `at`; no row: none.
+// The copies of the rows first + (thread / T), into the ring's place `at`.
 template <int V, int NV, bool ADD, bool SH>
-__device__ __forceinline__ void row_copies(const NormP &P, int64_t row, const Ring &ring, int at) {
-  const Place<V, NV, SH> L(P, row);
-  auto copy = [&](const void *p, int bf16, int64_t first, uint8_t *to) {
+__device__ __forceinline__ void row_copies(const NormP &P, int64_t first, const Ring &ring, int at) {
+  const int lane = threadIdx.x & 31;
+  auto row_of = [&](int thread) { return first + (P.T >= (int)blockDim.x ? 0 : thread / P.T); };
+  auto copy = [&](const void *p, int bf16, int64_t ld, uint8_t *to) {
     to += (size_t)at * ring_row(NV, bf16) * blockDim.x;
-    L.pieces([&](int j) {
-      const uint8_t *from = static_cast<const uint8_t *>(p) + (first + L.col(j)) * (bf16 ? 2 : 4);
-      if (bf16) {
-        cp_async16(to + (size_t)j * 16 * blockDim.x, from);
-      } else {
-        cp_async16(to + (size_t)(2 * j) * 16 * blockDim.x, from);
-        cp_async16(to + (size_t)(2 * j + 1) * 16 * blockDim.x, from + 16);
+    if (bf16) {
+      const int64_t row = row_of(threadIdx.x);
+      const Place<V, NV, SH> L(P, row, threadIdx.x);
+      L.pieces([&](int j) {
+        cp_async16(to + ((size_t)j * blockDim.x + threadIdx.x) * 16, static_cast<const uint16_t *>(p) + row * ld + L.col(j));
+      });
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const int thread = (int)threadIdx.x - lane + 16 * c + (lane >> 1);
+        const int64_t row = row_of(thread);
+        const Place<V, NV, SH> L(P, row, thread);
+        L.pieces([&](int j) {
+          cp_async16(to + ((size_t)j * blockDim.x + thread) * 32 + 16 * (lane & 1),
+                     static_cast<const float *>(p) + row * ld + L.col(j) + 4 * (lane & 1));
+        });
       }
-    });
+    }
   };
-  copy(P.y, P.y_bf16, row * P.ldy, ring.y);
-  if constexpr (ADD) copy(P.res, P.res_bf16, row * P.ldr, ring.res);
+  copy(P.y, P.y_bf16, P.ldy, ring.y);
+  if constexpr (ADD) copy(P.res, P.res_bf16, P.ldr, ring.res);
 }
 
 // One row, in the registers of T threads (all of a warp's, or a block's, come
@@ -210,7 +224,7 @@ template <int V, int NV, bool ADD, bool SH, bool RING>
 __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red)[4][32], const Vecs &vecs, uint32_t *s_max,
                                         const Ring &ring = Ring(), int at_ring = 0, float x0 = 0.f, float r0 = 0.f) {
   constexpr int N = NV / V;
-  const Place<V, NV, SH> L(P, row);
+  const Place<V, NV, SH> L(P, row, threadIdx.x);
   const int T = L.T, l = L.l, h = L.h, xc = L.xc;
   const bool live = row < P.t;
   auto col = [&](int j) { return L.col(j); };
@@ -218,15 +232,8 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
   auto load = [&](const void *p, int bf16, int64_t at, float *to, float &x, const uint8_t *from, float value) {
     if constexpr (RING) {
       from += (size_t)at_ring * ring_row(NV, bf16) * blockDim.x;
-      const size_t step = 16 * blockDim.x;
-      if (bf16)
-        pieces([&](int j) { load_as<8, true>(from + j * step, 0, to + j * 8); });
-      else
-        pieces([&](int j) {
-          const float4 a = *reinterpret_cast<const float4 *>(from + 2 * j * step), b = *reinterpret_cast<const float4 *>(from + (2 * j + 1) * step);
-          float *v = to + j * 8;
-          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        });
+      if (bf16) pieces([&](int j) { load_as<8, true>(from + ((size_t)j * blockDim.x + threadIdx.x) * 16, 0, to + j * 8); });
+      else pieces([&](int j) { load_as<8, false>(from + ((size_t)j * blockDim.x + threadIdx.x) * 32, 0, to + j * 8); });
       x = value;
       return;
     }
@@ -310,14 +317,38 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
   if constexpr (SH) return;  // (not launched so)
   uint8_t *q = static_cast<uint8_t *>(P.out) + row * P.ldo, *s = P.s + row * P.lds;
   if constexpr (V == 8) {
-    // 16 lanes hold a scale block
+    // 16 lanes hold a scale block.  All pieces' maxima together, as each is a
+    // chain of exchanges (one piece after the other: 65536 x 2048 111 us
+    // instead of 103).  NaN does not count in them and stays one in the
+    // conversion; an infinity makes the warp do it with care.
+    float a[N], am = 0.f;
 #pragma unroll
     for (int j = 0; j < N; j++) {
+      a[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; i++) a[j] = fmaxf(a[j], fabsf(v[j * 8 + i]));
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < N; j++) a[j] = fmaxf(a[j], __shfl_xor_sync(FULLM, a[j], o));
+#pragma unroll
+    for (int j = 0; j < N; j++) am = fmaxf(am, a[j]);
+    const bool care = __any_sync(FULLM, !(am <= 3.402823466e38f));
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      uint32_t w[2], e;
       float b[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) b[i] = v[j * 8 + i];
-      uint32_t w[2], e;
-      quant_block<8>(b, w, e);
+      if (care) {
+        quant_block<8>(b, w, e);
+      } else {
+        e = e8m0_of_amax(__float_as_uint(a[j]));
+        const float f = e8m0_inv(e);
+        w[0] = e4m3x4<false>(b[0] * f, b[1] * f, b[2] * f, b[3] * f);
+        w[1] = e4m3x4<false>(b[4] * f, b[5] * f, b[6] * f, b[7] * f);
+      }
       if (col(j) < h) {
         *reinterpret_cast<uint2 *>(q + col(j)) = make_uint2(w[0], w[1]);
         if ((l & 15) == 0) s[col(j) >> 7] = (uint8_t)e;
@@ -375,7 +406,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV <= 16 ? 2 : 0) norm_rows(const
   // the value more of a row, a row ahead
   auto more = [&](int64_t row) {
     if constexpr (SH && RING) {
-      const Place<V, NV, SH> L(P, row);
+      const Place<V, NV, SH> L(P, row, threadIdx.x);
       if (L.xc >= 0) {
         x = load1(P.y, P.y_bf16, row * P.ldy + L.xc);
         if constexpr (ADD) rx = load1(P.res, P.res_bf16, row * P.ldr + L.xc);
@@ -385,22 +416,22 @@ __global__ void __launch_bounds__(kMaxThreads, NV <= 16 ? 2 : 0) norm_rows(const
     }
   };
   if constexpr (RING) {
-    ring.y = at + 16 * threadIdx.x;
+    ring.y = at;
     at += (size_t)kRing * ring_row(NV, P.y_bf16) * blockDim.x;
     if (ADD) {
-      ring.res = at + 16 * threadIdx.x;
+      ring.res = at;
       at += (size_t)kRing * ring_row(NV, P.res_bf16) * blockDim.x;
     }
 #pragma unroll
     for (int i = 0; i < kRing - 1; i++) {
-      row_copies<V, NV, ADD, SH>(P, first + i * step + mine, ring, i);
+      row_copies<V, NV, ADD, SH>(P, first + i * step, ring, i);
       tc05::cp_commit();
     }
     more(first + mine);
   }
   Vecs vecs = {};
   if constexpr (SH) {
-    Place<V, NV, SH> L(P, first + mine < P.t ? first + mine : 0);
+    Place<V, NV, SH> L(P, first + mine < P.t ? first + mine : 0, threadIdx.x);
     auto place = [&](auto get, float &xv) {
       float4 *to = reinterpret_cast<float4 *>(at) + threadIdx.x;
       L.pieces([&](int j) {
@@ -420,11 +451,13 @@ __global__ void __launch_bounds__(kMaxThreads, NV <= 16 ? 2 : 0) norm_rows(const
   int half = 0, slot = 0;  // the next row's sums lie in the other half
   for (; first < P.t; first += step, half ^= 1) {
     if constexpr (RING) {
-      row_copies<V, NV, ADD, SH>(P, first + (kRing - 1) * step + mine, ring, slot ? slot - 1 : kRing - 1);
+      __syncwarp();  // the place's values are read
+      row_copies<V, NV, ADD, SH>(P, first + (kRing - 1) * step, ring, slot ? slot - 1 : kRing - 1);
       tc05::cp_commit();
       const float x0 = x, r0 = rx;
       more(first + step + mine);
       tc05::cp_wait_group<kRing - 1>();
+      __syncwarp();  // of all the warp's copies
       one_row<V, NV, ADD, SH, true>(P, first + mine, s_red[half], vecs, s_dyn, ring, slot, x0, r0);
       if (++slot == kRing) slot = 0;
     } else {
@@ -452,6 +485,17 @@ int piece(const NormP &p) {
   if (p.out_kind == kNormOutE4m3) need(p.out, p.ldo, 1, 8);
   else if (p.out_kind != kNormOutNone) need(p.out, p.ldo, p.out_kind == kNormOutBf16 ? 2 : 4, 16);
   return v;
+}
+
+// Whether the next rows' values are fetched ahead.  us without / with: add_norm
+// of bf16 on an fp32 stream 65536 x 2048 286 / 250, 8192 x 8192 181 / 143, on a
+// bf16 one 30000 x 4096 222 / 158, 30011 x 4090 243 / 216; all fp32 32768 x
+// 2048 160 / 184.  norm of bf16 65536 x 2048 93 / 86, 8192 x 16384 121 / 83,
+// 32816 x 4090 (SH) 109 / 116; fp32 32768 x 2048 79 / 88; to e4m3 65536 x 2048
+// 102 / 116 (instructions), 8192 x 16384 122 / 104.
+bool with_ring(const NormP &p, bool sh) {
+  if (!p.y_bf16) return false;
+  return p.res || (!sh && (p.out_kind != kNormOutE4m3 || p.h > 8192));
 }
 
 // vectors that SH holds in shared memory
@@ -485,11 +529,9 @@ int ring_bytes(const NormP &p, int nv, int block) {
   return kRing * block * (ring_row(nv, p.y_bf16) + (p.res ? ring_row(nv, p.res_bf16) : 0));
 }
 
-// Blocks that stay resident walk over the rows; where each has several, the
-// values are bf16 and shared memory allows, with the next rows on their way
-// (30000 rows x 4096 with a gate a channel: 225 -> 161 us; of fp32 values
-// enough are in flight without: 32768 x 2048 160 us without, 310 with).
-// done: launched.
+// Blocks that stay resident walk over the rows; where each has several and
+// shared memory allows, with the next row's values on their way.  done:
+// launched (without SH only in that case).
 template <int NV, bool SH>
 cudaError_t launch_walk(NormP p, int T, int n_sms, cudaStream_t st, bool &done) {
   p.T = T;
@@ -499,8 +541,7 @@ cudaError_t launch_walk(NormP p, int T, int n_sms, cudaStream_t st, bool &done) 
   static const int regs[4] = {SH ? registers(norm_rows<8, NV, false, SH, false>) : 128, SH ? registers(norm_rows<8, NV, true, SH, false>) : 128,
                               registers(norm_rows<8, NV, false, SH, true>), registers(norm_rows<8, NV, true, SH, true>)};
   if (vecs > kMaxVec) return cudaSuccess;
-  const bool small = p.y_bf16 && (!p.res || p.res_bf16);
-  for (int ring = small ? 1 : 0; ring >= (SH ? 0 : 1); ring--) {
+  for (int ring = with_ring(p, SH) ? 1 : 0; ring >= (SH ? 0 : 1); ring--) {
     const int smem = vecs + (ring ? ring_bytes(p, NV, block) : 0);
     if (smem > kMaxRing) continue;
     int fit = 65536 / (regs[2 * ring + (p.res != nullptr)] * block);
@@ -509,7 +550,7 @@ cudaError_t launch_walk(NormP p, int T, int n_sms, cudaStream_t st, bool &done) 
     int64_t cap = (int64_t)n_sms * (fit < 1 ? 1 : fit);
     if (SH && cap > 8) cap -= cap % 8;
     const int64_t rounds = (need + cap - 1) / cap;
-    if (ring && rounds < 2) continue;
+    if (ring && rounds < 6) continue;  // (4096 x 2048: 20 us without, 22 with)
     auto f = p.res ? norm_rows<8, NV, true, SH, true> : norm_rows<8, NV, false, SH, true>;
     if constexpr (SH)
       if (!ring) f = p.res ? norm_rows<8, NV, true, SH, false> : norm_rows<8, NV, false, SH, false>;
@@ -542,10 +583,9 @@ cudaError_t launch_form(NormP p, int T, cudaStream_t st) {
 // / 111, 32768 x 4096 113 / 104 / 97 / 110; one row x 2048 1.8 / 2.1 / 2.4 /
 // 3.1.  add_norm (fp32 residual): 65536 x 2048 305 / 286 / 297 / 324.
 template <class T>
-int values_a_thread(const NormP &p, int n_sms, T threads) {
+int values_a_thread(const NormP &p, int n_sms, bool sh, T threads) {
   int nv = 8;
-  const bool ahead = p.y_bf16 && (!p.res || p.res_bf16) && (p.out_kind != kNormOutE4m3 || p.h > 8192);
-  const int most = p.res || ahead ? 16 : 32;
+  const int most = p.res || with_ring(p, sh) ? 16 : 32;
   while (nv < most && threads(2 * nv) < threads(nv) && (int64_t)p.t * threads(2 * nv) >= (int64_t)n_sms * 64 * 32) nv *= 2;
   while (threads(nv) > kMaxThreads) nv *= 2;
   return nv;
@@ -563,7 +603,7 @@ int threads_for(int values, int nv, int least) {
 template <int V>
 cudaError_t launch_v(const NormP &p, int n_sms, cudaStream_t st) {
   auto threads = [&](int nv) { return threads_for(p.h, nv, p.out_kind == kNormOutE4m3 ? 128 / V : 4); };
-  const int nv = values_a_thread(p, n_sms, threads), T = threads(nv);
+  const int nv = values_a_thread(p, n_sms, false, threads), T = threads(nv);
   return nv == 8 ? launch_form<V, 8>(p, T, st) : (nv == 16 ? launch_form<V, 16>(p, T, st) :
          (nv == 32 ? launch_form<V, 32>(p, T, st) : launch_form<V, 64>(p, T, st)));
 }
@@ -575,7 +615,7 @@ cudaError_t launch_norm(NormP p, int n_sms, cudaStream_t st) {
   const bool sh = v < 8 && p.h >= 32 && alike(p);
   auto threads = [&](int nv) { return threads_for(p.h, nv, 16); };
   if (sh || (v == 8 && p.h >= 256)) {  // (shorter rows of whole pieces have fewer threads than a walk takes)
-    const int nv = values_a_thread(p, n_sms, threads), T = threads(nv);
+    const int nv = values_a_thread(p, n_sms, sh, threads), T = threads(nv);
     bool done = false;
     cudaError_t e = cudaSuccess;
     if (sh) e = nv == 8 ? launch_walk<8, true>(p, T, n_sms, st, done) : (nv == 16 ? launch_walk<16, true>(p, T, n_sms, st, done) :
