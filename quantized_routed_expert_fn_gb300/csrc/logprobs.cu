@@ -488,9 +488,16 @@ cudaError_t launch_t(const LogprobsP &p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st) {
-  // few rows: as many blocks a row as fill the SMs, of 4096 values or more
+  // Few rows: several blocks a row, of 16384 values or more while each has an
+  // SM, of 25000 when some SMs have two.  us with 1 / 2 / 4 / 8, fp32: 1 x
+  // 131072 18 / 12 / 9.4 / 7.9, 48 x 100003 14 / 11 / 10.2 / 12.2, 100 x 131072
+  // 16 / 14 / 14 / 18, 100 x 32000 7.7 / 8.3 / 9.6 / 15, 30 x 20000 6.8 / 7.3 / 7.2 / 7.3.
   p.S = 1;
-  while (p.S < kMaxS && (int64_t)p.t * p.S * 2 <= 2 * n_sms && p.v / (p.S * 2) >= 4096) p.S *= 2;
+  while (p.S < kMaxS) {
+    const int64_t blocks = (int64_t)p.t * p.S * 2, values = p.v / (p.S * 2);
+    if (!(blocks <= n_sms ? values >= 16384 : (blocks <= n_sms * 4 / 3 && values >= 25000))) break;
+    p.S *= 2;
+  }
   p.seg = ((p.v + p.S - 1) / p.S + 7) / 8 * 8;
   // Threads of a block: what it does once a row (orders, exchanges) costs as
   // much as some values of each thread.  us, 16384 rows, top 5, fp32, with 32 /
