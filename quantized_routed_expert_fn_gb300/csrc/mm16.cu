@@ -287,17 +287,16 @@ __device__ __forceinline__ void store_run(void *p, const uint32_t *v) {
                  : "memory");
 }
 // the same n values for every lane
-__device__ __forceinline__ void add_bias(float (&v)[16], const float *bias, int n) {
+__device__ __forceinline__ void load_bias(float (&v)[16], const float *bias, int n) {
   if (n == 16 && ((uintptr_t)bias & 15u) == 0) {
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       const float4 b = *reinterpret_cast<const float4 *>(bias + j);
-      v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+      v[j] = b.x, v[j + 1] = b.y, v[j + 2] = b.z, v[j + 3] = b.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; j++)
-      if (j < n) v[j] += bias[j];
+    for (int j = 0; j < 16; j++) v[j] = j < n ? bias[j] : 0.f;
   }
 }
 
@@ -641,12 +640,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
         for (int i = 0; i < 4; i++) {
           const int c0 = 16 * (grp + 4 * i), col = T.n0 + c0, n = min(16, P.n - col);
           const bool here = c0 < end;
-          float v[16], u[16];
-          if (here) {
-            read(c0, v);
-            if (P.gated) read(cols + c0, u);
-            if (grp + 4 * (i + 1) >= last) release();
-          }
           // the residuals' pieces in turn, those of other groups too: a warp
           // that skips a phase of a barrier cannot tell the next from the one
           // before the last
@@ -667,11 +660,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
             __syncwarp();
             if (lane == 0) tc05::mbar_arrive(&B.res_empty[rb]);
           }
+          float v[16], u[16], bias[16];
+          if (P.bias && here) load_bias(bias, P.bias + col, n);
+          if (here) {
+            read(c0, v);
+            if (P.gated) read(cols + c0, u);
+            if (grp + 4 * (i + 1) >= last) release();
+          }
           if (here && live) {
-            if (P.bias) add_bias(v, P.bias + col, n);
+            if (P.bias) {
+#pragma unroll
+              for (int j = 0; j < 16; j++) v[j] += bias[j];
+              if (P.gated) load_bias(bias, P.bias + P.n + col, n);
+            }
             activate_all(v, P.act);
             if (P.gated) {
-              if (P.bias) add_bias(u, P.bias + P.n + col, n);
+              if (P.bias) {
+#pragma unroll
+                for (int j = 0; j < 16; j++) u[j] += bias[j];
+              }
 #pragma unroll
               for (int j = 0; j < 16; j++) v[j] *= u[j];
             }
