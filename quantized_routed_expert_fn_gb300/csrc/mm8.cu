@@ -642,17 +642,18 @@ cudaError_t launch_tc(Mm8P &p, int grid, cudaStream_t st) {
   p.tok = rows * 128;
   p.stage = (KB * (p.tok + MB * 16384) + 1023) / 1024 * 1024;
   p.stages = LY::room / p.stage < kMaxStages ? LY::room / p.stage : kMaxStages;
+  // the most any launch asks for: another host thread's launch of the same
+  // kernel may stand between this and the launch below.  Before the tensor
+  // maps: it makes the device's context this thread's, which they need
+  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       LY::offRing + LY::room + 1024);
+  if (e != cudaSuccess) return e;
   bool ok = encode_fn() != nullptr;
   ok = ok && make_map8(&p.tm_b, p.b, p.k, (uint64_t)(p.G > 0 ? p.G : 1) * p.n, p.k, 128, KB);
   for (int i = 0; i < rows / LY::unit; i++)
     ok = ok && make_map8(&p.tm_a[i], p.a, p.k, p.t, p.lda, (uint32_t)((i + 1) * LY::unit), KB);
   if (!ok) return cudaErrorNotSupported;
   const int smem = LY::offRing + p.stages * p.stage + 1024;
-  // the most any launch asks for: another host thread's launch of the same
-  // kernel may stand between this and the launch below
-  cudaError_t e = cudaFuncSetAttribute(mm8_tc<MB, KIND, CG, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       LY::offRing + LY::room + 1024);
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[2];
   int n = 0;
   if (CG == 2) {
