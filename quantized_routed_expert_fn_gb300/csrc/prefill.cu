@@ -1249,6 +1249,13 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, ui
 }  // namespace
 
 int pf_tensor_maps(PfParams &p, const char **why) {
+  // makes the device's context this thread's (the first call of a new thread),
+  // which the maps need
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, pf_gemm<MODE_ROUTER>) != cudaSuccess) {
+    *why = "the kernels do not load";
+    return -1;
+  }
   const uint64_t H = (uint64_t)p.H, t = (uint64_t)p.t;
   if (!encode_fn()) {
     *why = "cuTensorMapEncodeTiled is not available from the driver";
