@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
   } else if (warp == kEpi + 2) {
     // ---------------------------------------------------------------- residuals
     // (tokens on the M side) this CTA's 128 tokens' of a tile, a piece of
-    // columns after the other
+    // columns after the other (what the last piece holds beyond the tile's
+    // columns is used by none)
     if (TOK && P.res) {
       int f = 0;
       bool ok = true;
