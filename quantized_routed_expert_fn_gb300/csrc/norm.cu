@@ -578,7 +578,7 @@ cudaError_t launch_form(NormP p, int T, cudaStream_t st) {
 
 // Values a thread holds.  What a thread does whatever their number (addresses,
 // exchanges, the root) costs as much as some 16: 32 of them, with a residual
-// 16, as long as the rows give every SM 64 warps; few rows want many threads.
+// 16, as long as the rows give every SM 64 (200) warps; few rows want many threads.
 // us with 8 / 16 / 32 / 64 values, bf16, norm: 65536 rows x 2048 101 / 95 / 89
 // / 111, 32768 x 4096 113 / 104 / 97 / 110; one row x 2048 1.8 / 2.1 / 2.4 /
 // 3.1.  add_norm (fp32 residual): 65536 x 2048 305 / 286 / 297 / 324.
@@ -586,7 +586,7 @@ template <class T>
 int values_a_thread(const NormP &p, int n_sms, bool sh, T threads) {
   int nv = 8;
   const int most = p.res || with_ring(p, sh) ? 16 : 32;
-  while (nv < most && threads(2 * nv) < threads(nv) && (int64_t)p.t * threads(2 * nv) >= (int64_t)n_sms * 64 * 32) nv *= 2;
+  while (nv < most && threads(2 * nv) < threads(nv) && (int64_t)p.t * threads(2 * nv) >= (int64_t)n_sms * (p.res ? 200 : 64) * 32) nv *= 2;
   while (threads(nv) > kMaxThreads) nv *= 2;
   return nv;
 }
