@@ -33,7 +33,6 @@ namespace {
 constexpr unsigned FULLM = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kU = 4;  // 16-byte chunks of a thread at a time, as many on their way
 constexpr int kMaxS = 8;
 
 typedef unsigned long long key_t64;
@@ -172,7 +171,8 @@ __device__ __forceinline__ void add_chunk(Sums &a, const uint4 &r, float c) {
   a.s0 += t0, a.s1 += t1;
 }
 
-template <bool BF16, int T>
+// T threads a block, U chunks of 16 bytes a thread at a time and as many on their way.
+template <bool BF16, int T, int U>
 __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ LogprobsP P) {
   using C = Chunk<BF16>;
   constexpr int CH = C::n, W = T / 32, kSize = BF16 ? 2 : 4;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
   const uint8_t *at = base + (int64_t)lo * kSize;
   const int off = (int)(((uintptr_t)at & 15u) / kSize), nch = (len + off + CH - 1) / CH;
   const uint4 *chunks = reinterpret_cast<const uint4 *>(at - off * kSize);
-  const int niter = (nch + T * kU - 1) / (T * kU);
+  const int niter = (nch + T * U - 1) / (T * U);
   const int whole0 = off ? 1 : 0, whole1 = (len + off) / CH;  // chunks that lie in the row
 
   float tok = 0.f;  // this thread's first given token
@@ -231,24 +231,24 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     return make_uint4(w[0], w[1], w[2], w[3]);
   };
   // whether all of iteration it's chunks lie in the row
-  auto inside = [&](int it) { return it * kU * T >= whole0 && (it + 1) * kU * T <= whole1; };
-  auto load = [&](uint4 (&r)[kU], int it) {
+  auto inside = [&](int it) { return it * U * T >= whole0 && (it + 1) * U * T <= whole1; };
+  auto load = [&](uint4 (&r)[U], int it) {
     if (inside(it)) {
 #pragma unroll
-      for (int u = 0; u < kU; u++) r[u] = ldg_stream4(chunks + (it * kU + u) * T + tid);
+      for (int u = 0; u < U; u++) r[u] = ldg_stream4(chunks + (it * U + u) * T + tid);
       return;
     }
 #pragma unroll
-    for (int u = 0; u < kU; u++) r[u] = load_one((it * kU + u) * T + tid);
+    for (int u = 0; u < U; u++) r[u] = load_one((it * U + u) * T + tid);
   };
-  auto max_of = [&](const uint4 (&r)[kU]) {
+  auto max_of = [&](const uint4 (&r)[U]) {
     float m = -kInf;
 #pragma unroll
-    for (int u = 0; u < kU; u++) m = fmaxf(m, chunk_max<BF16>(r[u]));  // drops NaN
+    for (int u = 0; u < U; u++) m = fmaxf(m, chunk_max<BF16>(r[u]));  // drops NaN
     return m;
   };
 
-  uint4 cur[kU], nxt[kU];
+  uint4 cur[U], nxt[U];
   load(cur, 0);
   // ---- the sums, and the largest value of each thread
   Sums sum;
@@ -261,6 +261,17 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
   }
   const float room = 4.f / c;  // how far above its reference a value may lie
   float most = -kInf;
+  // the values of one iteration with care; of many rows not unrolled, as that
+  // doubles the registers
+  auto careful_sums = [&] {
+    if constexpr (U > 4) {
+#pragma unroll
+      for (int u = 0; u < U; u++) add_chunk<BF16, true>(sum, cur[u], c);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < U; u++) add_chunk<BF16, true>(sum, u == 0 ? cur[0] : (u == 1 ? cur[1] : (u == 2 ? cur[2] : cur[3])), c);
+    }
+  };
   bool safe = false;
   for (int it = 0; it < niter; it++) {
     if (it + 1 < niter) load(nxt, it + 1);
@@ -274,21 +285,19 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     const Sums before = sum;
     const bool careful = safe || !inside(it) || __any_sync(FULLM, sum.big);
     if (careful) {
-#pragma unroll 1
-      for (int u = 0; u < kU; u++) add_chunk<BF16, true>(sum, u == 0 ? cur[0] : (u == 1 ? cur[1] : (u == 2 ? cur[2] : cur[3])), c);
+      careful_sums();
     } else {
 #pragma unroll
-      for (int u = 0; u < kU; u++) add_chunk<BF16, false>(sum, cur[u], c);
+      for (int u = 0; u < U; u++) add_chunk<BF16, false>(sum, cur[u], c);
       // masked values: these again, and the rest of the row, with care
       if (__any_sync(FULLM, !(fabsf(sum.s1) < kInf))) {
         safe = true;
         sum = before;
-#pragma unroll 1
-        for (int u = 0; u < kU; u++) add_chunk<BF16, true>(sum, u == 0 ? cur[0] : (u == 1 ? cur[1] : (u == 2 ? cur[2] : cur[3])), c);
+        careful_sums();
       }
     }
 #pragma unroll
-    for (int u = 0; u < kU; u++) cur[u] = nxt[u];
+    for (int u = 0; u < U; u++) cur[u] = nxt[u];
   }
 
   // ---- the largest values
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     first = __shfl_sync(FULLM, first, 0);
     if (has) s_cand[first + __popc(who & ((1u << lane) - 1u))] = (uint16_t)tid;
     __syncthreads();
-    const int n = s_cand_n, total = n * niter * kU;
+    const int n = s_cand_n, total = n * niter * U;
     for (int b = 0; b < total; b += T) {
       const int x = b + tid, j = n ? x / n : 0, i = j * T + (x < total ? s_cand[x - j * n] : 0);
       const bool in = x < total && i < nch;
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
   }
 }
 
-template <bool BF16, int T>
+template <bool BF16, int T, int U = 4>
 cudaError_t launch_t(const LogprobsP &p, cudaStream_t st) {
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -482,7 +491,7 @@ cudaError_t launch_t(const LogprobsP &p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = p.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_rows<BF16, T>, p);
+  return cudaLaunchKernelEx(&cfg, logprobs_rows<BF16, T, U>, p);
 }
 
 }  // namespace
@@ -508,6 +517,10 @@ cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st) {
   const bool few = (int64_t)p.t < 8 * (int64_t)n_sms;
   int T = bytes <= (few ? 4096 : 20480) ? 32 : (bytes <= (few ? 8192 : 40960) ? 64 : (bytes <= (few ? 20480 : 131072) ? 128 : 256));
   if (p.S > 1) T = 256;  // a warp for each of a row's lists
+  // fp32, no more than two blocks an SM: more of a row in flight for each (48 x 100003,
+  // not in L2: 14.4 -> 11.5 us; 4096 x 131072: 186 -> 328). Not bf16, where its registers
+  // leave one block an SM (16 x 131072: 7.9 -> 12.4).
+  if (!p.bf16 && T == 256 && (int64_t)p.t * p.S <= 2 * n_sms) return launch_t<false, 256, 8>(p, st);
   auto go = [&](auto n) { return p.bf16 ? launch_t<true, decltype(n)::value>(p, st) : launch_t<false, decltype(n)::value>(p, st); };
   if (T == 32) return go(std::integral_constant<int, 32>());
   if (T == 64) return go(std::integral_constant<int, 64>());
