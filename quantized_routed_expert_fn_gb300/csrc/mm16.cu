@@ -922,7 +922,9 @@ cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st) {
   int cg = 1;
   auto look = [&](bool tok, int nmt, int other, int per) {  // other: what the N side holds, per / 2 of a column
     const int c = nmt > 1 ? 2 : 1, nmp = (nmt + c - 1) / c;
-    for (int w = 256; w >= 32 * c; w -= 16 * c) {
+    // (a tile's columns are whole pieces of 16: the epilogue writes no fewer)
+    const int step = 32 / per > 16 * c ? 32 / per : 16 * c;
+    for (int w = 256; w >= 32 * c; w -= step) {
       const int cols = w * per / 2;
       const int64_t rounds = ((int64_t)((other + cols - 1) / cols) * nmp + n_sms / c - 1) / (n_sms / c), cost = rounds * (w + 48);
       if (cost < best) best = cost, p.w = w, tokens = tok, cg = c;

@@ -107,6 +107,15 @@ def test_large_tiles_are_exact(moe, t, n, k, gated, kind, res):
         assert torch.equal(out.double()[small], ref[small])
 
 
+@pytest.mark.parametrize("res", [None, "f32", "bf16"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("t,n,k", [(100, 4992, 72), (128, 8192, 64), (17, 10240, 40), (64, 10256, 136), (101, 14336, 64), (128, 20000, 48)],
+                         ids=lambda v: str(v))
+def test_gated_wide_products_of_few_rows(moe, t, n, k, kind, res):
+    """One tile of tokens and many columns, whose tiles have to end where the next begins: exact products of whole numbers."""
+    test_large_tiles_are_exact(moe, t, n, k, True, kind, res)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("t,n,k", [(1, 96, 256), (7, 513, 2048), (20, 200, 520), (150, 264, 1024), (300, 1001, 200), (1100, 640, 96)],
                          ids=lambda v: str(v))
