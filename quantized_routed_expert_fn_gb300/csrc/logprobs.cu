@@ -17,8 +17,8 @@
 //
 // A row is a cluster of S blocks (few rows) or one block; the blocks' sums
 // and lists meet in the first one's shared memory.  The bound is HBM, beside
-// some six instructions a value: 4096 x 131072 bf16 182 us, 5.9 TB/s (without
-// alternatives 156, 6.9); 1 x 131072 fp32, top 20: 8.0, of which launch, the
+// some six instructions a value: 4096 x 131072 bf16 185 us, 5.8 TB/s (without
+// alternatives 158, 6.8); 1 x 131072 fp32, top 20: 7.6, of which launch, the
 // orders and exchanges are nearly all.
 #include <cuda_runtime.h>
 #include <type_traits>

@@ -166,11 +166,6 @@ __device__ __forceinline__ bool mbar_sleep_wait_cluster(uint64_t *bar, uint32_t 
   return ok != 0;
 }
 // loads from one
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
