@@ -56,6 +56,7 @@ struct LogprobsP {
   float *top_logp;
   int k;
   int S, seg;  // blocks of a row, values of a block
+  int ahead, fetch;  // rows at once; bytes of the row that far ahead to bring to L2 meanwhile
 };
 cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st);
 

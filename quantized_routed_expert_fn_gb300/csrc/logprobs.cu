@@ -17,7 +17,7 @@
 //
 // A row is a cluster of S blocks (few rows) or one block; the blocks' sums
 // and lists meet in the first one's shared memory.  The bound is HBM, beside
-// some six instructions a value: 4096 x 131072 bf16 185 us, 5.8 TB/s (without
+// some six instructions a value: 4096 x 131072 bf16, top 5, 175 us, 6.1 TB/s (without
 // alternatives 158, 6.8); 1 x 131072 fp32, top 20: 7.6, of which launch, the
 // orders and exchanges are nearly all.
 #include <cuda_runtime.h>
@@ -34,6 +34,7 @@ constexpr unsigned FULLM = 0xffffffffu;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxS = 8;
+constexpr int kFetch = 32 * 1024;
 
 typedef unsigned long long key_t64;
 
@@ -340,6 +341,12 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     }
   };
   if (P.k > 0) {
+    // the row that takes this one's place begins in L2, as the block asks HBM
+    // for little until then
+    if (P.fetch && tid == 0 && row + P.ahead < P.t) {
+      const uintptr_t next = reinterpret_cast<uintptr_t>(base) + (uintptr_t)(P.ahead * P.ld * kSize);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((next + 15) & ~(uintptr_t)15), "r"(P.fetch) : "memory");
+    }
     // the threads' maxima in order: top_k of the row reach the top_k-th, and
     // only the threads whose own does have such values: their chunks again,
     // shared out over the block (they lie in L2, or did not long ago)
@@ -356,11 +363,19 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     if (has) s_cand[first + __popc(who & ((1u << lane) - 1u))] = (uint16_t)tid;
     __syncthreads();
     const int n = s_cand_n, total = n * niter * U;
-    for (int b = 0; b < total; b += T) {
-      const int x = b + tid, j = n ? x / n : 0, i = j * T + (x < total ? s_cand[x - j * n] : 0);
-      const bool in = x < total && i < nch;
-      uint4 r = in ? load_one(i) : make_uint4(~0u, ~0u, ~0u, ~0u);  // (no numbers)
-      if (__any_sync(FULLM, in && chunk_max<BF16>(r) >= tau_v)) push(r, i);
+    constexpr int G = T == 256 ? 2 : 1;  // chunks of a thread at a time (4096 x 131072 bf16, top 20: 219 us; 1: 224)
+    for (int b = 0; b < total; b += T * G) {
+      uint4 r[G];
+      int at_i[G];
+#pragma unroll
+      for (int u = 0; u < G; u++) {
+        const int x = b + u * T + tid, j = n ? x / n : 0, i = j * T + (x < total ? s_cand[x - j * n] : 0);
+        r[u] = x < total && i < nch ? load_one(i) : make_uint4(~0u, ~0u, ~0u, ~0u);  // (no numbers)
+        at_i[u] = i;
+      }
+#pragma unroll
+      for (int u = 0; u < G; u++)
+        if (__any_sync(FULLM, chunk_max<BF16>(r[u]) >= tau_v)) push(r[u], at_i[u]);
     }
     compact();
     merge_lists(s_top, W, s_list[warp][lane]);
@@ -479,7 +494,16 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
 }
 
 template <bool BF16, int T, int U = 4>
-cudaError_t launch_t(const LogprobsP &p, cudaStream_t st) {
+cudaError_t launch_t(LogprobsP p, int n_sms, cudaStream_t st) {
+  static const int fit = [] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, logprobs_rows<BF16, T, U>, T, 0) == cudaSuccess ? n : 0;
+  }();
+  p.ahead = fit * n_sms;
+  // 4096 x 131072 bf16 with 0 / 16 / 32 / 64 / 128 KB of the next row: top 1 178 /
+  // 169 / 164 / 168 / 173 us, top 5 185 / 180 / 179 / 184 / 189, top 20 224 / 226 /
+  // 227 / 232 / 230; shorter rows lose (16384 x 16000: 123 / 131 with 32)
+  p.fetch = T == 256 && p.S == 1 && (int64_t)p.v * (BF16 ? 2 : 4) >= 2 * kFetch ? kFetch : 0;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -520,8 +544,8 @@ cudaError_t launch_logprobs(LogprobsP p, int n_sms, cudaStream_t st) {
   // fp32, no more than two blocks an SM: more of a row in flight for each (48 x 100003,
   // not in L2: 14.4 -> 11.5 us; 4096 x 131072: 186 -> 328). Not bf16, where its registers
   // leave one block an SM (16 x 131072: 7.9 -> 12.4).
-  if (!p.bf16 && T == 256 && (int64_t)p.t * p.S <= 2 * n_sms) return launch_t<false, 256, 8>(p, st);
-  auto go = [&](auto n) { return p.bf16 ? launch_t<true, decltype(n)::value>(p, st) : launch_t<false, decltype(n)::value>(p, st); };
+  if (!p.bf16 && T == 256 && (int64_t)p.t * p.S <= 2 * n_sms) return launch_t<false, 256, 8>(p, n_sms, st);
+  auto go = [&](auto n) { return p.bf16 ? launch_t<true, decltype(n)::value>(p, n_sms, st) : launch_t<false, decltype(n)::value>(p, n_sms, st); };
   if (T == 32) return go(std::integral_constant<int, 32>());
   if (T == 64) return go(std::integral_constant<int, 64>());
   if (T == 128) return go(std::integral_constant<int, 128>());
