@@ -84,6 +84,31 @@ __device__ __forceinline__ void store_as(void *p, int64_t i, const float *v) {
   }
 }
 
+// Two values an instruction, each rounded as on its own.
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
+  asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n mul.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// x, y = a x + c, b y + d
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float c, float d) {
+  asm("{\n .reg .b64 u, v, w;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n mov.b64 w, {%4, %5};\n fma.rn.f32x2 u, u, v, w;\n"
+      " mov.b64 {%0, %1}, u;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+// s, t += a^2, b^2
+__device__ __forceinline__ void squares2(float &s, float &t, float a, float b) {
+  asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n fma.rn.f32x2 u, v, v, u;\n mov.b64 {%0, %1}, u;\n}\n"
+      : "+f"(s), "+f"(t)
+      : "f"(a), "f"(b));
+}
+template <int N>
+__device__ __forceinline__ void scale_all(float (&v)[N], float c) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) mul2(v[i], v[i + 1], c, c);
+}
+
 // Sum over the T threads of each row: a power of two lanes, or all warps of a
 // block; red:
 // a word for each warp, used once.  large (the same for all threads of a warp,
@@ -114,7 +139,7 @@ template <int NV>
 __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP &P, float *red) {
   float s4[4] = {x * x, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < NV; i++) s4[i & 3] = fmaf(v[i], v[i], s4[i & 3]);
+  for (int i = 0; i < NV; i += 2) squares2(s4[i & 3], s4[(i & 3) + 1], v[i], v[i + 1]);
   bool large, any;
   float ss = row_sum((s4[0] + s4[1]) + (s4[2] + s4[3]), P.T, red, any), eps = P.eps;
   if (any) {
@@ -130,8 +155,7 @@ __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP 
   // next to a border are told apart as by a division)
   const float inv = m < 1e38f ? fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r) : r;
   x *= inv;
-#pragma unroll
-  for (int i = 0; i < NV; i++) v[i] *= inv;
+  scale_all(v, inv);
 }
 
 // SH (V = 8): rows that do not start on 16 bytes, but all matrices' alike: the
@@ -260,8 +284,12 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
       } else {
         load_as<V, false>(weights, col(j), w);
       }
+      if constexpr (V > 1) {
 #pragma unroll
-      for (int i = 0; i < V; i++) v[j * V + i] *= w[i];
+        for (int i = 0; i < V; i += 2) mul2(v[j * V + i], v[j * V + i + 1], w[i], w[i + 1]);
+      } else {
+        v[j] *= w[0];
+      }
     });
     if (SH) x *= xw;
   };
@@ -282,8 +310,7 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
       if (P.gate_cols == 1) {
         const float g = live ? gate_of(P, load1(P.gate, P.gate_bf16, row * P.ldg)) : 1.f;
         x *= g;
-#pragma unroll
-        for (int i = 0; i < NV; i++) v[i] *= g;
+        scale_all(v, g);
       } else if (SH && P.ldg == 0) {
         weigh(nullptr, vecs.g, vecs.xg);
       } else {
@@ -303,8 +330,9 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
       }
     }
     x = fmaf(P.scale, x, P.res_scale * rx);
+    scale_all(r, P.res_scale);
 #pragma unroll
-    for (int i = 0; i < NV; i++) v[i] = fmaf(P.scale, v[i], P.res_scale * r[i]);
+    for (int i = 0; i < NV; i += 2) fma2(v[i], v[i + 1], P.scale, P.scale, r[i], r[i + 1]);
     store(P.ro, P.ro_bf16, row * P.ldro);
     if (P.out_kind == kNormOutNone) return;
   }
@@ -345,9 +373,9 @@ __device__ __forceinline__ void one_row(const NormP &P, int64_t row, float (&red
         quant_block<8>(b, w, e);
       } else {
         e = e8m0_of_amax(__float_as_uint(a[j]));
-        const float f = e8m0_inv(e);
-        w[0] = e4m3x4<false>(b[0] * f, b[1] * f, b[2] * f, b[3] * f);
-        w[1] = e4m3x4<false>(b[4] * f, b[5] * f, b[6] * f, b[7] * f);
+        scale_all(b, e8m0_inv(e));
+        w[0] = e4m3x4<false>(b[0], b[1], b[2], b[3]);
+        w[1] = e4m3x4<false>(b[4], b[5], b[6], b[7]);
       }
       if (col(j) < h) {
         *reinterpret_cast<uint2 *>(q + col(j)) = make_uint2(w[0], w[1]);
