@@ -9,9 +9,11 @@
 // values: V = 8 where all rows start on 16 bytes, or anywhere but alike (the
 // pieces then begin on 16 bytes in the row, see SH); 2 or 1 otherwise, so that
 // neighbouring lanes always touch neighbouring bytes.  Sums are 32-bit, in a
-// fixed tree.  65536 x 2048 bf16: 87 us, 6.2 TB/s; fp32 32768 x 2048: 78, 6.9;
+// fixed tree.  65536 x 2048 bf16: 84 us, 6.4 TB/s; fp32 32768 x 2048: 79, 6.8;
 // 32816 x 4090 bf16 114 (with pieces of 2: 160).  add_norm, 30000 x 4096, all
-// bf16, a gate a channel: 161 us, 6.1 TB/s; 30011 x 4090 214.
+// bf16, a gate a channel: 157 us, 6.3 TB/s; 30011 x 4090 207.  Arithmetic goes two
+// values an instruction (one by one: 102 instead of 98.7 us for 65536 x 2048 to e4m3,
+// 217 instead of 207 for the last).
 #include <cuda_runtime.h>
 
 #include <type_traits>
