@@ -11,9 +11,8 @@
 // neighbouring lanes always touch neighbouring bytes.  Sums are 32-bit, in a
 // fixed tree.  65536 x 2048 bf16: 84 us, 6.4 TB/s; fp32 32768 x 2048: 79, 6.8;
 // 32816 x 4090 bf16 114 (with pieces of 2: 160).  add_norm, 30000 x 4096, all
-// bf16, a gate a channel: 157 us, 6.3 TB/s; 30011 x 4090 207.  Arithmetic goes two
-// values an instruction (one by one: 102 instead of 98.7 us for 65536 x 2048 to e4m3,
-// 217 instead of 207 for the last).
+// bf16, a gate a channel: 157 us, 6.3 TB/s; 30011 x 4090 195.  Arithmetic goes two
+// values an instruction (one by one 2 to 4 % longer).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -179,12 +178,18 @@ __device__ __forceinline__ float load1(const void *p, int bf16, int64_t i) {
 }
 __device__ __forceinline__ float gate_of(const NormP &P, float g) { return P.gate_sigmoid && g == g ? logistic(g) : g; }
 
+// Which of a block's rows is a thread's (T up to 32 is a power of two; above, a
+// block has one row).
+__device__ __forceinline__ int row_of(int T, int thread) { return T <= 32 ? thread >> (31 - __clz(T)) : 0; }
+
 // What a thread holds of a row: pieces of V columns, and, SH, one value more.
 template <int V, int NV, bool SH>
 struct Place {
   int T, l, h, lead, xc;  // xc: its column, < 0: none
   __device__ __forceinline__ Place(const NormP &P, int64_t row, int thread) {
-    T = P.T, l = T >= (int)blockDim.x ? thread : thread & (T - 1);
+    // (either is right; each where it costs fewer registers: 30011 x 4090 195 us
+    // against 229, to e4m3 65536 x 2048 93 against 98)
+    T = P.T, l = (SH ? T >= (int)blockDim.x : T > 32) ? thread : thread & (T - 1);
     h = row < P.t ? P.h : 0, lead = SH ? (int)(-((row & 7) * P.ld8) & 7) : 0, xc = -1;
     if (SH && l < 8 && l < lead) xc = l;
     if (SH && l >= 8 && l < 16) xc = h - (h - lead) % 8 + l - 8;
@@ -217,11 +222,10 @@ __host__ __device__ constexpr int ring_row(int nv, int bf16) { return nv * (bf16
 template <int V, int NV, bool ADD, bool SH>
 __device__ __forceinline__ void row_copies(const NormP &P, int64_t first, const Ring &ring, int at) {
   const int lane = threadIdx.x & 31;
-  auto row_of = [&](int thread) { return first + (P.T >= (int)blockDim.x ? 0 : thread / P.T); };
   auto copy = [&](const void *p, int bf16, int64_t ld, uint8_t *to) {
     to += (size_t)at * ring_row(NV, bf16) * blockDim.x;
     if (bf16) {
-      const int64_t row = row_of(threadIdx.x);
+      const int64_t row = first + row_of(P.T, threadIdx.x);
       const Place<V, NV, SH> L(P, row, threadIdx.x);
       L.pieces([&](int j) {
         cp_async16(to + ((size_t)j * blockDim.x + threadIdx.x) * 16, static_cast<const uint16_t *>(p) + row * ld + L.col(j));
@@ -230,7 +234,7 @@ __device__ __forceinline__ void row_copies(const NormP &P, int64_t first, const 
 #pragma unroll
       for (int c = 0; c < 2; c++) {
         const int thread = (int)threadIdx.x - lane + 16 * c + (lane >> 1);
-        const int64_t row = row_of(thread);
+        const int64_t row = first + row_of(P.T, thread);
         const Place<V, NV, SH> L(P, row, thread);
         L.pieces([&](int j) {
           cp_async16(to + ((size_t)j * blockDim.x + thread) * 32 + 16 * (lane & 1),
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kMaxThreads, NV <= 16 ? 2 : 0) norm_rows(const
   extern __shared__ __align__(16) uint32_t s_dyn[];  // e4m3, V < 8: maxima [N][warps]; the ring; SH: vectors
   pdl_wait_prev();
   pdl_launch_next();
-  const int per = P.T >= (int)blockDim.x ? 1 : (int)blockDim.x / P.T, mine = per > 1 ? (int)threadIdx.x / P.T : 0;
+  const int per = row_of(P.T, blockDim.x - 1) + 1, mine = row_of(P.T, threadIdx.x);
   if constexpr (!WALK) {
     one_row<V, NV, ADD, SH, false>(P, (int64_t)blockIdx.x * per + mine, s_red[0], Vecs(), s_dyn);
     return;
