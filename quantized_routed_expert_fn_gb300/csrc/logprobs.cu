@@ -95,18 +95,23 @@ __device__ __forceinline__ void merge_lists(K (*lists)[32], int n, K mine) {
 }
 
 // What a thread, a block or a row has summed.  ref: the reference logit (-inf:
-// nothing yet); mu = ref * c, in 32 bits, is what the sums are relative to
-// unless it is so large that l * c may overflow: then they are to ref itself.
+// nothing yet); mu = ref * c, rounded to 32 bits, is what the sums are relative
+// to (a term is then one multiply-add) as long as its rounding stays small: of
+// 2^20 it is up to 2^-5 of a power of two, of 2^32 more than the exponents
+// hold.  From 2^20 on (masks, large logits or scales) they are to ref itself.
 struct Sums {
   float ref, mu, s0, s1;
   bool big;
 };
 __device__ __forceinline__ void set_ref(Sums &a, float ref, float c) {
-  a.ref = ref, a.mu = ref * c, a.big = !(fabsf(a.mu) < 1e30f);
+  a.ref = ref, a.mu = ref * c, a.big = !(fabsf(a.mu) < 1048576.f);
 }
-// how far (in powers of two, 0 or below) a's reference lies below one at M
+// how far ref * c lies above what the sums are relative to
+__device__ __forceinline__ float slack(const Sums &a, float c) { return a.big ? 0.f : fmaf(a.ref, c, -a.mu); }
+// how far (in powers of two, 0 or below but for that rounding) what a's sums
+// are relative to lies below the same of M
 __device__ __forceinline__ float below(const Sums &a, const Sums &M, float c) {
-  const float d = a.ref == M.ref ? 0.f : (a.big || M.big ? (a.ref - M.ref) * c : a.mu - M.mu);
+  const float d = a.ref == M.ref ? 0.f : (a.big || M.big ? (a.ref - M.ref) * c - slack(a, c) + slack(M, c) : a.mu - M.mu);
   return fmaxf(d, -300.f);
 }
 __device__ __forceinline__ void move_to(Sums &a, const Sums &M, float c) {
@@ -147,8 +152,7 @@ __device__ __forceinline__ float chunk_max(const uint4 &r) {
 }
 
 // A chunk's terms.  SAFE: masked values (infinities below, NaN) count nothing,
-// and references may be so large that l * c overflows; without it such values
-// leave s1 no number.
+// and references may be large; without it masked values leave s1 no number.
 template <bool BF16, bool SAFE>
 __device__ __forceinline__ void add_chunk(Sums &a, const uint4 &r, float c) {
   constexpr int CH = Chunk<BF16>::n;
@@ -463,16 +467,16 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
     float lz, h;
     if (all.ref == kInf) {
       lz = logf((float)ninf), h = lz;
-    } else if (all.s0 > 0.f) {
+    } else if (all.ref == -kInf) {  // no logit
+      lz = 0.f, h = 0.f;
+    } else {
       const float l2 = log2f(all.s0);
       // relative to ref: mu is ref * c rounded
-      lz = kLn2 * (all.big ? l2 : l2 + fmaf(-all.ref, c, all.mu)), h = kLn2 * (l2 - all.s1 / all.s0);
-    } else {
-      lz = 0.f, h = 0.f;
+      lz = kLn2 * (l2 - slack(all, c)), h = kLn2 * (l2 - all.s1 / all.s0);
     }
     if (lane == 0) {
       s_row[0] = all.ref, s_row[1] = lz;
-      if (P.entropy) P.entropy[row] = fmaxf(h, 0.f);
+      if (P.entropy) P.entropy[row] = h < 0.f ? 0.f : h;
     }
     auto logp = [&](float x) { return x == all.ref ? -lz : fmaf(P.scale, x - all.ref, -lz); };
     if (lane < P.k) {
