@@ -120,6 +120,12 @@ __device__ __forceinline__ void move_to(Sums &a, const Sums &M, float c) {
   a.ref = M.ref, a.mu = M.mu, a.big = M.big;
 }
 
+// ln p of a logit, lz being ln Z relative to ref (in halves: the difference may
+// pass the 32-bit range and the scale bring it back)
+__device__ __forceinline__ float ln_p(float l, float ref, float scale, float lz) {
+  return l == ref ? -lz : fmaf(2.f * scale, 0.5f * l - 0.5f * ref, -lz);
+}
+
 template <bool BF16>
 struct Chunk {
   static constexpr int n = BF16 ? 8 : 4;
@@ -478,11 +484,10 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
       s_row[0] = all.ref, s_row[1] = lz;
       if (P.entropy) P.entropy[row] = h < 0.f ? 0.f : h;
     }
-    auto logp = [&](float x) { return x == all.ref ? -lz : fmaf(P.scale, x - all.ref, -lz); };
     if (lane < P.k) {
       const float x = of_okey((uint32_t)(top >> 32));
       P.top_idx[row * P.k + lane] = top ? ~(uint32_t)top : 0xffffffffu;
-      P.top_logp[row * P.k + lane] = top ? logp(x) : -kInf;
+      P.top_logp[row * P.k + lane] = top ? ln_p(x, all.ref, P.scale, lz) : -kInf;
     }
   }
   __syncthreads();
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(T) logprobs_rows(const __grid_constant__ Logpr
       if ((unsigned)tok_id < (unsigned)P.v) tok = C::load1(base, tok_id);
     }
     const bool in = (unsigned)tok_id < (unsigned)P.v && tok > -kInf;  // false for NaN
-    P.logp[row * P.m + i] = !in ? -kInf : (tok == ref ? -lz : fmaf(P.scale, tok - ref, -lz));
+    P.logp[row * P.m + i] = in ? ln_p(tok, ref, P.scale, lz) : -kInf;
   }
 }
 

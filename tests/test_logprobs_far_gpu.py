@@ -65,3 +65,12 @@ def test_large_offsets_and_scales(moe, v, copies, scale, dtype):  # noqa: F811
     a = np.stack(rows)
     tokens = np.stack([a.argmax(1), np.full(len(a), v // 3), np.full(len(a), v - 1)], 1)
     check_rows(moe, a, dtype, tokens, (20, 0), scale, copies)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_differences_past_the_range(moe, dtype):  # noqa: F811
+    """Logits whose difference no 32-bit number holds, under a scale that brings it back: ln p is a number."""
+    g = np.random.default_rng(5)
+    a = np.stack([np.where(g.random(3000) < 0.5, -3e38, 3e38), np.where(np.arange(3000) == 77, 3e38, -3e38)])
+    tokens = np.array([[0, 1, 2], [77, 5, 6]])
+    check_rows(moe, a, dtype, tokens, (8,), 1e-38, 20)
