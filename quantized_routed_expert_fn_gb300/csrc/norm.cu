@@ -145,11 +145,12 @@ __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP 
   float ss = row_sum((s4[0] + s4[1]) + (s4[2] + s4[3]), P.T, red, any), eps = P.eps;
   if (any) {
     const float c = !(ss < 1e37f) ? 7.888609052210118e-31f : 1.f;
-    x *= c, ss = x * x;
+    x *= c;
+    float again = x * x;
 #pragma unroll
-    for (int i = 0; i < NV; i++) v[i] *= c, ss = fmaf(v[i], v[i], ss);
-    ss = row_sum(ss, P.T, red + 32, large);
-    eps = eps * c * c;
+    for (int i = 0; i < NV; i++) v[i] *= c, again = fmaf(v[i], v[i], again);
+    again = row_sum(again, P.T, red + 32, large);
+    if (c != 1.f) ss = again, eps = eps * c * c;  // (a row beside such a one keeps its own sum)
   }
   const float m = fmaf(ss, P.inv_h, eps), r = rsqrtf(m);
   // one step of Newton's: the root's error is the last bit's (e4m3 values
