@@ -133,22 +133,22 @@ __device__ __forceinline__ float row_sum(float v, int T, float *red, bool &large
 }
 
 // v and x *= 1 / sqrt(mean over the row of their squares + eps).  A row whose
-// sum of squares comes near the end of the 32-bit range is summed again 2^-100
-// smaller (exact: its largest value is at least 1e16); infinities and NaN stay
-// what the formula makes of them.
+// sum of squares comes near the end of the 32-bit range is summed again with
+// its values 2^-100 smaller (those that this makes inexact lie 2^70 and more
+// below the largest), and its quotients are made 2^-100 smaller after the
+// product; infinities and NaN stay what the formula makes of them.
 template <int NV>
 __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP &P, float *red) {
   float s4[4] = {x * x, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < NV; i += 2) squares2(s4[i & 3], s4[(i & 3) + 1], v[i], v[i + 1]);
   bool large, any;
-  float ss = row_sum((s4[0] + s4[1]) + (s4[2] + s4[3]), P.T, red, any), eps = P.eps;
+  float ss = row_sum((s4[0] + s4[1]) + (s4[2] + s4[3]), P.T, red, any), eps = P.eps, c = 1.f;
   if (any) {
-    const float c = !(ss < 1e37f) ? 7.888609052210118e-31f : 1.f;
-    x *= c;
-    float again = x * x;
+    if (!(ss < 1e37f)) c = 7.888609052210118e-31f;
+    float again = c * x * (c * x);
 #pragma unroll
-    for (int i = 0; i < NV; i++) v[i] *= c, again = fmaf(v[i], v[i], again);
+    for (int i = 0; i < NV; i++) again = fmaf(c * v[i], c * v[i], again);
     again = row_sum(again, P.T, red + 32, large);
     if (c != 1.f) ss = again, eps = eps * c * c;  // (a row beside such a one keeps its own sum)
   }
@@ -158,6 +158,7 @@ __device__ __forceinline__ void normalise(float (&v)[NV], float &x, const NormP 
   const float inv = m < 1e38f ? fmaf(0.5f * r, fmaf(-m * r, r, 1.f), r) : r;
   x *= inv;
   scale_all(v, inv);
+  if (any) x *= c, scale_all(v, c);
 }
 
 // SH (V = 8): rows that do not start on 16 bytes, but all matrices' alike: the

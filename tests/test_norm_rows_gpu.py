@@ -1,7 +1,8 @@
-"""moe_norm and moe_add_norm: what a row gives is its own, whatever lies beside it."""
+"""moe_norm and moe_add_norm: what a row gives is its own, whatever lies beside it, and rows of far apart values."""
 import numpy as np
 import pytest
 
+import ref8
 import refblock as rb
 from test_norm_gpu import cuda, f64, moe, outputs  # noqa: F401
 
@@ -38,3 +39,36 @@ def test_neighbours_do_not_change_a_row(moe, h, out):  # noqa: F811
     o, s = outputs(t, h, out)
     moe.norm(cuda(plain), o, scales=s)
     assert torch.equal(o[:1], one)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("h", [64, 257, 2048, 4090])
+def test_values_far_below_a_rows_largest(moe, h, out):  # noqa: F811
+    """Rows whose squares leave the 32-bit range and whose values run over all of it: the small ones keep their bits."""
+    g = np.random.default_rng(h)
+    t = 16
+    a = np.sign(g.normal(size=(t, h))) * 10.0 ** g.uniform(-37, 19, size=(t, h))
+    for r in range(t):
+        a[r, r] = 10.0 ** (19 + 1.2 * r)
+    x = cuda(a.astype(np.float32))
+    w = cuda((10.0 ** g.uniform(-1, 20, size=h)).astype(np.float32))  # (the largest are the first ones: no product overflows)
+    w[:t] = 1
+    for weight in (None, w):
+        o, s = outputs(t, h, out)
+        moe.norm(x, o, w=weight, scales=s)
+        torch.cuda.synchronize()
+        # the norm, and its product with the weight, are numbers of 32 bits each: below 2^-126 they have a step of 2^-149 and
+        # may be off by half of it, the first times w
+        ref = rb.norm(f64(x), None if weight is None else f64(weight))
+        bound = np.abs(ref) * (rb.NORM + 4) * rb.U + (1 + (0 if weight is None else f64(weight))) * 2.0 ** -150
+        if out != "e4m3":
+            rb.check(f64(o), ref, bound, out)
+            continue
+        # half a step: 2^-4 of the value, or 2^-10 of the scale; blocks of numbers from 2^-100 on have the least scale
+        step = np.repeat(np.exp2(s.cpu().numpy().astype(np.float64) - 127), 128, 1)[:, :h]
+        got = ref8.E4M3[o.cpu().numpy()] * step
+        assert (np.abs(got - ref) <= bound * 1.1 + np.maximum(np.abs(ref) * 2.0 ** -4, step * 2.0 ** -10)).all()
+        for at in range(0, h, 128):
+            top = np.abs(ref[:, at:at + 128]).max(1)
+            use = top / step[:, at]
+            assert (use <= 448 * 1.001).all() and ((use > 224 * 0.999) | (top < 2.0 ** -100)).all()
