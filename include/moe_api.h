@@ -387,9 +387,9 @@ size_t moe_experts8_workspace(const moe_layer8 *L, int t, int top_k);
  *        moe_quant8 gives them (a scale byte per 128 of a row, [t] rows of
  *        ceil(h / 128), lds apart; NULL for the other types); may be x
  *        itself (same address, stride and type), else overlaps no input
- * t 0..2^30, h 1..32768; eps positive.  A row whose sum of squares leaves the
- * fp32 range is normalised all the same; infinities and NaN give what the
- * formula gives (e4m3: NaN).  Needs no workspace; has no device-side
+ * t 0..2^30, h 1..32768; eps 2^-126 (a normal number) to 1e37.  A row whose sum
+ * of squares leaves the fp32 range is normalised all the same; infinities and
+ * NaN give what the formula gives (e4m3: NaN).  Needs no workspace; has no device-side
  * failures.  This is the x^ of MOE_PRENORM for any row count, with a weight. */
 int moe_norm(const void *x, int x_dtype, int64_t ldx, const float *w, float eps, int t, int h, void *out, int out_dtype,
              int64_t ldo, uint8_t *scales, int64_t lds, moe_stream_t stream);

@@ -50,8 +50,10 @@ bool apart_or_same(const Mat &out, const Mat &in) {
 }
 bool apart(const Mat &out, const Mat &in) { return !overlap(out.p, out.bytes(), in.p, in.bytes()); }
 
+// Beside an eps below the normal numbers squares would count that are cut off
+// there; above 1e37 the mean and eps may pass the 32-bit range together.
 int check_eps(float eps) {
-  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(MOE_EINVAL, "eps must be positive and finite");
+  if (!(eps >= 0x1p-126f) || !(eps <= 1e37f)) return fail(MOE_EINVAL, "eps outside 2^-126..1e37");
   return MOE_OK;
 }
 
