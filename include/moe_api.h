@@ -446,8 +446,10 @@ enum { MOE_MM16_GATED = 1 /* b holds 2n rows: rows 0..n-1 the gate, then up */ }
  *   z[r][j] = sum over k of a[r][k] b[j][k] + bias[j]
  *   h = act(z), with MOE_MM16_GATED  h[r][j] = act(z[r][j]) * z[r][n + j]
  *   out[r][j] = row_scale[r] * h[r][j] + residual[r][j]
- * in fp32 (the tensor cores' sums cut off what lies below 2^-23 of them) up to
- * the one rounding to out's type.
+ * in fp32 up to the one rounding to out's type.  The tensor cores' sums cut off
+ * what lies below 2^-23 of them at every step of 16 of k; 4096 of k (of bf16
+ * outputs 32768) at most are summed so, and longer sums added up from these in
+ * fp32: terms of one sign lose 2^-15 (2^-12) of the sum at most, whatever k.
  *   a    bf16 [t] rows of k, lda apart;  b bf16 [n] (gated [2n]) rows of k,
  *        ldb apart; both and their rows start on 16 bytes (lda, ldb % 8 == 0),
  *        k itself may be odd

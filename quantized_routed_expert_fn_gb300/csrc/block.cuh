@@ -81,7 +81,8 @@ struct Mm16Args {
   // tensor cores: N side of a tile, k blocks, M and N tiles, CTAs that split
   // k, ring, columns of tensor memory
   int w, nk, nmt, ntt, split, stage, stages, tmem_cols;
-  int two;  // k in two halves, each with an accumulator
+  int two;    // k in two halves, each with an accumulator
+  int chunk;  // k blocks of one sum of the tensor cores at most
 };
 struct Mm16P : Mm16Args {
   CUtensorMap tm_a, tm_b, tm_r;

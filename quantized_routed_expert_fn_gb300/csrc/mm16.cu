@@ -122,6 +122,13 @@ __device__ __forceinline__ void finish4(const Mm16Args &P, int64_t r, int j, con
 // ------------------------------------------------------------ few rows
 
 constexpr int kFewWarps = 8;
+// The tensor cores cut off what lies below 2^-23 of a sum at every step of 16
+// of k, towards zero.  The k blocks of 64 that are summed so at most; longer
+// sums are added up from these in 32 bits, rounded to nearest.  Terms of one
+// sign then lose 2^-15 of the sum at most whatever k (measured: 1.0e-5; of
+// 65536 in two sums 1.7e-4, of 2^20 in one 0.55 %), of bf16 outputs, whose
+// rounding is 2^-8, 2^-12.
+constexpr int kSumBlocks = 64, kSumBlocksBf16 = 512;
 
 // A tile: 16 weight rows (gated: 8 gate rows and the 8 up rows of the same
 // outputs) by 8 * NT token rows.  Lane (g, q) = (lane / 4, lane % 4) loads 16
@@ -131,7 +138,8 @@ constexpr int kFewWarps = 8;
 // sides.  Warp w takes the blocks w, w + 8, ...; the warps' sums meet in
 // shared memory in a fixed order.  A CTA walks the tiles i, i + grid, ...,
 // the next D blocks' weights always on their way, across the tiles' ends.
-template <int NT, int D>
+// LONG: a warp's sums go to shared memory every kSumBlocks blocks.
+template <int NT, int D, bool LONG>
 __global__ void __launch_bounds__(32 * kFewWarps) mm16_few_rows(const __grid_constant__ Mm16Args P) {
   __shared__ float red[2][kFewWarps][16][8 * NT + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
@@ -184,6 +192,17 @@ __global__ void __launch_bounds__(32 * kFewWarps) mm16_few_rows(const __grid_con
     for (int j = 0; j < NT; j++)
 #pragma unroll
       for (int i = 0; i < 4; i++) acc[j][i] = 0.f;
+    // onto what lies at this lane's places
+    auto add_up = [&](bool first) {
+#pragma unroll
+      for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          float &to = red[buf][warp][g + 8 * (i >> 1)][8 * j + 2 * q + (i & 1)];
+          to = first ? acc[j][i] : to + acc[j][i];
+          acc[j][i] = 0.f;
+        }
+    };
     for (int i0 = 0; i0 < rounds; i0 += D) {
 #pragma unroll
       for (int d = 0; d < D; d++) {
@@ -198,12 +217,17 @@ __global__ void __launch_bounds__(32 * kFewWarps) mm16_few_rows(const __grid_con
         }
         load(a[d], b[d]);
       }
+      if (LONG && (i0 + D) % kSumBlocks == 0) add_up(i0 + D == kSumBlocks);
     }
+    if constexpr (LONG) {
+      add_up(rounds < kSumBlocks);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const int c = 8 * j + 2 * q;
-      red[buf][warp][g][c] = acc[j][0], red[buf][warp][g][c + 1] = acc[j][1];
-      red[buf][warp][g + 8][c] = acc[j][2], red[buf][warp][g + 8][c + 1] = acc[j][3];
+      for (int j = 0; j < NT; j++) {
+        const int c = 8 * j + 2 * q;
+        red[buf][warp][g][c] = acc[j][0], red[buf][warp][g][c + 1] = acc[j][1];
+        red[buf][warp][g + 8][c] = acc[j][2], red[buf][warp][g + 8][c + 1] = acc[j][3];
+      }
     }
     __syncthreads();  // the other buffer is read: every thread is past the tile before
     auto sum = [&](int row, int c) {
@@ -419,7 +443,12 @@ struct Outputs {
 
 enum { kWeights = 0, kSplit = 1, kTokens = 2 };  // what is on the M side; kSplit: weights, k split over a cluster
 
-template <int CG, int FORM>
+// LONG: a tile's k is summed P.chunk blocks at a time in the first half of tensor
+// memory, and added up in the second.  A kernel of its own, as its loops cost
+// the others 1 to 4 %.  One accumulator at a time: tiles of 160 columns, of
+// which two and the sum so far fit, took 501 us instead of 340 at 2048 x 2048 x
+// 65536, fp32.
+template <int CG, int FORM, bool LONG>
 __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__ Mm16P P) {
   constexpr bool CL = CG == 2, SPLIT = FORM == kSplit, TOK = FORM == kTokens;
   static_assert(!SPLIT || CG == 1, "a split tile is one CTA's rows");
@@ -463,6 +492,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
   const int my_tiles = cl < ntiles ? (ntiles - 1 - cl) / ncl + 1 : 0;
   int kb0 = 0, kb1 = P.nk;
   if constexpr (SPLIT) kb0 = (int)((int64_t)P.nk * rank / P.split), kb1 = (int)((int64_t)P.nk * (rank + 1) / P.split);
+  const int parts = LONG ? (kb1 - kb0 + P.chunk - 1) / P.chunk : 1;  // sums of a tile
+  const bool single = LONG || P.two;  // one accumulator, the other half of tensor memory taken
   // tile i: the M tiles of an N tile follow one another
   int tt = cl / nmp, mp = cl - tt * nmp;
   const int step_t = ncl / nmp, step_m = ncl - step_t * nmp;
@@ -487,29 +518,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
       bool ok = true;
       const uint32_t base = smem_u32(ring), idesc = tc05::idesc_f16(128 * CG, w);
       for (int lt = 0; lt < my_tiles && ok; lt++) {
-        const int b = P.two ? 0 : lt & 1, use = P.two ? lt : lt >> 1;
-        if (!tc_wait<CL>(&B.acc_empty[b], (uint32_t)((use & 1) ^ 1), P)) break;
-        tc05::fence_after();
-        uint32_t d = tmem + (uint32_t)(b * 256);
-        int start = kb0;
-        for (int kb = kb0; kb < kb1; kb++) {
-          if (P.two && kb == P.nk / 2) d += 256, start = kb;
-          if (!tc_wait<CL>(&B.full[s], ph, P)) {
+        for (int p = 0; p < parts && ok; p++) {
+          const int b = single ? 0 : lt & 1, use = single ? lt * parts + p : lt >> 1;
+          if (!tc_wait<CL>(&B.acc_empty[b], (uint32_t)((use & 1) ^ 1), P)) {
             ok = false;
             break;
           }
           tc05::fence_after();
-          const uint32_t st = base + (uint32_t)(s * P.stage);
-          const uint64_t ad = tc05::sdesc(st), bd = tc05::sdesc(st + 16384);
+          uint32_t d = tmem + (uint32_t)(b * 256);
+          int start = LONG ? kb0 + p * P.chunk : kb0;
+          const int end = LONG ? min(kb1, start + P.chunk) : kb1;
+          for (int kb = start; kb < end; kb++) {
+            if (!LONG && P.two && kb == P.nk / 2) d += 256, start = kb;
+            if (!tc_wait<CL>(&B.full[s], ph, P)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after();
+            const uint32_t st = base + (uint32_t)(s * P.stage);
+            const uint64_t ad = tc05::sdesc(st), bd = tc05::sdesc(st + 16384);
 #pragma unroll
-          for (int j = 0; j < 4; j++) tc05::mma_f16<CG>(d, ad + 2 * j, bd + 2 * j, idesc, kb != start || j != 0);
-          if constexpr (CG == 1) tc05::commit(&B.empty[s]);
-          else tc05::commit_pair(&B.empty[s]);
-          if (++s == S) s = 0, ph ^= 1;
-        }
-        if (ok) {
-          if constexpr (CG == 1) tc05::commit(&B.acc_full[b]);
-          else tc05::commit_pair(&B.acc_full[b]);
+            for (int j = 0; j < 4; j++) tc05::mma_f16<CG>(d, ad + 2 * j, bd + 2 * j, idesc, kb != start || j != 0);
+            if constexpr (CG == 1) tc05::commit(&B.empty[s]);
+            else tc05::commit_pair(&B.empty[s]);
+            if (++s == S) s = 0, ph ^= 1;
+          }
+          if (ok) {
+            if constexpr (CG == 1) tc05::commit(&B.acc_full[b]);
+            else tc05::commit_pair(&B.acc_full[b]);
+          }
         }
       }
       // every MMA issued here has completed before TMEM is released
@@ -598,27 +635,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
     int res_at = 0;  // pieces of residuals before the tile
     for (int lt = 0; lt < my_tiles; lt++) {
       const Tile T = next_tile();
-      const int b = P.two ? 0 : lt & 1, use = P.two ? lt : lt >> 1, nbase = T.mt * rows;
-      const bool rows4 = P.wide && nbase + rows <= P.n;
-      Outputs<FORM == kWeights ? 4 : 2> O;  // the first piece's residuals, and later the next one's
-      if (FORM == kWeights && T.mt < P.nmt && 16 * grp < T.nlen) O.fetch(P, T.n0 + 16 * grp, min(16, T.nlen - 16 * grp), nbase, q, 4, rows4);
-      // the warps stop together (they share named barriers)
-      // (one waits for the MMAs, the others for it)
-      fine = tc05::named_and(5, 32 * kEpi, res_ok && (warp != 0 || tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)(use & 1), P)));
-      if (!fine) break;
-      tc05::fence_after();
-      const uint32_t tl = tmem + (uint32_t)(b * 256) + ((uint32_t)(32 * q) << 16);
-      auto read = [&](int at, float (&x)[16]) {  // 16 columns of the tile's sums
-        tc05::ld16(tl + at, x);
-        if (P.two) {
+      const int b = single ? 0 : lt & 1, nbase = T.mt * rows;
+      auto sums = [&](uint32_t at, bool both, float (&x)[16]) {  // 16 columns
+        tc05::ld16(at, x);
+        if (both) {
           float y[16];
-          tc05::ld16(tl + 256 + at, y);
+          tc05::ld16(at + 256, y);
 #pragma unroll
           for (int j = 0; j < 16; j++) x[j] += y[j];
         }
       };
-      const int o = nbase + (P.gated ? row & 63 : row);
-      const int brow = P.gated && row >= 64 ? P.n + o : o;
       auto release = [&] {  // the accumulator is read: the MMAs may fill it again
         tc05::fence_before();
         __syncwarp();
@@ -627,6 +653,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
           else tc05::mbar_arrive_cluster(tc05::map_rank(&B.acc_empty[b], 0));
         }
       };
+      // (the warps stop together, as they share named barriers: one waits for
+      // the MMAs, the others for it)
+      if constexpr (LONG) {
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+        for (int p = 0; p < parts - 1; p++) {
+          fine = tc05::named_and(5, 32 * kEpi, res_ok && (warp != 0 || tc_warp_wait<CL>(&B.acc_full[0], (uint32_t)((lt * parts + p) & 1), P)));
+          if (!fine) break;
+          tc05::fence_after();
+#pragma unroll 1
+          for (int c0 = 16 * grp; c0 < w; c0 += 4 * kEpi) {
+            float v[16];
+            sums(tl + c0, p > 0, v);
+            tc05::st16(tl + 256 + c0, v);
+          }
+          tc05::wait_st();
+          release();
+        }
+        if (!fine) break;
+      }
+      const int use = single ? lt * parts + parts - 1 : lt >> 1;
+      const bool rows4 = P.wide && nbase + rows <= P.n;
+      Outputs<FORM == kWeights ? 4 : 2> O;  // the first piece's residuals, and later the next one's
+      if (FORM == kWeights && T.mt < P.nmt && 16 * grp < T.nlen) O.fetch(P, T.n0 + 16 * grp, min(16, T.nlen - 16 * grp), nbase, q, 4, rows4);
+      fine = tc05::named_and(5, 32 * kEpi, res_ok && (warp != 0 || tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)(use & 1), P)));
+      if (!fine) break;
+      tc05::fence_after();
+      const uint32_t tl = tmem + (uint32_t)(b * 256) + ((uint32_t)(32 * q) << 16);
+      auto read = [&](int at, float (&x)[16]) { sums(tl + at, LONG ? parts > 1 : !SPLIT && P.two, x); };
+      const int o = nbase + (P.gated ? row & 63 : row);
+      const int brow = P.gated && row >= 64 ? P.n + o : o;
       if constexpr (TOK) {
         // a lane has a token, and its columns one after another: no exchange
         // (through shared memory, which copies and MMAs keep busy, the
@@ -716,7 +772,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
         float *z = reinterpret_cast<float *>(ring);
         for (int c0 = 16 * grp; c0 < w; c0 += 4 * kEpi) {
           float v[16];
-          tc05::ld16(tl + c0, v);
+          read(c0, v);
 #pragma unroll
           for (int j = 0; j < 16; j++) z[(c0 + j) * 128 + row] = v[j];
         }
@@ -819,8 +875,8 @@ bool make_map16(CUtensorMap *m, const void *base, uint64_t k, uint64_t rows, uin
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int FORM>
-cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
+template <int CG, int FORM, bool LONG>
+cudaError_t launch_form(Mm16P &p, int n_sms, cudaStream_t st) {
   constexpr bool SPLIT = FORM == kSplit;
   const int nrows = p.w / CG;  // rows of the N side that a CTA loads
   p.stage = 16384 + nrows * 128;
@@ -831,12 +887,12 @@ cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
     // begin beside it: its k blocks (or the sums, [w][128]), its accumulator
     const int need = (p.nk + p.split - 1) / p.split, sums = (p.w * 512 + p.stage - 1) / p.stage;
     p.stages = min(p.stages, need > sums ? need : sums);
-    p.tmem_cols = p.w <= 32 ? 32 : (p.w <= 64 ? 64 : 128);
+    p.tmem_cols = LONG ? 512 : (p.w <= 32 ? 32 : (p.w <= 64 ? 64 : 128));
   }
   // the most any launch asks for: another host thread's launch of the same
   // kernel may stand between this and the launch below.  Before the tensor
   // maps: it makes the device's context this thread's, which they need
-  cudaError_t e = cudaFuncSetAttribute(mm16_tc<CG, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOffRing + kRoom + 1024);
+  cudaError_t e = cudaFuncSetAttribute(mm16_tc<CG, FORM, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOffRing + kRoom + 1024);
   if (e != cudaSuccess) return e;
   const int box_a = FORM == kTokens ? 128 : nrows, box_b = FORM == kTokens ? (p.gated ? p.w / 2 : nrows) : (p.gated ? 64 : 128);
   if (encode_fn() == nullptr || !make_map16(&p.tm_b, p.b, p.k, (uint64_t)p.n * (p.gated ? 2 : 1), p.ldb, (uint32_t)box_b) ||
@@ -865,7 +921,12 @@ cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = (unsigned)n;
-  return cudaLaunchKernelEx(&cfg, mm16_tc<CG, FORM>, p);
+  return cudaLaunchKernelEx(&cfg, mm16_tc<CG, FORM, LONG>, p);
+}
+template <int CG, int FORM>
+cudaError_t launch_tc(Mm16P &p, int n_sms, cudaStream_t st) {
+  const bool several = !p.two && (p.nk + p.split - 1) / p.split > p.chunk;
+  return several ? launch_form<CG, FORM, true>(p, n_sms, st) : launch_form<CG, FORM, false>(p, n_sms, st);
 }
 
 }  // namespace
@@ -877,7 +938,8 @@ cudaError_t launch_few(const Mm16Args &p, int n_sms, cudaStream_t st) {
   // most; two (three) thread blocks an SM fit
   const int most = n_sms * (blocks > 2 ? 2 : 3);
   const dim3 grid((unsigned)(tiles < most ? tiles : most));
-  auto f = blocks > 2 ? mm16_few_rows<NT, 4> : (blocks > 1 ? mm16_few_rows<NT, 2> : mm16_few_rows<NT, 1>);
+  auto f = blocks > kSumBlocks ? mm16_few_rows<NT, 4, true> : (blocks > 2 ? mm16_few_rows<NT, 4, false> :
+           (blocks > 1 ? mm16_few_rows<NT, 2, false> : mm16_few_rows<NT, 1, false>));
   return launch_pdl(f, grid, 32 * kFewWarps, 0, st, p);
 }
 
@@ -893,6 +955,7 @@ cudaError_t launch_mm16_few(const Mm16Args &p, int n_sms, cudaStream_t st) {
 cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st) {
   const int rows = p.gated ? 64 : 128;
   p.nmt = (p.n + rows - 1) / rows, p.nk = (p.k + 63) / 64;
+  p.chunk = p.out_bf16 ? kSumBlocksBf16 : kSumBlocks;
   // Too few tiles for the SMs: k is split over a cluster.  Clusters of 4 and 8
   // CTAs of this size do not fill every SM (36 and 15 fit at once).  Then as
   // narrow tiles as still fit: less to add up and to write for each CTA (128 x
@@ -911,10 +974,9 @@ cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st) {
       return launch_tc<1, kSplit>(p, n_sms, st);
     }
   }
-  // fp32 results of long sums: the two halves of k in an accumulator each, as
-  // the tensor cores cut off what lies below 2^-23 of a sum at every step
-  // (1024 x 1024 x 8192: 1.1e-6 of the result in one sum)
-  p.two = !p.out_bf16 && p.k > 4096;
+  // fp32 results up to twice as long: the two halves of k in an accumulator each
+  p.split = 1;
+  p.two = !p.out_bf16 && p.k > 64 * p.chunk && p.nk <= 2 * p.chunk;
   // The tile width with the least (rounds of tiles) x (width + what a tile
   // costs whatever its width), with the weights or the tokens on the M side.
   int64_t best = INT64_MAX;
