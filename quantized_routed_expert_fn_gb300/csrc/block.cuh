@@ -79,8 +79,8 @@ struct Mm16Args {
   int *status;
   unsigned long long timeout_ns;
   // tensor cores: N side of a tile, k blocks, M and N tiles, CTAs that split
-  // k, ring, columns of tensor memory
-  int w, nk, nmt, ntt, split, stage, stages, tmem_cols;
+  // k, ring
+  int w, nk, nmt, ntt, split, stage, stages;
   int two;    // k in two halves, each with an accumulator
   int chunk;  // k blocks of one sum of the tensor cores at most
 };

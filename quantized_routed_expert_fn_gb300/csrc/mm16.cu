@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
     fence_mbar_init();
   }
   if (warp == kEpi) {
-    if constexpr (CG == 1) tc05::alloc(&B.tmem, P.tmem_cols);
+    if constexpr (CG == 1) tc05::alloc(&B.tmem, 512);
     else tc05::alloc_pair(&B.tmem, 512);
   }
   pdl_wait_prev();  // the operands may be the previous kernel's
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
   if constexpr (CG == 1 && !SPLIT) __syncthreads();
   else tc05::cluster_sync();
   if (warp == kEpi) {
-    if constexpr (CG == 1) tc05::dealloc(tmem, P.tmem_cols);
+    if constexpr (CG == 1) tc05::dealloc(tmem, 512);
     else tc05::dealloc_pair(tmem, 512);
   }
 }
@@ -881,14 +881,7 @@ cudaError_t launch_form(Mm16P &p, int n_sms, cudaStream_t st) {
   const int nrows = p.w / CG;  // rows of the N side that a CTA loads
   p.stage = 16384 + nrows * 128;
   p.stages = kRoom / p.stage < kMaxStages ? kRoom / p.stage : kMaxStages;
-  p.tmem_cols = 512;
-  if (SPLIT) {
-    // no more than the one tile needs, so that the next launch's blocks may
-    // begin beside it: its k blocks (or the sums, [w][128]), its accumulator
-    const int need = (p.nk + p.split - 1) / p.split, sums = (p.w * 512 + p.stage - 1) / p.stage;
-    p.stages = min(p.stages, need > sums ? need : sums);
-    p.tmem_cols = LONG ? 512 : (p.w <= 32 ? 32 : (p.w <= 64 ? 64 : 128));
-  }
+  // (a split tile's sums, [w][128] with w up to 128, lie in two of the stages)
   // the most any launch asks for: another host thread's launch of the same
   // kernel may stand between this and the launch below.  Before the tensor
   // maps: it makes the device's context this thread's, which they need
