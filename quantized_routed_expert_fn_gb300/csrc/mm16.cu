@@ -443,6 +443,27 @@ struct Outputs {
 
 enum { kWeights = 0, kSplit = 1, kTokens = 2 };  // what is on the M side; kSplit: weights, k split over a cluster
 
+// 16 columns of an accumulator, with what lies in the other half of tensor memory
+__device__ __forceinline__ void read_sums(uint32_t at, bool both, float (&x)[16]) {
+  tc05::ld16(at, x);
+  if (both) {
+    float y[16];
+    tc05::ld16(at + 256, y);
+#pragma unroll
+    for (int j = 0; j < 16; j++) x[j] += y[j];
+  }
+}
+// Warp: an accumulator is read, and the MMAs may fill it again.
+template <int CG>
+__device__ __forceinline__ void release_acc(uint64_t *bar) {
+  tc05::fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    if constexpr (CG == 1) tc05::mbar_arrive(bar);
+    else tc05::mbar_arrive_cluster(tc05::map_rank(bar, 0));
+  }
+}
+
 // LONG: a tile's k is summed P.chunk blocks at a time in the first half of tensor
 // memory, and added up in the second.  A kernel of its own, as its loops cost
 // the others 1 to 4 %.  One accumulator at a time: tiles of 160 columns, of
@@ -493,7 +514,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
   int kb0 = 0, kb1 = P.nk;
   if constexpr (SPLIT) kb0 = (int)((int64_t)P.nk * rank / P.split), kb1 = (int)((int64_t)P.nk * (rank + 1) / P.split);
   const int parts = LONG ? (kb1 - kb0 + P.chunk - 1) / P.chunk : 1;  // sums of a tile
-  const bool single = LONG || P.two;  // one accumulator, the other half of tensor memory taken
+  // whether there is one accumulator, the other half of tensor memory taken (read
+  // again each time: a flag kept costs registers that the epilogue spills)
+  auto single = [&] { return LONG || P.two; };
   // tile i: the M tiles of an N tile follow one another
   int tt = cl / nmp, mp = cl - tt * nmp;
   const int step_t = ncl / nmp, step_m = ncl - step_t * nmp;
@@ -519,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
       const uint32_t base = smem_u32(ring), idesc = tc05::idesc_f16(128 * CG, w);
       for (int lt = 0; lt < my_tiles && ok; lt++) {
         for (int p = 0; p < parts && ok; p++) {
-          const int b = single ? 0 : lt & 1, use = single ? lt * parts + p : lt >> 1;
+          const int b = single() ? 0 : lt & 1, use = single() ? lt * parts + p : lt >> 1;
           if (!tc_wait<CL>(&B.acc_empty[b], (uint32_t)((use & 1) ^ 1), P)) {
             ok = false;
             break;
@@ -635,26 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
     int res_at = 0;  // pieces of residuals before the tile
     for (int lt = 0; lt < my_tiles; lt++) {
       const Tile T = next_tile();
-      const int b = single ? 0 : lt & 1, nbase = T.mt * rows;
-      auto sums = [&](uint32_t at, bool both, float (&x)[16]) {  // 16 columns
-        tc05::ld16(at, x);
-        if (both) {
-          float y[16];
-          tc05::ld16(at + 256, y);
-#pragma unroll
-          for (int j = 0; j < 16; j++) x[j] += y[j];
-        }
-      };
-      auto release = [&] {  // the accumulator is read: the MMAs may fill it again
-        tc05::fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 1) tc05::mbar_arrive(&B.acc_empty[b]);
-          else tc05::mbar_arrive_cluster(tc05::map_rank(&B.acc_empty[b], 0));
-        }
-      };
-      // (the warps stop together, as they share named barriers: one waits for
-      // the MMAs, the others for it)
+      const int b = single() ? 0 : lt & 1, use = single() ? lt * parts + parts - 1 : lt >> 1, nbase = T.mt * rows;
       if constexpr (LONG) {
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
         for (int p = 0; p < parts - 1; p++) {
@@ -664,25 +668,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
 #pragma unroll 1
           for (int c0 = 16 * grp; c0 < w; c0 += 4 * kEpi) {
             float v[16];
-            sums(tl + c0, p > 0, v);
+            read_sums(tl + c0, p > 0, v);
             tc05::st16(tl + 256 + c0, v);
           }
           tc05::wait_st();
-          release();
+          release_acc<CG>(&B.acc_empty[0]);
         }
         if (!fine) break;
       }
-      const int use = single ? lt * parts + parts - 1 : lt >> 1;
       const bool rows4 = P.wide && nbase + rows <= P.n;
       Outputs<FORM == kWeights ? 4 : 2> O;  // the first piece's residuals, and later the next one's
       if (FORM == kWeights && T.mt < P.nmt && 16 * grp < T.nlen) O.fetch(P, T.n0 + 16 * grp, min(16, T.nlen - 16 * grp), nbase, q, 4, rows4);
+      // the warps stop together (they share named barriers)
+      // (one waits for the MMAs, the others for it)
       fine = tc05::named_and(5, 32 * kEpi, res_ok && (warp != 0 || tc_warp_wait<CL>(&B.acc_full[b], (uint32_t)(use & 1), P)));
       if (!fine) break;
       tc05::fence_after();
       const uint32_t tl = tmem + (uint32_t)(b * 256) + ((uint32_t)(32 * q) << 16);
-      auto read = [&](int at, float (&x)[16]) { sums(tl + at, LONG ? parts > 1 : !SPLIT && P.two, x); };
+      auto read = [&](int at, float (&x)[16]) { read_sums(tl + at, LONG ? parts > 1 : !SPLIT && P.two, x); };
       const int o = nbase + (P.gated ? row & 63 : row);
       const int brow = P.gated && row >= 64 ? P.n + o : o;
+      auto release = [&] { release_acc<CG>(&B.acc_empty[b]); };
       if constexpr (TOK) {
         // a lane has a token, and its columns one after another: no exchange
         // (through shared memory, which copies and MMAs keep busy, the
