@@ -104,6 +104,13 @@ cudaError_t launch_mm16_tc(Mm16P p, int n_sms, cudaStream_t st);
 
 #ifdef __CUDACC__
 
+// two values to bf16 (nearest, ties to even), lo in the lower half
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // 1 / (1 + exp(-x)) of a number, small values to their last bits.  exp(-|x|)
 // is 2^t, t = -|x| log2(e) carried in two terms, so that its relative error
 // does not grow with |x|; the quotient's by an approximate reciprocal of 1 ..

@@ -12,8 +12,8 @@
 // those, and only threads whose own does have such values: those threads'
 // values are looked at again, by the whole block, and the ones that reach it
 // go through lists in shared memory that are cut to their largest 32.  (With
-// candidates collected in the one pass, 4096 rows of 131072 with top 5 took 272
-// us instead of 182.)
+// candidates collected in the one pass, 4096 rows of 131072 with top 5 took half
+// as long again.)
 //
 // A row is a cluster of S blocks (few rows) or one block; the blocks' sums
 // and lists meet in the first one's shared memory.  The bound is HBM, beside

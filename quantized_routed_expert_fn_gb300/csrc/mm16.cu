@@ -3,15 +3,18 @@
 //   out = row_scale[r] * h + residual
 //
 // Two kernels:
-//   few   up to 32 rows, by mm16_few: the weights are streamed once from HBM
+//   few   up to 16 rows, by mm16_few: the weights are streamed once from HBM
 //         straight into the fragments of mma.sync, a CTA takes 16 weight rows
 //         and splits k over its warps.
 //   tc    any number of rows: tcgen05 (kind::f16, fp32 accumulators in TMEM)
-//         fed by TMA.  Weights on the M side, tokens on the N side, as the
-//         8-bit products have them: M stays full whatever the number of rows.
-//         Persistent over CTA pairs (256 weight rows x up to 256 tokens), or,
-//         where there are too few tiles for the SMs, a cluster of S CTAs a
-//         tile that split k and add their accumulators in a fixed order.
+//         fed by TMA, in three forms.  Weights on the M side, tokens on the N
+//         side, as the 8-bit products have them: M stays full whatever the
+//         number of rows.  The same where there are too few tiles for the SMs,
+//         a cluster of S CTAs a tile that split k and add their accumulators
+//         in a fixed order.  Tokens on the M side: a lane has a token's
+//         outputs one after another, and nothing is exchanged for them.  The
+//         first and the last are persistent, over CTA pairs (256 x up to 256)
+//         where the M side has two tiles.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -19,6 +22,7 @@
 #include "block.cuh"
 #include "fp8.cuh"
 #include "tc05.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -76,11 +80,6 @@ __device__ __forceinline__ uint16_t bf16_of(float v) {
   uint16_t h;
   asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
   return h;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // One output: row r, column j, from h = the activated product.
@@ -854,22 +853,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm16_tc(const __grid_constant__
     if constexpr (CG == 1) tc05::dealloc(tmem, 512);
     else tc05::dealloc_pair(tmem, 512);
   }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return (EncodeTiledFn) nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
 }
 
 // rows of k values (bf16 or fp32), ld apart: boxes of 128 bytes x box_rows, 128B swizzle, zeros outside

@@ -22,6 +22,7 @@
 
 #include "fp8.cuh"
 #include "tc05.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -597,23 +598,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) mm8_tc(const __grid_constant__ 
     tc05::cluster_sync();
     if (warp == 8) tc05::dealloc_pair(tmem, 512);
   }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return (EncodeTiledFn) nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
 }
 
 // bytes [rows] x cols, rows ld apart, 128B swizzle, zeros outside: boxes of

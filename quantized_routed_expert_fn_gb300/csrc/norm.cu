@@ -57,13 +57,6 @@ __device__ __forceinline__ void load_as(const void *p, int64_t i, float *v) {
   }
 }
 
-// two values to bf16 (nearest, ties to even), lo in the lower half
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int V, bool BF16>
 __device__ __forceinline__ void store_as(void *p, int64_t i, const float *v) {
   if constexpr (BF16) {
@@ -560,7 +553,7 @@ int registers(F f) {
   return cudaFuncGetAttributes(&a, f) == cudaSuccess && a.numRegs > 0 ? (a.numRegs + 7) / 8 * 8 : 128;
 }
 
-// Bytes of shared memory of a walking launch, and whether it may be.
+// Bytes of shared memory that rows on their way take.
 int ring_bytes(const NormP &p, int nv, int block) {
   return kRing * block * (ring_row(nv, p.y_bf16) + (p.res ? ring_row(nv, p.res_bf16) : 0));
 }

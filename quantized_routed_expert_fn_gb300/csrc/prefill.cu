@@ -27,6 +27,7 @@
 #include "codec.cuh"
 #include "prefill.cuh"
 #include "tc05.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -1214,23 +1215,6 @@ void pf_carve(PfParams &p, void *work) {
 }
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return (EncodeTiledFn) nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
 
 // bf16 [rows][cols] row-major, box (64 columns = 128 bytes) x box_rows, 128B swizzle
 // (a k-panel buffer is [cols / 64 * entries][64])
