@@ -478,9 +478,9 @@ int moe_mm16(const uint16_t *a, int64_t lda, int t, const uint16_t *b, int64_t l
  *   tokens  [t][m] int32, logp [t][m] float32; NULL when m is 0 (m up to 1024)
  *   entropy [t] float32, or NULL
  *   top_idx [t][top_k] uint32, top_logp [t][top_k] float32; NULL when top_k is 0 (up to min(32, v))
- * t 0..2^27, v 1..2^24.  ln p carries an absolute error of some 2^-23 beside
- * its relative one (the sum over the row is held to 32 bits).  Needs no
- * workspace; has no device-side failures. */
+ * t 0..2^27, v 1..2^24.  ln p and the entropy carry an absolute error of
+ * some 2^-21 beside their relative one (the sums over the row are held to 32
+ * bits).  Needs no workspace; has no device-side failures. */
 int moe_logprobs(const void *logits, int logit_dtype, int64_t ld, int t, int v, float scale, const int32_t *tokens, int m,
                  float *logp, float *entropy, uint32_t *top_idx, float *top_logp, int top_k, moe_stream_t stream);
 

@@ -10,7 +10,7 @@
 // pieces then begin on 16 bytes in the row, see SH); 2 or 1 otherwise, so that
 // neighbouring lanes always touch neighbouring bytes.  Sums are 32-bit, in a
 // fixed tree.  65536 x 2048 bf16: 84 us, 6.4 TB/s; fp32 32768 x 2048: 79, 6.8;
-// 32816 x 4090 bf16 114 (with pieces of 2: 160).  add_norm, 30000 x 4096, all
+// 32816 x 4090 bf16 107 (with pieces of 2: 160).  add_norm, 30000 x 4096, all
 // bf16, a gate a channel: 157 us, 6.3 TB/s; 30011 x 4090 195.  Arithmetic goes two
 // values an instruction (one by one 2 to 4 % longer).
 #include <cuda_runtime.h>
@@ -183,7 +183,7 @@ struct Place {
   int T, l, h, lead, xc;  // xc: its column, < 0: none
   __device__ __forceinline__ Place(const NormP &P, int64_t row, int thread) {
     // (either is right; each where it costs fewer registers: 30011 x 4090 195 us
-    // against 229, to e4m3 65536 x 2048 93 against 98)
+    // against 229, to e4m3 65536 x 2048 94 against 98)
     T = P.T, l = (SH ? T >= (int)blockDim.x : T > 32) ? thread : thread & (T - 1);
     h = row < P.t ? P.h : 0, lead = SH ? (int)(-((row & 7) * P.ld8) & 7) : 0, xc = -1;
     if (SH && l < 8 && l < lead) xc = l;
