@@ -125,7 +125,7 @@ constexpr int kFewWarps = 8;
 // of k, towards zero.  The k blocks of 64 that are summed so at most; longer
 // sums are added up from these in 32 bits, rounded to nearest.  Terms of one
 // sign then lose 2^-15 of the sum at most whatever k (measured: 1.0e-5; of
-// 65536 in two sums 1.7e-4, of 2^20 in one 0.55 %), of bf16 outputs, whose
+// 65536 in two sums 1.7e-4, of 2^19 in one 0.28 %), of bf16 outputs, whose
 // rounding is 2^-8, 2^-12.
 constexpr int kSumBlocks = 64, kSumBlocksBf16 = 512;
 
